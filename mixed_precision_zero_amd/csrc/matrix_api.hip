@@ -157,7 +157,8 @@ extern "C" int neox_orthogonalize(const neox_ns_config* cfg, const void* src, in
     for (uint64_t z = 0; z < count; z += most) {
         const uint64_t n = std::min(most, count - z);
         const OrthIO io{(const uint8_t*)src + z * src_stride * sb, (uint8_t*)dst + z * dst_stride * db,
-                        src_ld, src_stride, dst_ld, dst_stride, src_dtype, dst_dtype, (float)scale, cfg->eps};
+                        src_ld, src_stride, dst_ld, dst_stride, src_dtype, dst_dtype, (float)scale,
+                        d0 % (4 * db) == 0 && dst_ld % 4 == 0 && (count == 1 || dst_stride % 4 == 0), cfg->eps};
         const hipError_t e = enqueue_orth(s, w, (uint32_t)n, io, coef, cfg->steps,
                                           static_cast<hipStream_t>(hip_stream));
         if (e != hipSuccess) return set_hip_error(e, "orthogonalize launch");

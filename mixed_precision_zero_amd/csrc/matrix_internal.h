@@ -30,7 +30,6 @@ struct NsShape {
     uint32_t rows, cols;   // of the source
     uint32_t m, n;         // of the wide form
     uint32_t mp, np;       // padded
-    uint32_t tile;         // side of a block's output tile
     uint32_t parts;        // partial sums per matrix
     bool tall;             // the wide form is the source's transpose
     float s;               // S, a power of two: the iterate is stored times S
@@ -47,6 +46,7 @@ struct OrthIO {
     uint64_t src_ld, src_stride, dst_ld, dst_stride;
     int32_t src_dtype, dst_dtype;
     float scale;
+    bool vec;              // dst can be written four elements at a time
     double eps;
 };
 struct MuonMat {           // device table entry

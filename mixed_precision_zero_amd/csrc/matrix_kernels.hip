@@ -33,16 +33,6 @@ __host__ __device__ inline const DevState* state_of(const OrthIO&) { return null
 __host__ __device__ inline const DevState* state_of(const MuonIO& io) { return io.st; }
 __device__ __forceinline__ bool skipped(const DevState* st) { return st && st->skip; }
 
-// The destination of the iterate between steps: none.
-struct NoIO {
-    const DevState* st;
-};
-__host__ __device__ inline const DevState* state_of(const NoIO& io) { return io.st; }
-struct NoDst {
-    __device__ NoDst(const NoIO&, uint32_t, float) {}
-    __device__ void store(uint32_t, uint32_t, uint32_t, float) const {}
-};
-
 template <int NT>
 __device__ __forceinline__ double sum_block(double v) {
 #pragma unroll
@@ -157,7 +147,21 @@ __global__ __launch_bounds__(256) void ns_convert_kernel(IO io, NsShape s, NsBuf
 // ------------------------------------------------------------------------------------
 // the products
 // ------------------------------------------------------------------------------------
-// tile (ti, tj), tj <= ti, of number t in row order of the lower triangle
+// Which tile a block works on.  Blocks [0, nfull) take whole 256 x 256 tiles; the others take
+// quarters (128 x 128) of what is left: the tiles that would start another, mostly empty round
+// on the chip's 256 CUs, and those that the matrix's edge cuts.  Tiles of a symmetric product
+// lie on and below the diagonal, those on it last (a quarter of them above it is left out).
+struct TileMap {
+    uint32_t nfull;        // blocks with whole tiles
+    uint32_t inner;        // whole tiles per matrix
+    uint32_t edges;        // cut tiles per matrix
+    uint32_t count;        // matrices
+    uint32_t pi, qi;       // whole tiles down and across
+    uint32_t q;            // tiles across, a cut one counted
+    uint32_t mp, np;       // sides
+};
+
+// (i, j), j <= i, number t in row order of a lower triangle
 __device__ __forceinline__ void lower(uint32_t t, uint32_t& ti, uint32_t& tj) {
     uint32_t i = (uint32_t)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
     while (i * (i + 1) / 2 > t) --i;
@@ -166,208 +170,452 @@ __device__ __forceinline__ void lower(uint32_t t, uint32_t& ti, uint32_t& tj) {
     tj = t - i * (i + 1) / 2;
 }
 
-template <class Core>
+struct TileAt {
+    uint32_t z, i, j;      // matrix, first row and column
+    bool full, none;
+};
+
+template <bool SYM>
+__device__ __forceinline__ TileAt place(const TileMap& m) {
+    TileAt r{};
+    uint32_t k, quarter = 0;
+    r.full = blockIdx.x < m.nfull;
+    if (r.full) {
+        // consecutive blocks go to the eight XCDs in turn: give each XCD, and so each L2, one
+        // run of neighbouring tiles
+        const uint32_t per = m.nfull / 8;
+        k = m.nfull % 8 ? blockIdx.x : blockIdx.x % 8 * per + blockIdx.x / 8;
+    } else {
+        k = m.nfull + (blockIdx.x - m.nfull) / 4;
+        quarter = (blockIdx.x - m.nfull) % 4;
+    }
+    const uint32_t total = m.inner * m.count;
+    uint32_t ti, tj;
+    if (k < total) {
+        r.z = k / m.inner;
+        k -= r.z * m.inner;
+        if (SYM) {
+            const uint32_t below = m.pi * (m.pi - 1) / 2;
+            if (k < below) {
+                lower(k, ti, tj);
+                ++ti;
+            } else {
+                ti = tj = k - below;
+            }
+        } else {
+            // runs of eight tile rows, column by column: 64 tiles in a row share 8 + 8 panels
+            const uint32_t g = k / (8 * m.qi), rows = min(8u, m.pi - 8 * g), in = k - g * 8 * m.qi;
+            ti = 8 * g + in % rows;
+            tj = in / rows;
+        }
+    } else {
+        k -= total;
+        r.z = k / m.edges;
+        k -= r.z * m.edges;
+        if (SYM) {
+            ti = m.pi;
+            tj = k;
+        } else {
+            const uint32_t right = m.q > m.qi ? m.pi : 0;
+            ti = k < right ? k : m.pi;
+            tj = k < right ? m.qi : k - right;
+        }
+    }
+    r.i = ti * 256 + (quarter >> 1) * 128;
+    r.j = tj * 256 + (quarter & 1) * 128;
+    r.none = r.i >= m.mp || r.j >= m.np || (SYM && !r.full && r.j > r.i);
+    return r;
+}
+
+// The same for launches of one tile size only, one block per tile.
+template <class Core, bool SYM>
+__device__ __forceinline__ TileAt place_even(uint32_t mp, uint32_t np) {
+    const uint32_t p = mp / Core::BP, q = np / Core::BQ, tiles = SYM ? p * (p + 1) / 2 : p * q;
+    TileAt r{};
+    r.z = blockIdx.x / tiles;
+    const uint32_t t = blockIdx.x % tiles;
+    uint32_t ti, tj;
+    if (SYM) {
+        lower(t, ti, tj);
+    } else {
+        ti = t / q;
+        tj = t % q;
+    }
+    r.i = ti * Core::BP;
+    r.j = tj * Core::BQ;
+    return r;
+}
+
 __device__ __forceinline__ TileRows rows_of(const uint16_t* base, uint64_t row, uint32_t len, int block) {
     return TileRows{(const uint8_t*)(base + row * len), nullptr, (uint32_t)block, len * 2u, 0u};
 }
 
-template <class Core>
-__global__ __launch_bounds__(Core::NT) void ns_gram_kernel(const DevState* st, NsShape s, NsBuf w, float inv_s2) {
-    if (skipped(st)) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * Core::kStage];
-    const uint32_t side = s.mp / Core::BP, tiles = side * (side + 1) / 2;
-    const uint32_t z = blockIdx.x / tiles;
-    uint32_t ti, tj;
-    lower(blockIdx.x % tiles, ti, tj);
-    const uint16_t* x = w.xh + (uint64_t)z * s.mp * s.np;
-    Core t;
-    t.run(rows_of<Core>(x, (uint64_t)ti * Core::BP, s.np, Core::BP),
-          rows_of<Core>(x, (uint64_t)tj * Core::BQ, s.np, Core::BQ), s.np * 2, lds);
-    uint16_t* a = w.a + (uint64_t)z * s.mp * s.mp;
-    float* da = w.da + (uint64_t)z * s.mp;
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+// A lane of a 16 x 16 result tile holds four consecutive rows of one column.  These are the
+// elements of the same tile that are four consecutive columns of one row (row lane % 16,
+// columns 4 (lane / 16) + 0..3): the four FP16 values, taken as the left operand of a product
+// with the identity, come out transposed and exact.
+__device__ __forceinline__ tf32x4 transposed(f16x4 v) {
     const uint32_t lane = threadIdx.x & 63;
-    const uint32_t ib = ti * Core::BP + Core::wave_p() + (lane >> 4) * 4;
-    const uint32_t jb = tj * Core::BQ + Core::wave_q() + (lane & 15);
+    f16x4 one;
 #pragma unroll
-    for (int u = 0; u < Core::TP; ++u)
+    for (int e = 0; e < 4; ++e) one[e] = (lane >> 4) * 4 + e == (lane & 15) ? (_Float16)1.0f : (_Float16)0.0f;
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(v, one, tf32x4{0, 0, 0, 0}, 0, 0, 0);
+}
+__device__ __forceinline__ f16x4 pack4(tf32x4 v) {
+    return f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+}
+__device__ __forceinline__ f16x4 load4(const uint16_t* p) { return *(const f16x4*)p; }
+__device__ __forceinline__ void store4(uint16_t* p, f16x4 v) { *(f16x4*)p = v; }
+
+// Where this lane's elements of result tile (u, v) are: rows i .. i + 3 of column j; and
+// transposed, row ti, columns tj .. tj + 3.
+template <class Core>
+struct Lane {
+    uint32_t i, j, ti, tj;
+    __device__ Lane(const TileAt& t, int u, int v) {
+        const uint32_t lane = threadIdx.x & 63;
+        const uint32_t r = t.i + Core::wave_p() + 16 * u, c = t.j + Core::wave_q() + 16 * v;
+        i = r + (lane >> 4) * 4;
+        j = c + (lane & 15);
+        ti = r + (lane & 15);
+        tj = c + (lane >> 4) * 4;
+    }
+};
+
+// An FP16 result on and below the diagonal, to both sides of it, without the diagonal; the
+// diagonal to d.
+template <class Core>
+__device__ __forceinline__ void store_sym(const TileAt& t, const Lane<Core>& l, tf32x4 x, uint16_t* out,
+                                          uint32_t ld, float* d) {
+    if (t.i == t.j) {
 #pragma unroll
-        for (int v = 0; v < Core::TQ; ++v) {
-            const uint32_t j = jb + 16 * v;
-            uint16_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t i = ib + 16 * u + e;
-                const float x = t.acc[u][v][e] * inv_s2;
-                if (i == j) da[i] = x;
-                h[e] = i == j ? (uint16_t)0 : to_f16(x);
-                a[(uint64_t)i * s.mp + j] = h[e];
+        for (int e = 0; e < 4; ++e)
+            if (l.i + e == l.j) {
+                d[l.j] = x[e];
+                x[e] = 0.0f;
             }
-            if (ti != tj)
-                *(ushort4*)(a + (uint64_t)j * s.mp + ib + 16 * u) = make_ushort4(h[0], h[1], h[2], h[3]);
-        }
+    }
+    const f16x4 h = pack4(x);
+    if (t.i != t.j) store4(out + (uint64_t)l.j * ld + l.i, h);
+    store4(out + (uint64_t)l.ti * ld + l.tj, pack4(transposed(h)));
 }
 
-template <class Core>
-__global__ __launch_bounds__(Core::NT) void ns_poly_kernel(const DevState* st, NsShape s, NsBuf w, NsCoef k) {
-    if (skipped(st)) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * Core::kStage];
-    const uint32_t side = s.mp / Core::BP, tiles = side * (side + 1) / 2;
-    const uint32_t z = blockIdx.x / tiles;
-    uint32_t ti, tj;
-    lower(blockIdx.x % tiles, ti, tj);
-    const uint16_t* a = w.a + (uint64_t)z * s.mp * s.mp;
-    Core t;
-    t.run(rows_of<Core>(a, (uint64_t)ti * Core::BP, s.mp, Core::BP),
-          rows_of<Core>(a, (uint64_t)tj * Core::BQ, s.mp, Core::BQ), s.mp * 2, lds);
-    uint16_t* b = w.b + (uint64_t)z * s.mp * s.mp;
-    const float* da = w.da + (uint64_t)z * s.mp;
-    float* db = w.db + (uint64_t)z * s.mp;
-    const uint32_t lane = threadIdx.x & 63;
-    const uint32_t ib = ti * Core::BP + Core::wave_p() + (lane >> 4) * 4;
-    const uint32_t jb = tj * Core::BQ + Core::wave_q() + (lane & 15);
+// A = X X^T
+struct Gram {
+    static constexpr bool SYM = true;
+    NsBuf w;
+    uint32_t mp, np;
+    float inv_s2;
+    template <class Core>
+    __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
+        const uint16_t* x = w.xh + (uint64_t)at.z * mp * np;
+        Core t;
+        t.run(rows_of(x, at.i, np, Core::BP), rows_of(x, at.j, np, Core::BQ), np * 2, lds);
+        uint16_t* a = w.a + (uint64_t)at.z * mp * mp;
+        float* da = w.da + (uint64_t)at.z * mp;
 #pragma unroll
-    for (int u = 0; u < Core::TP; ++u)
+        for (int u = 0; u < Core::TP; ++u)
 #pragma unroll
-        for (int v = 0; v < Core::TQ; ++v) {
-            const uint32_t j = jb + 16 * v;
-            // A = O + D: A A = O O + (D_i + D_j) O_ij + D_i^2 on the diagonal (O is 0 there)
-            const ushort4 o4 = *(const ushort4*)(a + (uint64_t)j * s.mp + ib + 16 * u);
-            const uint16_t o[4] = {o4.x, o4.y, o4.z, o4.w};
-            uint16_t h[4];
+            for (int v = 0; v < Core::TQ; ++v)
+                store_sym<Core>(at, Lane<Core>(at, u, v), t.acc[u][v] * inv_s2, a, mp, da);
+    }
+};
+
+// B = b A + c A A.  A = O + D: A A = O O + (D_i + D_j) O_ij, and D_i^2 on the diagonal, where
+// O is 0.
+struct Poly {
+    static constexpr bool SYM = true;
+    NsBuf w;
+    uint32_t mp, np;
+    float kb, kc;
+    template <class Core>
+    __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
+        const uint16_t* a = w.a + (uint64_t)at.z * mp * mp;
+        const float* da = w.da + (uint64_t)at.z * mp;
+        Core t;
+        t.run(rows_of(a, at.i, mp, Core::BP), rows_of(a, at.j, mp, Core::BQ), mp * 2, lds);
+        uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
+        float* db = w.db + (uint64_t)at.z * mp;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t i = ib + 16 * u + e;
-                const float di = da[i], off = f16(o[e]);
-                float sq = __builtin_fmaf(di + da[j], off, t.acc[u][v][e]);
-                float lin = off;
-                if (i == j) {
-                    sq = __builtin_fmaf(di, di, sq);
-                    lin = di;
+        for (int u = 0; u < Core::TP; ++u)
+#pragma unroll
+            for (int v = 0; v < Core::TQ; ++v) {
+                const Lane<Core> l(at, u, v);
+                const f16x4 o = load4(a + (uint64_t)l.j * mp + l.i);
+                const tf32x4 di = *(const tf32x4*)(da + l.i);
+                const float dj = da[l.j];
+                tf32x4 x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool diag = l.i + e == l.j;
+                    const float off = (float)o[e];
+                    float sq = __builtin_fmaf(di[e] + dj, off, t.acc[u][v][e]);
+                    if (diag) sq = __builtin_fmaf(dj, dj, sq);
+                    x[e] = __builtin_fmaf(kc, sq, kb * (diag ? dj : off));
                 }
-                const float x = __builtin_fmaf(k.c, sq, k.b * lin);
-                if (i == j) db[i] = x;
-                h[e] = i == j ? (uint16_t)0 : to_f16(x);
-                b[(uint64_t)i * s.mp + j] = h[e];
+                store_sym<Core>(at, l, x, b, mp, db);
             }
-            if (ti != tj)
-                *(ushort4*)(b + (uint64_t)j * s.mp + ib + 16 * u) = make_ushort4(h[0], h[1], h[2], h[3]);
-        }
-}
+    }
+};
 
-// What the last step's result becomes.
+// X <- a X + B X, to the buffers of the next step
+struct Apply {
+    static constexpr bool SYM = false;
+    NsBuf w;
+    uint32_t mp, np;
+    float ka;
+    int from;
+    template <class Core>
+    __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
+        const uint64_t xz = (uint64_t)at.z * mp * np;
+        const uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
+        const uint16_t* xt = w.xt[from] + xz;
+        Core t;
+        t.run(rows_of(b, at.i, mp, Core::BP), rows_of(xt, at.j, mp, Core::BQ), mp * 2, lds);
+        const float* db = w.db + (uint64_t)at.z * mp;
+        uint16_t* lt = w.lt + xz;
+        uint16_t* xo = w.xt[from ^ 1] + xz;
+        uint16_t* xh = w.xh + xz;
+#pragma unroll
+        for (int u = 0; u < Core::TP; ++u)
+#pragma unroll
+            for (int v = 0; v < Core::TQ; ++v) {
+                const Lane<Core> l(at, u, v);
+                const uint64_t p = (uint64_t)l.j * mp + l.i;
+                const f16x4 h = load4(xt + p), o = load4(lt + p);
+                const tf32x4 d = *(const tf32x4*)(db + l.i);
+                tf32x4 y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[e] = __builtin_fmaf(ka + d[e], __builtin_fmaf((float)o[e], 1.0f / kLo, (float)h[e]),
+                                          t.acc[u][v][e]);
+                const f16x4 nh = pack4(y);
+                f16x4 nl;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) nl[e] = (_Float16)((y[e] - (float)nh[e]) * kLo);
+                store4(xo + p, nh);
+                store4(lt + p, nl);
+                store4(xh + (uint64_t)l.ti * np + l.tj, pack4(transposed(nh)));
+            }
+    }
+};
+
+// What the last step's result becomes: four consecutive elements of a row at (r, c), the first
+// `n` of them inside the matrix.
 struct OrthDst {
     const OrthIO& io;
     uint64_t at;
     float f;
-    __device__ OrthDst(const OrthIO& i, uint32_t z, float inv_s)
-        : io(i), at(z * i.dst_stride), f(i.scale * inv_s) {}
-    __device__ void store(uint32_t r, uint32_t c, uint32_t, float x) const {
-        store_elem(io.dst, io.dst_dtype, at + r * io.dst_ld + c, x * f);
+    bool vec;
+    __device__ OrthDst(const OrthIO& i, const NsShape&, uint32_t z, float inv_s)
+        : io(i), at(z * i.dst_stride), f(i.scale * inv_s), vec(i.vec) {}
+    __device__ __forceinline__ void store(uint32_t r, uint32_t c, uint32_t n, tf32x4 x) const {
+        const uint64_t p = at + r * io.dst_ld + c;
+        if (vec && n == 4) {
+            x = x * f;
+            if (io.dst_dtype == NEOX_F32) *(tf32x4*)((float*)io.dst + p) = x;
+            else *(ushort4*)((uint16_t*)io.dst + p) =
+                     make_ushort4(float_to_half(io.dst_dtype, x[0]), float_to_half(io.dst_dtype, x[1]),
+                                  float_to_half(io.dst_dtype, x[2]), float_to_half(io.dst_dtype, x[3]));
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+                if (e < n) store_elem(io.dst, io.dst_dtype, p + e, x[e] * f);
+        }
     }
 };
 struct MuonDst {
     const MuonIO& io;
     MuonMat mat;
+    uint32_t cols;
     float f, wd;
-    __device__ MuonDst(const MuonIO& i, uint32_t z, float inv_s)
-        : io(i), mat(i.mats[z]), f(i.scale * inv_s), wd(mat.decay ? i.wd : 0.0f) {}
-    __device__ void store(uint32_t r, uint32_t c, uint32_t cols, float x) const {
-        const uint64_t i = (uint64_t)r * cols + c;
-        const float w = mat.master[i];
-        const float n = opaque(__builtin_fmaf(-io.lr, __builtin_fmaf(wd, w, x * f), w));
-        mat.master[i] = n;
-        mat.half[i] = float_to_half(io.dtype, n);
+    bool vec;
+    __device__ MuonDst(const MuonIO& i, const NsShape& s, uint32_t z, float inv_s)
+        : io(i), mat(i.mats[z]), cols(s.cols), f(i.scale * inv_s), wd(mat.decay ? i.wd : 0.0f),
+          vec(mat.vec && s.cols % 4 == 0) {}
+    __device__ __forceinline__ float step(float w, float x) const {
+        return opaque(__builtin_fmaf(-io.lr, __builtin_fmaf(wd, w, x * f), w));
+    }
+    __device__ __forceinline__ void store(uint32_t r, uint32_t c, uint32_t n, tf32x4 x) const {
+        const uint64_t p = (uint64_t)r * cols + c;
+        if (vec && n == 4) {
+            tf32x4 w = *(const tf32x4*)(mat.master + p);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = step(w[e], x[e]);
+            *(tf32x4*)(mat.master + p) = w;
+            *(ushort4*)(mat.half + p) = make_ushort4(float_to_half(io.dtype, w[0]), float_to_half(io.dtype, w[1]),
+                                                     float_to_half(io.dtype, w[2]), float_to_half(io.dtype, w[3]));
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+                if (e < n) {
+                    const float w = step(mat.master[p + e], x[e]);
+                    mat.master[p + e] = w;
+                    mat.half[p + e] = float_to_half(io.dtype, w);
+                }
+        }
     }
 };
 
-// LAST: the result goes to Dst instead of the buffers.
-template <class Core, class IO, class Dst, bool LAST>
-__global__ __launch_bounds__(Core::NT) void ns_apply_kernel(IO io, NsShape s, NsBuf w, float ka,
-                                                            int from, float inv_s) {
-    if (skipped(state_of(io))) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * Core::kStage];
-    const uint32_t np_t = s.np / Core::BQ, tiles = s.mp / Core::BP * np_t;
-    const uint32_t z = blockIdx.x / tiles, tt = blockIdx.x % tiles;
-    const uint32_t ti = tt / np_t, tj = tt % np_t;
-    const uint64_t xz = (uint64_t)z * s.mp * s.np;
-    const uint16_t* b = w.b + (uint64_t)z * s.mp * s.mp;
-    const uint16_t* xt = w.xt[from] + xz;
-    Core t;
-    t.run(rows_of<Core>(b, (uint64_t)ti * Core::BP, s.mp, Core::BP),
-          rows_of<Core>(xt, (uint64_t)tj * Core::BQ, s.mp, Core::BQ), s.mp * 2, lds);
-    const float* db = w.db + (uint64_t)z * s.mp;
-    uint16_t* lt = w.lt + xz;
-    uint16_t* xo = w.xt[from ^ 1] + xz;
-    uint16_t* xh = w.xh + xz;
-    const Dst dst(io, z, inv_s);
-    const uint32_t lane = threadIdx.x & 63;
-    const uint32_t ib = ti * Core::BP + Core::wave_p() + (lane >> 4) * 4;
-    const uint32_t jb = tj * Core::BQ + Core::wave_q() + (lane & 15);
+// The last step.  The operands are exchanged where the source is not transposed, so that a
+// lane's four elements always are neighbours in a row of the source: there D's rows are j and
+// its columns i, the iterate's first half comes from xh and its second, transposed, from lt.
+template <class IO, class Dst, bool TALL>
+struct Last {
+    static constexpr bool SYM = false;
+    IO io;
+    NsBuf w;
+    NsShape s;
+    float ka, inv_s;
+    int from;
+    template <class Core>
+    __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
+        const uint32_t mp = s.mp, np = s.np;
+        const uint64_t xz = (uint64_t)at.z * mp * np;
+        const uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
+        const uint16_t* xt = w.xt[from] + xz;
+        const uint16_t* xh = w.xh + xz;
+        const uint16_t* lt = w.lt + xz;
+        const float* db = w.db + (uint64_t)at.z * mp;
+        const TileRows br = rows_of(b, TALL ? at.i : at.j, mp, TALL ? Core::BP : Core::BQ);
+        const TileRows xr = rows_of(xt, TALL ? at.j : at.i, mp, TALL ? Core::BQ : Core::BP);
+        Core t;
+        t.run(TALL ? br : xr, TALL ? xr : br, mp * 2, lds);
+        const Dst dst(io, s, at.z, inv_s);
 #pragma unroll
-    for (int u = 0; u < Core::TP; ++u)
+        for (int u = 0; u < Core::TP; ++u)
 #pragma unroll
-        for (int v = 0; v < Core::TQ; ++v) {
-            const uint32_t j = jb + 16 * v, i = ib + 16 * u;
-            const uint64_t at = (uint64_t)j * s.mp + i;
-            const ushort4 h4 = *(const ushort4*)(xt + at), l4 = *(const ushort4*)(lt + at);
-            const uint16_t h[4] = {h4.x, h4.y, h4.z, h4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
-            uint16_t nh[4], nl[4];
+            for (int v = 0; v < Core::TQ; ++v) {
+                const Lane<Core> l(at, u, v);
+                tf32x4 y;
+                if constexpr (TALL) {
+                    // D rows are i: four i of one j
+                    const uint64_t p = (uint64_t)l.j * mp + l.i;
+                    const f16x4 h = load4(xt + p), o = load4(lt + p);
+                    const tf32x4 d = *(const tf32x4*)(db + l.i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = __builtin_fmaf(f16(l[e]), 1.0f / kLo, f16(h[e]));
-                const float y = __builtin_fmaf(ka + db[i + e], x, t.acc[u][v][e]);
-                if constexpr (LAST) {
-                    if (i + e < s.m && j < s.n) {
-                        if (s.tall) dst.store(j, i + e, s.cols, y);
-                        else dst.store(i + e, j, s.cols, y);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = __builtin_fmaf(ka + d[e], __builtin_fmaf((float)o[e], 1.0f / kLo, (float)h[e]),
+                                              t.acc[u][v][e]);
+                    if (l.j < s.n && l.i < s.m) dst.store(l.j, l.i, min(4u, s.m - l.i), y);
                 } else {
-                    nh[e] = to_f16(y);
-                    nl[e] = to_f16((y - f16(nh[e])) * kLo);
-                    xh[(uint64_t)(i + e) * s.np + j] = nh[e];
+                    // D rows are j (l.i), its columns i (l.j): four j of one i
+                    const f16x4 h = load4(xh + (uint64_t)l.j * np + l.i);
+                    const tf32x4 o = transposed(load4(lt + (uint64_t)l.ti * mp + l.tj));
+                    const float d = ka + db[l.j];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = __builtin_fmaf(d, __builtin_fmaf(o[e], 1.0f / kLo, (float)h[e]), t.acc[u][v][e]);
+                    if (l.j < s.m && l.i < s.n) dst.store(l.j, l.i, min(4u, s.n - l.i), y);
                 }
             }
-            if constexpr (!LAST) {
-                *(ushort4*)(xo + at) = make_ushort4(nh[0], nh[1], nh[2], nh[3]);
-                *(ushort4*)(lt + at) = make_ushort4(nl[0], nl[1], nl[2], nl[3]);
-            }
-        }
+    }
+};
+
+using Core256 = TileCore<256, 256, 2, 4, false>;
+using Core128w = TileCore<128, 128, 2, 4, false>;      // quarters, by the same 512 threads
+using Core128 = TileCore<128, 128, 2, 2, false>;
+using Core64 = TileCore<64, 64, 2, 2, false, 4>;
+
+template <class Op>
+__global__ __launch_bounds__(512, 2) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
+    if (skipped(st)) return;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Core256::kLds];
+    const TileAt at = place<Op::SYM>(m);
+    if (at.full) op.template tile<Core256>(at, lds);
+    else if (!at.none) op.template tile<Core128w>(at, lds);
+}
+template <class Op, class Core>
+__global__ __launch_bounds__(Core::NT) void ns_even_kernel(Op op, const DevState* st, uint32_t mp, uint32_t np) {
+    if (skipped(st)) return;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
+    op.template tile<Core>(place_even<Core, Op::SYM>(mp, np), lds);
 }
 
 // ------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------
-template <class Core, class IO, class Src, class Dst>
+constexpr uint32_t kCUs = 256;
+
+// One product over `count` matrices with mp x np results (mp = np for the symmetric ones).
+// The tile is chosen by what the launch would take per 128 bytes of K, from times measured on
+// the full chip (us per slab): a round of 256 x 256 tiles (one block per CU) 1.45; of quarters
+// in the same kernel 0.55; of 128 x 128 tiles 0.52 with one block per CU and 1.03 with two; of
+// 64 x 64 tiles 0.23 and 0.39.  Results do not depend on the choice: every element's products
+// are added in the same order.
+template <class Op>
+hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_t np, uint32_t count,
+                          hipStream_t stream) {
+    auto rounds = [](uint64_t n, double one, double two) {
+        return n <= kCUs ? one : two * (double)((n + 2 * kCUs - 1) / (2 * kCUs));
+    };
+    const uint64_t p64 = mp / 64, q64 = np / 64;
+    const uint64_t n64 = (Op::SYM ? p64 * (p64 + 1) / 2 : p64 * q64) * count;
+    const double c64 = rounds(n64, 0.23, 0.39);
+    if (mp % 128 || np % 128) {
+        ns_even_kernel<Op, Core64><<<(uint32_t)n64, Core64::NT, 0, stream>>>(op, st, mp, np);
+        return hipGetLastError();
+    }
+    const uint64_t p128 = mp / 128, q128 = np / 128;
+    const uint64_t n128 = (Op::SYM ? p128 * (p128 + 1) / 2 : p128 * q128) * count;
+    const double c128 = rounds(n128, 0.52, 1.03);
+    TileMap m{};
+    m.count = count;
+    m.pi = mp / 256;
+    m.qi = np / 256;
+    m.q = (np + 255) / 256;
+    m.mp = mp;
+    m.np = np;
+    const bool cut_p = mp % 256 != 0, cut_q = np % 256 != 0;
+    if (Op::SYM) {
+        m.inner = m.pi * (m.pi + 1) / 2;
+        m.edges = cut_p ? m.pi + 1 : 0;
+    } else {
+        m.inner = m.pi * m.qi;
+        m.edges = (cut_q ? m.pi : 0) + (cut_p ? m.q : 0);
+    }
+    const uint64_t total = (uint64_t)m.inner * count, cut = (uint64_t)m.edges * count;
+    auto cost = [&](uint64_t full) {
+        const uint64_t quarters = 4 * (total - full + cut);
+        return 1.45 * (double)((full + kCUs - 1) / kCUs) + 0.55 * (double)((quarters + kCUs - 1) / kCUs);
+    };
+    const uint64_t whole = total / kCUs * kCUs;
+    const uint64_t full = cost(total) <= cost(whole) ? total : whole;
+    const double c256 = cost(full);
+    if (c256 < c128 && c256 < c64) {
+        m.nfull = (uint32_t)full;
+        const uint64_t blocks = full + 4 * (total - full + cut);
+        ns_mixed_kernel<Op><<<(uint32_t)blocks, 512, 0, stream>>>(op, st, m);
+    } else if (c128 < c64) {
+        ns_even_kernel<Op, Core128><<<(uint32_t)n128, Core128::NT, 0, stream>>>(op, st, mp, np);
+    } else {
+        ns_even_kernel<Op, Core64><<<(uint32_t)n64, Core64::NT, 0, stream>>>(op, st, mp, np);
+    }
+    return hipGetLastError();
+}
+
+template <class IO, class Src, class Dst>
 hipError_t enqueue_steps(const NsShape& s, const NsBuf& w, uint32_t count, const IO& io,
                          const NsCoef* coef, int steps, hipStream_t stream) {
     const uint32_t conv = s.mp / 64 * (s.np / 64) * count;
     ns_convert_kernel<Src><<<conv, 256, 0, stream>>>(io, s, w);
     hipError_t e = hipGetLastError();
-    const uint32_t side = s.mp / Core::BP;
-    const uint32_t sym = side * (side + 1) / 2 * count, full = side * (s.np / Core::BQ) * count;
+    const DevState* st = state_of(io);
     const float inv_s2 = 1.0f / (s.s * s.s), inv_s = 1.0f / s.s;
     for (int k = 0; k < steps && e == hipSuccess; ++k) {
-        ns_gram_kernel<Core><<<sym, Core::NT, 0, stream>>>(state_of(io), s, w, inv_s2);
-        e = hipGetLastError();
-        if (e != hipSuccess) break;
-        ns_poly_kernel<Core><<<sym, Core::NT, 0, stream>>>(state_of(io), s, w, coef[k]);
-        e = hipGetLastError();
+        e = launch_product(Gram{w, s.mp, s.np, inv_s2}, st, s.mp, s.mp, count, stream);
+        if (e == hipSuccess) e = launch_product(Poly{w, s.mp, s.np, coef[k].b, coef[k].c}, st, s.mp, s.mp, count, stream);
         if (e != hipSuccess) break;
         if (k + 1 < steps)
-            ns_apply_kernel<Core, NoIO, NoDst, false><<<full, Core::NT, 0, stream>>>(NoIO{state_of(io)}, s, w, coef[k].a, k & 1, inv_s);
+            e = launch_product(Apply{w, s.mp, s.np, coef[k].a, k & 1}, st, s.mp, s.np, count, stream);
+        else if (s.tall)
+            e = launch_product(Last<IO, Dst, true>{io, w, s, coef[k].a, inv_s, k & 1}, st, s.mp, s.np, count, stream);
         else
-            ns_apply_kernel<Core, IO, Dst, true><<<full, Core::NT, 0, stream>>>(io, s, w, coef[k].a, k & 1, inv_s);
-        e = hipGetLastError();
+            e = launch_product(Last<IO, Dst, false>{io, w, s, coef[k].a, inv_s, k & 1}, st, s.np, s.mp, count, stream);
     }
     return e;
-}
-
-using Core128 = TileCore<128, 128, 2, 2, false>;
-
-template <class IO, class Src, class Dst>
-hipError_t enqueue_any(const NsShape& s, const NsBuf& w, uint32_t count, const IO& io,
-                       const NsCoef* coef, int steps, hipStream_t stream) {
-    return enqueue_steps<Core128, IO, Src, Dst>(s, w, count, io, coef, steps, stream);
 }
 
 }  // namespace
@@ -377,7 +625,7 @@ hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const 
     orth_norm_kernel<<<s.parts * count, 256, 0, stream>>>(io, s.rows, s.cols, s.parts, w.part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return enqueue_any<OrthIO, OrthSrc, OrthDst>(s, w, count, io, coef, steps, stream);
+    return enqueue_steps<OrthIO, OrthSrc, OrthDst>(s, w, count, io, coef, steps, stream);
 }
 
 hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const MuonIO& io,
@@ -385,7 +633,7 @@ hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const 
     muon_momentum_kernel<<<s.parts * count, 256, 0, stream>>>(io, (uint64_t)s.rows * s.cols, s.parts, w.part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return enqueue_any<MuonIO, MuonSrc, MuonDst>(s, w, count, io, coef, steps, stream);
+    return enqueue_steps<MuonIO, MuonSrc, MuonDst>(s, w, count, io, coef, steps, stream);
 }
 
 // ------------------------------------------------------------------------------------
@@ -398,9 +646,10 @@ NsShape ns_shape(uint64_t rows, uint64_t cols) {
     s.tall = rows > cols;
     s.m = s.tall ? s.cols : s.rows;
     s.n = s.tall ? s.rows : s.cols;
-    s.tile = 128;
-    s.mp = (s.m + s.tile - 1) / s.tile * s.tile;
-    s.np = (s.n + s.tile - 1) / s.tile * s.tile;
+    // whole 64 x 64 tiles where the small side has few of them, else whole 128 x 128 ones
+    const uint32_t t = s.m <= 512 ? 64 : 128;
+    s.mp = (s.m + t - 1) / t * t;
+    s.np = (s.n + t - 1) / t * t;
     // one partial sum for each 16K elements, at most one for each row
     const uint64_t want = (rows * cols + 16383) / 16384;
     s.parts = (uint32_t)(want < kNsParts ? want : kNsParts);

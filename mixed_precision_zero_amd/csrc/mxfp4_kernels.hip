@@ -101,7 +101,7 @@ __global__ __launch_bounds__(Core::NT) void product_kernel(const uint8_t* a_code
                                                            uint32_t m, const uint8_t* b_codes,
                                                            const uint8_t* b_scales, uint32_t n, MxShape sh,
                                                            void* c, int dtype, uint64_t ldc) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * Core::kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
     const uint32_t tn = (n + Core::BP - 1) / Core::BP;
     const uint32_t p0 = blockIdx.x % tn * Core::BP, q0 = blockIdx.x / tn * Core::BQ;
     const TileRows p{b_codes + (uint64_t)p0 * sh.code_pitch, b_scales + (uint64_t)p0 * sh.scale_pitch,

@@ -5,7 +5,7 @@
 // same bytes per lane: 16 bytes of row (lane % 16), lane group (lane / 16) of four covering
 // 64 bytes of K.  So everything up to the matrix instruction is one code over bytes: a slab
 // of 128 bytes of K (64 FP16 or 256 FP4 elements) per operand row goes from global memory
-// straight to LDS (global_load_lds, 16 bytes a lane), double buffered, and each wave reads
+// straight to LDS (buffer_load ... lds, 16 bytes a lane) and each wave reads
 // its rows back as 16-byte fragments.
 //
 // LDS layout: row r's eight 16-byte chunks sit at chunk position c ^ (r & 7), so that the
@@ -14,6 +14,8 @@
 // Which K elements meet in which instruction is free as long as both operands agree: the
 // lane group g takes chunks 2g and 2g + 1 of a slab, so its two MXFP4 scales are adjacent.
 #pragma once
+
+#include "neox_matrix.h"
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -27,30 +29,47 @@ typedef int32_t ti32x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kSlab = 128;       // bytes of K per row and stage
 
-// One operand of a block: `rows` valid rows from base, row r at r * pitch bytes.  Rows past
-// the last valid one read that one again (their results are not stored).
+// One operand of a block: `rows` rows of `pitch` bytes from base.  Rows past the last one read
+// as zeros (the loads carry the operand's length, and the hardware returns 0 behind it).
 struct TileRows {
     const uint8_t* base;
     const uint8_t* scales;            // MXFP4: row r's at r * spitch
     uint32_t rows, pitch, spitch;
 };
 
-static __device__ __attribute__((aligned(16))) const uint32_t g_zero_chunk[4] = {0, 0, 0, 0};
-
-__device__ __forceinline__ void load_lds16(const void* g, void* l) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                     (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+// A raw buffer of n bytes: offsets at or behind n read 0.  Flags: the 32-bit data format word
+// of gfx9's untyped buffers.
+__device__ __forceinline__ rsrc_t raw_buffer(const void* p, uint32_t n) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, n, 0x00027000);
 }
+constexpr uint32_t kNowhere = 0x80000000u;      // an offset behind every operand (at most 2^31 bytes)
 
-template <int BP_, int BQ_, int WP_, int WQ_, bool FP4_>
+// BP x BQ output tile by WP x WQ waves, FP16 or MXFP4, NS slabs of K in LDS.
+//
+// A slab is worked on in two halves (64 bytes of K each).  While the products of one half run,
+// the fragments of the next are read: after the products of tile row i, its P fragment is
+// overwritten by the next half's, and the Q fragments alternate between two sets.  The reads of
+// slab s + 1 need it to have landed, so the block's one barrier per slab sits in the second
+// half of slab s, behind the first row of products (which covers the latency of slab s's last
+// reads; behind the second or third row it measured 2-3% slower).  Behind it slab s's buffer is free, and the load of slab s + NS goes there.
+// Row by row the order is pinned: left to itself the compiler reads all fragments at once,
+// which needs 252 registers instead of 240 for FP16 and spills for MXFP4.
+template <int BP_, int BQ_, int WP_, int WQ_, bool FP4_, int NS_ = 2>
 struct TileCore {
-    static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_;
+    static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NS = NS_;
     static constexpr bool FP4 = FP4_;
     static constexpr int NT = WP * WQ * 64;
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;      // 16x16 tiles per wave
-    static constexpr int LP = BP * 8 / NT, LQ = BQ * 8 / NT;        // 16-byte loads per thread
+    static constexpr int LP = BP * 8 / NT, LQ = BQ * 8 / NT;        // 16-byte loads per thread and slab
     static constexpr int kStage = (BP + BQ) * kSlab;
+    // MXFP4: the scales of four slabs, 32 bytes a row, double buffered
+    static constexpr int kGroup = (BP + BQ) * 32;
+    static constexpr int SP = BP * 8 / NT, SQ = BQ * 8 / NT;        // 4-byte loads per thread and group
+    static constexpr int kLds = NS * kStage + (FP4 ? 2 * kGroup : 0);
     static_assert(LP >= 1 && LQ >= 1 && BP * 8 % NT == 0 && BQ * 8 % NT == 0, "whole loads");
+    static_assert(NS >= 2 && (!FP4 || NS == 2), "");
+    static_assert(kLds <= 160 * 1024, "LDS of a CU");
 
     // acc[i][j]: 16x16 tile (i, j) of this wave; element e of a lane is D row
     // 16 i + 4 (lane / 16) + e, column 16 j + lane % 16 of the wave's part.
@@ -59,114 +78,176 @@ struct TileCore {
     static __device__ __forceinline__ int wave_p() { return (int)(threadIdx.x >> 6) / WQ * (BP / WP); }
     static __device__ __forceinline__ int wave_q() { return (int)(threadIdx.x >> 6) % WQ * (BQ / WQ); }
 
-    template <int L>
-    static __device__ __forceinline__ void offsets(const TileRows& t, uint32_t (&off)[L]) {
-        const uint32_t tid = threadIdx.x;
-        const uint32_t c = (tid & 7) ^ ((tid >> 3) & 7);
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            uint32_t r = (tid >> 3) + i * (NT / 8);
-            r = r < t.rows ? r : t.rows - 1;
-            off[i] = r * t.pitch + c * 16;
-        }
-    }
-    template <int L>
-    static __device__ __forceinline__ void issue(const uint8_t* base, const uint32_t (&off)[L],
-                                                 uint8_t* lds, bool dead) {
-        uint8_t* w = lds + (threadIdx.x & ~63u) * 16;               // wave-uniform
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const uint8_t* g = base + off[i];
-            if (dead) g = (const uint8_t*)g_zero_chunk;
-            load_lds16(g, w + i * NT * 16);
-        }
-    }
     static __device__ __forceinline__ tu32x4 frag(const uint8_t* rows, int row, int chunk) {
         return *(const tu32x4*)(rows + row * kSlab + ((chunk ^ (row & 7)) << 4));
     }
+    // Waits until at most n of this wave's loads are under way and its LDS reads are done,
+    // then for everybody.  (A fence would wait for all loads.)
+    template <int n>
+    static __device__ __forceinline__ void wait_barrier() {
+        static_assert(n < 64, "vmcnt has six bits");
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 0x0070);   // vmcnt(n) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
 
-    // lds: 2 * kStage bytes.  kbytes: bytes of K, a multiple of 128 (FP16) or 64 (MXFP4).
+    // lds: kLds bytes.  kbytes: bytes of K, a multiple of 128 (FP16) or 64 (MXFP4).
     __device__ __forceinline__ void run(const TileRows& p, const TileRows& q, uint32_t kbytes,
                                         uint8_t* lds) {
-        const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-        uint32_t po[LP], qo[LQ];
-        offsets(p, po);
-        offsets(q, qo);
+        const uint32_t tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
         const uint32_t slabs = (kbytes + kSlab - 1) / kSlab;
+        const rsrc_t pb = raw_buffer(p.base, p.rows * p.pitch), qb = raw_buffer(q.base, q.rows * q.pitch);
+        // this thread's chunk of its first row; the others are NT / 8 rows further each
+        const uint32_t chunk = (tid & 7) ^ ((tid >> 3) & 7);
+        const uint32_t pv = (tid >> 3) * p.pitch + chunk * 16, qv = (tid >> 3) * q.pitch + chunk * 16;
+        const uint32_t pstep = NT / 8 * p.pitch, qstep = NT / 8 * q.pitch;
         // MXFP4: the last slab may be half a slab; its second half is read as zeros
-        const bool upper = ((threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7)) >= 4;
         const bool half_tail = FP4 && (kbytes & 64u);
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int rp = wave_p() + (int)l16, rq = wave_q() + (int)l16;
-        uint32_t sp[TP], sq[TQ], spn[TP], sqn[TQ];
-        auto scales = [&](uint32_t s) {
+        uint8_t* sl = lds + NS * kStage;
+
+        typedef __attribute__((address_space(3))) void* lptr;
+        // Load n (of LP + LQ) of slab s.  Slabs behind the last one are loaded from nowhere: the
+        // loop has no branches, and the number of loads under way at each wait is known.
+        auto stage = [&](int n, uint32_t s, uint8_t* buf) {
+            const bool live = s < slabs - (half_tail && chunk >= 4 ? 1 : 0);
+            if (n < LP)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(pb, (lptr)(buf + wave * 1024 + n * NT * 16), 16,
+                                                         live ? pv : kNowhere, s * kSlab + n * pstep, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    qb, (lptr)(buf + BP * kSlab + wave * 1024 + (n - LP) * NT * 16), 16, live ? qv : kNowhere,
+                    s * kSlab + (n - LP) * qstep, 0, 0);
+        };
+        // Quarter k of the scales of slabs 4u .. 4u + 3: a group is loaded over the four slabs
+        // before it, so that these loads need no branch either.
+        rsrc_t psb = pb, qsb = qb;
+        uint32_t psv = 0, qsv = 0;
+        // dword of a row's 32 bytes; rows 8 to 15 of 16 swap halves, to use the banks rows 0 to 7
+        // leave
+        const uint32_t sdw = (tid & 7) ^ (tid >> 4 & 4);
+        if constexpr (FP4) {
+            psb = raw_buffer(p.scales, p.rows * p.spitch);
+            qsb = raw_buffer(q.scales, q.rows * q.spitch);
+            psv = (tid >> 3) * p.spitch + sdw * 4;
+            qsv = (tid >> 3) * q.spitch + sdw * 4;
+        }
+        auto group = [&](uint32_t u, uint32_t k) {
             if constexpr (FP4) {
-                const uint32_t at = s * 8 + 2 * g;
-                const bool in = at < p.spitch;
+                static_assert(SP == SQ && SP % 2 == 0, "whole quarters");
+                const bool in = u * 32 + sdw * 4 < p.spitch;
+                const uint32_t v = in ? (k < 2 ? psv : qsv) : kNowhere;
+                const uint32_t step = NT / 8 * p.spitch;             // both operands have one K
+                uint8_t* w = sl + (u & 1) * kGroup + wave * 256;
 #pragma unroll
-                for (int i = 0; i < TP; ++i) {
-                    uint32_t r = (uint32_t)(rp + 16 * i);
-                    r = r < p.rows ? r : p.rows - 1;
-                    spn[i] = in ? *(const uint16_t*)(p.scales + (size_t)r * p.spitch + at) : 0x7F7Fu;
-                }
+                for (int i = 0; i < SP / 2; ++i)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(k < 2 ? psb : qsb,
+                                                             (lptr)(w + (k * (SP / 2) + i) * NT * 4), 4, v,
+                                                             u * 32 + ((k & 1) * (SP / 2) + i) * step, 0, 0);
+            }
+        };
+        tu32x4 fp[TP], fq[2][TQ];
+        uint32_t sp[TP], sq[2][TQ];                  // MXFP4: two scale bytes each
+        auto row = [&](int i, int h, int set) {
 #pragma unroll
-                for (int j = 0; j < TQ; ++j) {
-                    uint32_t r = (uint32_t)(rq + 16 * j);
-                    r = r < q.rows ? r : q.rows - 1;
-                    sqn[j] = in ? *(const uint16_t*)(q.scales + (size_t)r * q.spitch + at) : 0x7F7Fu;
+            for (int j = 0; j < TQ; ++j) {
+                if constexpr (FP4) {
+                    const ti32x8 x = {(int)fp[i].x, (int)fp[i].y, (int)fp[i].z, (int)fp[i].w, 0, 0, 0, 0};
+                    const tu32x4 f = fq[h][j];
+                    const ti32x8 y = {(int)f.x, (int)f.y, (int)f.z, (int)f.w, 0, 0, 0, 0};
+                    acc[i][j] = h == 0
+                        ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[i][j], 4, 4, 0, (int)sp[i],
+                                                                           0, (int)sq[set][j])
+                        : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[i][j], 4, 4, 1, (int)sp[i],
+                                                                           1, (int)sq[set][j]);
+                } else {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(tf16x8, fp[i]),
+                                                                       __builtin_bit_cast(tf16x8, fq[h][j]),
+                                                                       acc[i][j], 0, 0, 0);
                 }
             }
         };
-        auto stage = [&](uint32_t s, uint8_t* buf) {
-            const bool dead = half_tail && s == slabs - 1 && upper;
-            issue<LP>(p.base + (size_t)s * kSlab, po, buf, dead);
-            issue<LQ>(q.base + (size_t)s * kSlab, qo, buf + BP * kSlab, dead);
-            scales(s);
+        auto read_p = [&](int i, const uint8_t* c, int h) { fp[i] = frag(c, rp + 16 * i, 2 * (int)g + h); };
+        auto read_q = [&](int j, const uint8_t* c, int h) {
+            fq[h][j] = frag(c + BP * kSlab, rq + 16 * j, 2 * (int)g + h);
+        };
+        const uint32_t sswap = (l16 & 8) << 1;
+        auto scale_p = [&](int i, uint32_t s) {
+            if constexpr (FP4)
+                sp[i] = *(const uint16_t*)(sl + ((s >> 2) & 1) * kGroup + (rp + 16 * i) * 32 + (((s & 3) * 8 + 2 * g) ^ sswap));
+        };
+        auto scale_q = [&](int j, uint32_t s, int set) {
+            if constexpr (FP4)
+                sq[set][j] = *(const uint16_t*)(sl + ((s >> 2) & 1) * kGroup + (BP + rq + 16 * j) * 32 +
+                                                (((s & 3) * 8 + 2 * g) ^ sswap));
         };
 #pragma unroll
         for (int i = 0; i < TP; ++i)
 #pragma unroll
             for (int j = 0; j < TQ; ++j) acc[i][j] = tf32x4{0, 0, 0, 0};
-        stage(0, lds);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) group(0, k);
+        group(1, 0);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+#pragma unroll
+            for (int n = 0; n < LP + LQ; ++n) stage(n, k, lds + k * kStage);
+        }
+        wait_barrier<(NS - 1) * (LP + LQ)>();
+#pragma unroll
+        for (int i = 0; i < TP; ++i) {
+            read_p(i, lds, 0);
+            scale_p(i, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) {
+            read_q(j, lds, 0);
+            scale_q(j, 0, 0);
+        }
+        uint32_t at = 0;                             // buffer of slab s
         for (uint32_t s = 0; s < slabs; ++s) {
-            const uint8_t* cur = lds + (s & 1) * kStage;
+            uint8_t* cur = lds + at * kStage;
+            at = at + 1 == NS ? 0 : at + 1;
+            const uint8_t* nxt = lds + at * kStage;
+            // first half: products of (s, 0), reads of (s, 1)
+#pragma unroll
+            for (int i = 0; i < TP; ++i) {
+                row(i, 0, 0);
+                read_p(i, cur, 1);
+#pragma unroll
+                for (int j = i * TQ / TP; j < (i + 1) * TQ / TP; ++j) read_q(j, cur, 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // second half: products of (s, 1), reads of (s + 1, 0); behind the last slab these
+            // read a buffer that holds an older one, or nothing, and are not used
+#pragma unroll
+            for (int i = 0; i < TP; ++i) {
+                row(i, 1, 0);
+                if (i == 0) wait_barrier<(NS - 2) * (LP + LQ)>();
+                // the loads of slab s + NS, spread over the rows: issued at once they queue up and
+                // hold back the products behind them (6% slower)
+#pragma unroll
+                for (int t = i * (LP + LQ) / TP; t < (i + 1) * (LP + LQ) / TP; ++t) stage(t, s + NS, cur);
+                if (i == TP - 1) group(((s + 1) >> 2) + 1, (s + 1) & 3);
+                read_p(i, nxt, 0);
+                scale_p(i, s + 1);
+#pragma unroll
+                for (int j = i * TQ / TP; j < (i + 1) * TQ / TP; ++j) {
+                    read_q(j, nxt, 0);
+                    scale_q(j, s + 1, 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
             if constexpr (FP4) {
 #pragma unroll
-                for (int i = 0; i < TP; ++i) sp[i] = spn[i];
-#pragma unroll
-                for (int j = 0; j < TQ; ++j) sq[j] = sqn[j];
-            }
-            // this thread's loads have landed; after the barrier everybody's have, and
-            // everybody is done reading the other buffer
-            __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-            __syncthreads();
-            if (s + 1 < slabs) stage(s + 1, lds + ((s + 1) & 1) * kStage);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                tu32x4 fp[TP], fq[TQ];
-#pragma unroll
-                for (int i = 0; i < TP; ++i) fp[i] = frag(cur, rp + 16 * i, 2 * (int)g + h);
-#pragma unroll
-                for (int j = 0; j < TQ; ++j) fq[j] = frag(cur + BP * kSlab, rq + 16 * j, 2 * (int)g + h);
-#pragma unroll
-                for (int i = 0; i < TP; ++i)
-#pragma unroll
-                    for (int j = 0; j < TQ; ++j) {
-                        if constexpr (FP4) {
-                            const ti32x8 x = {(int)fp[i].x, (int)fp[i].y, (int)fp[i].z, (int)fp[i].w, 0, 0, 0, 0};
-                            const ti32x8 y = {(int)fq[j].x, (int)fq[j].y, (int)fq[j].z, (int)fq[j].w, 0, 0, 0, 0};
-                            acc[i][j] = h == 0
-                                ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                      x, y, acc[i][j], 4, 4, 0, (int)sp[i], 0, (int)sq[j])
-                                : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                      x, y, acc[i][j], 4, 4, 1, (int)sp[i], 1, (int)sq[j]);
-                        } else {
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                                __builtin_bit_cast(tf16x8, fp[i]), __builtin_bit_cast(tf16x8, fq[j]),
-                                acc[i][j], 0, 0, 0);
-                        }
-                    }
+                for (int j = 0; j < TQ; ++j) sq[0][j] = sq[1][j];
             }
         }
+        wait_barrier<0>();       // nothing writes to or reads from lds any more
     }
 };
 
