@@ -266,40 +266,100 @@ __device__ __forceinline__ tf32x4 transposed(f16x4 v) {
 __device__ __forceinline__ f16x4 pack4(tf32x4 v) {
     return f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
 }
-__device__ __forceinline__ f16x4 load4(const uint16_t* p) { return *(const f16x4*)p; }
-__device__ __forceinline__ void store4(uint16_t* p, f16x4 v) { *(f16x4*)p = v; }
 
-// Where this lane's elements of result tile (u, v) are: rows i .. i + 3 of column j; and
-// transposed, row ti, columns tj .. tj + 3.
-template <class Core>
-struct Lane {
-    uint32_t i, j, ti, tj;
-    __device__ Lane(const TileAt& t, int u, int v) {
-        const uint32_t lane = threadIdx.x & 63;
-        const uint32_t r = t.i + Core::wave_p() + 16 * u, c = t.j + Core::wave_q() + 16 * v;
-        i = r + (lane >> 4) * 4;
-        j = c + (lane & 15);
-        ti = r + (lane & 15);
-        tj = c + (lane >> 4) * 4;
+// ROWS x COLS FP16 elements of a row-major array in a wave's own part of LDS, on their way
+// between its result tiles and memory: a lane's four elements are 8 bytes of 16 different rows
+// an instruction, which memory serves at half the rate of whole rows, so rows of COLS elements
+// (64 or 128 bytes) are moved 16 bytes a lane instead.  The 16-byte chunks of a row are
+// permuted by its number so that 16 rows at one column fall on different banks.  Only the wave
+// that owns the part uses it, and its LDS operations execute in order: no barrier is needed.
+template <int ROWS, int COLS>
+struct Patch {
+    static constexpr int kRow = COLS * 2, kChunks = kRow / 16, kBytes = ROWS * kRow;
+    static constexpr int kPass = kBytes / 1024;          // 64 lanes of 16 bytes
+    static_assert((kRow == 64 || kRow == 128) && kBytes % 1024 == 0, "");
+    static __device__ __forceinline__ uint32_t turn(uint32_t row) { return (row >> (kRow == 128 ? 1 : 2)) & (kChunks - 1); }
+    // four elements at (row, col), col a multiple of 4
+    static __device__ __forceinline__ f16x4* at(uint8_t* l, uint32_t row, uint32_t col) {
+        return (f16x4*)(l + row * kRow + (((col >> 3) ^ turn(row)) << 4) + (col & 4) * 2);
     }
+    // starts loading from g (row r at r * ld); wave_wait() before it is used
+    static __device__ __forceinline__ void load(uint8_t* l, const uint16_t* g, uint32_t ld) {
+        const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+        for (int k = 0; k < kPass; ++k) {
+            const uint32_t row = (k * 64 + lane) / kChunks, c = (lane % kChunks) ^ turn(row);
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(g + (uint64_t)row * ld + c * 8),
+                (__attribute__((address_space(3))) void*)(l + k * 1024), 16, 0, 0);
+        }
+    }
+    static __device__ __forceinline__ void store(const uint8_t* l, uint16_t* g, uint32_t ld) {
+        const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+        for (int k = 0; k < kPass; ++k) {
+            const uint32_t row = (k * 64 + lane) / kChunks, c = (lane % kChunks) ^ turn(row);
+            *(tu32x4*)(g + (uint64_t)row * ld + c * 8) = *(const tu32x4*)(l + (k * 64 + lane) * 16);
+        }
+    }
+};
+// All of this wave's memory operations so far are done.
+__device__ __forceinline__ void wave_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);         // vmcnt(0) lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A wave's results of a block tile, worked on in pieces of 16 kU x 16 TQ elements.
+template <class Core>
+struct Piece {
+    static constexpr int kU = Core::TP < 4 ? Core::TP : 4, kV = Core::TQ;
+    using Down = Patch<16 * kV, 16 * kU>;       // rows are D's columns: an array [j][i]
+    using Across = Patch<16 * kU, 16 * kV>;     // rows are D's rows: [i][j]
+    static constexpr int kBytes = Down::kBytes;
+    static_assert(2 * kBytes <= Core::kLds / (Core::NT / 64), "two patches per wave");
+    uint32_t i, j;         // first row and column in the matrix
+    uint32_t li, lj;       // this lane's first row and its column within 16 x 16
+    uint8_t *l0, *l1;      // LDS of two patches
+    __device__ Piece(const TileAt& t, int u0, uint8_t* lds) {
+        const uint32_t lane = threadIdx.x & 63;
+        i = t.i + Core::wave_p() + 16 * u0;
+        j = t.j + Core::wave_q();
+        li = (lane >> 4) * 4;
+        lj = lane & 15;
+        l0 = lds + (threadIdx.x >> 6) * (Core::kLds / (Core::NT / 64));
+        l1 = l0 + kBytes;
+    }
+    // The places of tile (u, v)'s elements of this lane, and of their transposes, in a patch.
+    __device__ __forceinline__ f16x4* down(uint8_t* l, int u, int v) const { return Down::at(l, 16 * v + lj, 16 * u + li); }
+    __device__ __forceinline__ f16x4* across(uint8_t* l, int u, int v) const { return Across::at(l, 16 * u + lj, 16 * v + li); }
 };
 
 // An FP16 result on and below the diagonal, to both sides of it, without the diagonal; the
 // diagonal to d.
 template <class Core>
-__device__ __forceinline__ void store_sym(const TileAt& t, const Lane<Core>& l, tf32x4 x, uint16_t* out,
-                                          uint32_t ld, float* d) {
-    if (t.i == t.j) {
+__device__ __forceinline__ void store_sym(const TileAt& t, const Piece<Core>& p, tf32x4 (&x)[Piece<Core>::kU][Core::TQ],
+                                          uint16_t* out, uint32_t ld, float* d) {
+    using P = Piece<Core>;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (l.i + e == l.j) {
-                d[l.j] = x[e];
-                x[e] = 0.0f;
+    for (int u = 0; u < P::kU; ++u)
+#pragma unroll
+        for (int v = 0; v < P::kV; ++v) {
+            if (t.i == t.j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (p.i + 16 * u + p.li + e == p.j + 16 * v + p.lj) {
+                        d[p.j + 16 * v + p.lj] = x[u][v][e];
+                        x[u][v][e] = 0.0f;
+                    }
             }
-    }
-    const f16x4 h = pack4(x);
-    if (t.i != t.j) store4(out + (uint64_t)l.j * ld + l.i, h);
-    store4(out + (uint64_t)l.ti * ld + l.tj, pack4(transposed(h)));
+            const f16x4 h = pack4(x[u][v]);
+            *p.down(p.l0, u, v) = h;
+            *p.across(p.l1, u, v) = pack4(transposed(h));
+        }
+    if (t.i != t.j) P::Down::store(p.l0, out + (uint64_t)p.j * ld + p.i, ld);
+    P::Across::store(p.l1, out + (uint64_t)p.i * ld + p.j, ld);
 }
 
 // A = X X^T
@@ -310,16 +370,21 @@ struct Gram {
     float inv_s2;
     template <class Core>
     __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
+        using P = Piece<Core>;
         const uint16_t* x = w.xh + (uint64_t)at.z * mp * np;
         Core t;
         t.run(rows_of(x, at.i, np, Core::BP), rows_of(x, at.j, np, Core::BQ), np * 2, lds);
         uint16_t* a = w.a + (uint64_t)at.z * mp * mp;
         float* da = w.da + (uint64_t)at.z * mp;
 #pragma unroll
-        for (int u = 0; u < Core::TP; ++u)
+        for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
+            tf32x4 x[P::kU][Core::TQ];
 #pragma unroll
-            for (int v = 0; v < Core::TQ; ++v)
-                store_sym<Core>(at, Lane<Core>(at, u, v), t.acc[u][v] * inv_s2, a, mp, da);
+            for (int u = 0; u < P::kU; ++u)
+#pragma unroll
+                for (int v = 0; v < P::kV; ++v) x[u][v] = t.acc[u0 + u][v] * inv_s2;
+            store_sym<Core>(at, P(at, u0, lds), x, a, mp, da);
+        }
     }
 };
 
@@ -332,6 +397,7 @@ struct Poly {
     float kb, kc;
     template <class Core>
     __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
+        using P = Piece<Core>;
         const uint16_t* a = w.a + (uint64_t)at.z * mp * mp;
         const float* da = w.da + (uint64_t)at.z * mp;
         Core t;
@@ -339,24 +405,31 @@ struct Poly {
         uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
         float* db = w.db + (uint64_t)at.z * mp;
 #pragma unroll
-        for (int u = 0; u < Core::TP; ++u)
+        for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
+            const P p(at, u0, lds);
+            P::Down::load(p.l0, a + (uint64_t)p.j * mp + p.i, mp);
+            wave_wait();
+            tf32x4 x[P::kU][Core::TQ];
 #pragma unroll
-            for (int v = 0; v < Core::TQ; ++v) {
-                const Lane<Core> l(at, u, v);
-                const f16x4 o = load4(a + (uint64_t)l.j * mp + l.i);
-                const tf32x4 di = *(const tf32x4*)(da + l.i);
-                const float dj = da[l.j];
-                tf32x4 x;
+            for (int u = 0; u < P::kU; ++u) {
+                const tf32x4 di = *(const tf32x4*)(da + p.i + 16 * u + p.li);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool diag = l.i + e == l.j;
-                    const float off = (float)o[e];
-                    float sq = __builtin_fmaf(di[e] + dj, off, t.acc[u][v][e]);
-                    if (diag) sq = __builtin_fmaf(dj, dj, sq);
-                    x[e] = __builtin_fmaf(kc, sq, kb * (diag ? dj : off));
+                for (int v = 0; v < P::kV; ++v) {
+                    const float dj = da[p.j + 16 * v + p.lj];
+                    const f16x4 o = *p.down(p.l0, u, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const bool diag = p.i + 16 * u + p.li + e == p.j + 16 * v + p.lj;
+                        const float off = (float)o[e];
+                        float sq = __builtin_fmaf(di[e] + dj, off, t.acc[u0 + u][v][e]);
+                        if (diag) sq = __builtin_fmaf(dj, dj, sq);
+                        x[u][v][e] = __builtin_fmaf(kc, sq, kb * (diag ? dj : off));
+                    }
                 }
-                store_sym<Core>(at, l, x, b, mp, db);
             }
+            store_sym<Core>(at, p, x, b, mp, db);
+            if (u0 + P::kU < Core::TP) wave_wait();      // the next load overwrites the patches
+        }
     }
 };
 
@@ -369,36 +442,48 @@ struct Apply {
     int from;
     template <class Core>
     __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
+        using P = Piece<Core>;
         const uint64_t xz = (uint64_t)at.z * mp * np;
         const uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
         const uint16_t* xt = w.xt[from] + xz;
         Core t;
         t.run(rows_of(b, at.i, mp, Core::BP), rows_of(xt, at.j, mp, Core::BQ), mp * 2, lds);
         const float* db = w.db + (uint64_t)at.z * mp;
-        uint16_t* lt = w.lt + xz;
-        uint16_t* xo = w.xt[from ^ 1] + xz;
-        uint16_t* xh = w.xh + xz;
 #pragma unroll
-        for (int u = 0; u < Core::TP; ++u)
+        for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
+            const P p(at, u0, lds);
+            const uint64_t down = xz + (uint64_t)p.j * mp + p.i;
+            P::Down::load(p.l0, w.xt[from] + down, mp);
+            P::Down::load(p.l1, w.lt + down, mp);
+            wave_wait();
 #pragma unroll
-            for (int v = 0; v < Core::TQ; ++v) {
-                const Lane<Core> l(at, u, v);
-                const uint64_t p = (uint64_t)l.j * mp + l.i;
-                const f16x4 h = load4(xt + p), o = load4(lt + p);
-                const tf32x4 d = *(const tf32x4*)(db + l.i);
-                tf32x4 y;
+            for (int u = 0; u < P::kU; ++u) {
+                const tf32x4 d = *(const tf32x4*)(db + p.i + 16 * u + p.li);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y[e] = __builtin_fmaf(ka + d[e], __builtin_fmaf((float)o[e], 1.0f / kLo, (float)h[e]),
-                                          t.acc[u][v][e]);
-                const f16x4 nh = pack4(y);
-                f16x4 nl;
+                for (int v = 0; v < P::kV; ++v) {
+                    f16x4 *ph = p.down(p.l0, u, v), *pl = p.down(p.l1, u, v);
+                    const f16x4 h = *ph, o = *pl;
+                    tf32x4& y = t.acc[u0 + u][v];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) nl[e] = (_Float16)((y[e] - (float)nh[e]) * kLo);
-                store4(xo + p, nh);
-                store4(lt + p, nl);
-                store4(xh + (uint64_t)l.ti * np + l.tj, pack4(transposed(nh)));
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = __builtin_fmaf(ka + d[e], __builtin_fmaf((float)o[e], 1.0f / kLo, (float)h[e]), y[e]);
+                    const f16x4 nh = pack4(y);
+                    f16x4 nl;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) nl[e] = (_Float16)((y[e] - (float)nh[e]) * kLo);
+                    *ph = nh;
+                    *pl = nl;
+                }
             }
+            P::Down::store(p.l0, w.xt[from ^ 1] + down, mp);
+            P::Down::store(p.l1, w.lt + down, mp);
+#pragma unroll
+            for (int u = 0; u < P::kU; ++u)
+#pragma unroll
+                for (int v = 0; v < P::kV; ++v) *p.across(p.l0, u, v) = pack4(transposed(pack4(t.acc[u0 + u][v])));
+            P::Across::store(p.l0, w.xh + xz + (uint64_t)p.i * np + p.j, np);
+            if (u0 + P::kU < Core::TP) wave_wait();
+        }
     }
 };
 
@@ -484,33 +569,47 @@ struct Last {
         Core t;
         t.run(TALL ? br : xr, TALL ? xr : br, mp * 2, lds);
         const Dst dst(io, s, at.z, inv_s);
+        using P = Piece<Core>;
 #pragma unroll
-        for (int u = 0; u < Core::TP; ++u)
+        for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
+            const P p(at, u0, lds);
+            if constexpr (TALL) {
+                // D rows are i: four i of one j
+                P::Down::load(p.l0, xt + (uint64_t)p.j * mp + p.i, mp);
+                P::Down::load(p.l1, lt + (uint64_t)p.j * mp + p.i, mp);
+            } else {
+                // D rows (p.i) are j and its columns (p.j) are i: four j of one i
+                P::Down::load(p.l0, xh + (uint64_t)p.j * np + p.i, np);
+                P::Across::load(p.l1, lt + (uint64_t)p.i * mp + p.j, mp);
+            }
+            wave_wait();
 #pragma unroll
-            for (int v = 0; v < Core::TQ; ++v) {
-                const Lane<Core> l(at, u, v);
-                tf32x4 y;
-                if constexpr (TALL) {
-                    // D rows are i: four i of one j
-                    const uint64_t p = (uint64_t)l.j * mp + l.i;
-                    const f16x4 h = load4(xt + p), o = load4(lt + p);
-                    const tf32x4 d = *(const tf32x4*)(db + l.i);
+            for (int u = 0; u < P::kU; ++u) {
+                const uint32_t i = p.i + 16 * u + p.li;
+                const tf32x4 di = TALL ? *(const tf32x4*)(db + i) : tf32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int v = 0; v < P::kV; ++v) {
+                    const uint32_t j = p.j + 16 * v + p.lj;
+                    const f16x4 h = *p.down(p.l0, u, v);
+                    tf32x4 o;
+                    if constexpr (TALL) {
+                        const f16x4 q = *p.down(p.l1, u, v);
+                        o = tf32x4{(float)q[0], (float)q[1], (float)q[2], (float)q[3]};
+                    } else {
+                        o = transposed(*p.across(p.l1, u, v));
+                    }
+                    const float dj = TALL ? 0.0f : db[j];
+                    tf32x4 y;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[e] = __builtin_fmaf(ka + d[e], __builtin_fmaf((float)o[e], 1.0f / kLo, (float)h[e]),
-                                              t.acc[u][v][e]);
-                    if (l.j < s.n && l.i < s.m) dst.store(l.j, l.i, min(4u, s.m - l.i), y);
-                } else {
-                    // D rows are j (l.i), its columns i (l.j): four j of one i
-                    const f16x4 h = load4(xh + (uint64_t)l.j * np + l.i);
-                    const tf32x4 o = transposed(load4(lt + (uint64_t)l.ti * mp + l.tj));
-                    const float d = ka + db[l.j];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[e] = __builtin_fmaf(d, __builtin_fmaf(o[e], 1.0f / kLo, (float)h[e]), t.acc[u][v][e]);
-                    if (l.j < s.m && l.i < s.n) dst.store(l.j, l.i, min(4u, s.n - l.i), y);
+                        y[e] = __builtin_fmaf(ka + (TALL ? di[e] : dj), __builtin_fmaf(o[e], 1.0f / kLo, (float)h[e]),
+                                              t.acc[u0 + u][v][e]);
+                    const uint32_t rows = TALL ? s.n : s.m, cols = TALL ? s.m : s.n;
+                    if (j < rows && i < cols) dst.store(j, i, min(4u, cols - i), y);
                 }
             }
+            if (u0 + P::kU < Core::TP) wave_wait();
+        }
     }
 };
 
