@@ -158,7 +158,8 @@ extern "C" int neox_orthogonalize(const neox_ns_config* cfg, const void* src, in
         const uint64_t n = std::min(most, count - z);
         const OrthIO io{(const uint8_t*)src + z * src_stride * sb, (uint8_t*)dst + z * dst_stride * db,
                         src_ld, src_stride, dst_ld, dst_stride, src_dtype, dst_dtype, (float)scale,
-                        d0 % (4 * db) == 0 && dst_ld % 4 == 0 && (count == 1 || dst_stride % 4 == 0), cfg->eps};
+                        d0 % (4 * db) == 0 && dst_ld % 4 == 0 && (count == 1 || dst_stride % 4 == 0),
+                        s0 % (4 * sb) == 0 && src_ld % 4 == 0 && (count == 1 || src_stride % 4 == 0), cfg->eps};
         const hipError_t e = enqueue_orth(s, w, (uint32_t)n, io, coef, cfg->steps,
                                           static_cast<hipStream_t>(hip_stream));
         if (e != hipSuccess) return set_hip_error(e, "orthogonalize launch");
@@ -502,8 +503,8 @@ static int mx_sides(uint64_t rows, uint64_t cols) {
     if (rows == 0 || cols == 0 || rows > kMaxMx || cols > kMaxMx)
         return set_error(NEOX_EINVAL, "a copy of %llu x %llu: sides of 1 to 2^31 - 1",
                          (unsigned long long)rows, (unsigned long long)cols);
-    // one thread per block of 32
-    if (rows > (kMaxBlocks - 1) * 256 / mx_shape(cols).scale_pitch)
+    // bytes of the codes and offsets in them stay far from 64 bits
+    if (rows > (1ull << 40) / mx_shape(cols).code_pitch)
         return set_error(NEOX_EINVAL, "a copy of %llu x %llu is too large", (unsigned long long)rows,
                          (unsigned long long)cols);
     return NEOX_OK;

@@ -47,6 +47,7 @@ struct OrthIO {
     int32_t src_dtype, dst_dtype;
     float scale;
     bool vec;              // dst can be written four elements at a time
+    bool vec_src;          // src read so
     double eps;
 };
 struct MuonMat {           // device table entry

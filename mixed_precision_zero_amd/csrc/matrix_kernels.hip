@@ -23,9 +23,6 @@ namespace nz1 {
 
 namespace {
 
-__device__ __forceinline__ float f16(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
-__device__ __forceinline__ uint16_t to_f16(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
-
 constexpr float kLo = 2048.0f;            // lt holds (x - hi) * kLo
 
 // The step state whose skip flag the kernels heed (none: always run).
@@ -46,23 +43,68 @@ __device__ __forceinline__ double sum_block(double v) {
     return r;
 }
 
+// Four or eight consecutive elements, as one or two 16-byte loads (8 bytes for four halves).
+__device__ __forceinline__ tf32x4 halves4(int dtype, uint2 q) {
+    return tf32x4{half_to_float(dtype, (uint16_t)q.x), half_to_float(dtype, (uint16_t)(q.x >> 16)),
+                  half_to_float(dtype, (uint16_t)q.y), half_to_float(dtype, (uint16_t)(q.y >> 16))};
+}
+__device__ __forceinline__ tf32x4 vec4(const void* p, int dtype, uint64_t i) {
+    if (dtype == NEOX_F32) return *(const tf32x4*)((const float*)p + i);
+    return halves4(dtype, *(const uint2*)((const uint16_t*)p + i));
+}
+
 // ------------------------------------------------------------------------------------
 // squared norm of each source matrix; for Muon also the momentum's own update
+//
+// Memory-bound: 1,024 threads a block and at most kNsParts blocks a matrix, so that one large
+// matrix still has a block on every CU with two vectors in flight a thread.
 // ------------------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void orth_norm_kernel(OrthIO io, uint32_t rows, uint32_t cols,
-                                                        uint32_t parts, double* __restrict__ part) {
+constexpr int kNormThreads = 1024;
+
+__device__ __forceinline__ double square4(tf32x4 v, double s) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = __builtin_fma((double)v[e], (double)v[e], s);
+    return s;
+}
+
+__global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(OrthIO io, uint32_t rows, uint32_t cols,
+                                                                 uint32_t parts, double* __restrict__ part) {
     const uint32_t z = blockIdx.x / parts, p = blockIdx.x % parts;
     const uint32_t per = (rows + parts - 1) / parts;
     const uint32_t r0 = p * per, r1 = min(rows, r0 + per);
-    double s = 0.0;
-    for (uint32_t r = r0; r < r1; ++r) {
-        const uint64_t at = z * io.src_stride + r * io.src_ld;
-        for (uint32_t c = threadIdx.x; c < cols; c += 256) {
-            const double x = load_elem(io.src, io.src_dtype, at + c);
-            s = __builtin_fma(x, x, s);
+    const uint64_t at = z * io.src_stride;
+    double s = 0.0, t = 0.0;
+    if (io.vec_src && cols % 4 == 0) {
+        // this block's rows as one run of vectors, two in flight
+        const uint32_t w = cols / 4;
+        uint32_t r = r0 + threadIdx.x / w, c = threadIdx.x % w;
+        const uint32_t dr = kNormThreads / w, dc = kNormThreads % w;
+        auto next = [&]() {
+            r += dr;
+            c += dc;
+            if (c >= w) {
+                c -= w;
+                ++r;
+            }
+        };
+        while (r < r1) {
+            const tf32x4 v = vec4(io.src, io.src_dtype, at + r * io.src_ld + 4 * c);
+            next();
+            if (r < r1) {
+                const tf32x4 q = vec4(io.src, io.src_dtype, at + r * io.src_ld + 4 * c);
+                t = square4(q, t);
+            }
+            s = square4(v, s);
+            next();
         }
+    } else {
+        for (uint32_t r = r0; r < r1; ++r)
+            for (uint32_t c = threadIdx.x; c < cols; c += kNormThreads) {
+                const double x = load_elem(io.src, io.src_dtype, at + r * io.src_ld + c);
+                s = __builtin_fma(x, x, s);
+            }
     }
-    s = sum_block<256>(s);
+    s = sum_block<kNormThreads>(s + t);
     if (threadIdx.x == 0) part[(uint64_t)z * kNsParts + p] = s;
 }
 
@@ -70,21 +112,47 @@ __device__ __forceinline__ float direction(const MuonIO& io, float g, float m) {
     return io.nesterov ? __builtin_fmaf(io.mu, m, g) : m;
 }
 
-__global__ __launch_bounds__(256) void muon_momentum_kernel(MuonIO io, uint64_t numel,
-                                                            uint32_t parts, double* __restrict__ part) {
+__global__ __launch_bounds__(kNormThreads) void muon_momentum_kernel(MuonIO io, uint64_t numel,
+                                                                     uint32_t parts, double* __restrict__ part) {
     if (io.st->skip) return;
     const float gs = io.st->gscale;
     const uint32_t z = blockIdx.x / parts, p = blockIdx.x % parts;
     const MuonMat mat = io.mats[z];
     double s = 0.0;
-    for (uint64_t i = (uint64_t)p * 256 + threadIdx.x; i < numel; i += (uint64_t)parts * 256) {
+    uint64_t done = 0;
+    if (mat.vec) {
+        const uint64_t n4 = numel / 4, step = (uint64_t)parts * kNormThreads;
+        done = n4 * 4;
+        for (uint64_t i = (uint64_t)p * kNormThreads + threadIdx.x; i < n4; i += 2 * step) {
+            const uint64_t j = i + step < n4 ? i + step : i;        // the same again at the end
+            tf32x4 g[2], m[2];
+            g[0] = halves4(io.dtype, *(const uint2*)(mat.grad + 4 * i));
+            g[1] = halves4(io.dtype, *(const uint2*)(mat.grad + 4 * j));
+            m[0] = *(const tf32x4*)(mat.mom + 4 * i);
+            m[1] = *(const tf32x4*)(mat.mom + 4 * j);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (k == 1 && j == i) break;
+                tf32x4 u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = g[k][e] * gs;
+                    m[k][e] = __builtin_fmaf(io.mu, m[k][e], x);
+                    u[e] = direction(io, x, m[k][e]);
+                }
+                *(tf32x4*)(mat.mom + 4 * (k ? j : i)) = m[k];
+                s = square4(u, s);
+            }
+        }
+    }
+    for (uint64_t i = done + (uint64_t)p * kNormThreads + threadIdx.x; i < numel; i += (uint64_t)parts * kNormThreads) {
         const float g = half_to_float(io.dtype, mat.grad[i]) * gs;
         const float m = __builtin_fmaf(io.mu, mat.mom[i], g);
         mat.mom[i] = m;
         const double u = direction(io, g, m);
         s = __builtin_fma(u, u, s);
     }
-    s = sum_block<256>(s);
+    s = sum_block<kNormThreads>(s);
     if (threadIdx.x == 0) part[(uint64_t)z * kNsParts + p] = s;
 }
 
@@ -94,21 +162,38 @@ __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonIO io, uint64_t 
 struct OrthSrc {
     const OrthIO& io;
     uint64_t at;
-    __device__ OrthSrc(const OrthIO& i, uint32_t z) : io(i), at(z * i.src_stride) {}
+    bool vec;
+    __device__ OrthSrc(const OrthIO& i, const NsShape& s, uint32_t z)
+        : io(i), at(z * i.src_stride), vec(i.vec_src && s.cols % 4 == 0) {}
     __device__ float load(uint32_t r, uint32_t c, uint32_t) const {
         return load_elem(io.src, io.src_dtype, at + r * io.src_ld + c);
+    }
+    __device__ tf32x4 load4(uint32_t r, uint32_t c, uint32_t) const {
+        return vec4(io.src, io.src_dtype, at + r * io.src_ld + c);
     }
 };
 struct MuonSrc {
     const MuonIO& io;
     MuonMat mat;
     float gs;
-    __device__ MuonSrc(const MuonIO& i, uint32_t z) : io(i), mat(i.mats[z]), gs(i.st->gscale) {}
+    bool vec;
+    __device__ MuonSrc(const MuonIO& i, const NsShape& s, uint32_t z)
+        : io(i), mat(i.mats[z]), gs(i.st->gscale), vec(mat.vec && s.cols % 4 == 0) {}
     __device__ float load(uint32_t r, uint32_t c, uint32_t cols) const {
         const uint64_t i = (uint64_t)r * cols + c;
         return direction(io, half_to_float(io.dtype, mat.grad[i]) * gs, mat.mom[i]);
     }
+    __device__ tf32x4 load4(uint32_t r, uint32_t c, uint32_t cols) const {
+        const uint64_t i = (uint64_t)r * cols + c;
+        const tf32x4 g = halves4(io.dtype, *(const uint2*)(mat.grad + i)), m = *(const tf32x4*)(mat.mom + i);
+        tf32x4 u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = direction(io, g[e] * gs, m[e]);
+        return u;
+    }
 };
+
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 template <class Src, class IO>
 __global__ __launch_bounds__(256) void ns_convert_kernel(IO io, NsShape s, NsBuf w) {
@@ -118,29 +203,52 @@ __global__ __launch_bounds__(256) void ns_convert_kernel(IO io, NsShape s, NsBuf
     const uint32_t z = blockIdx.x / (ti * tj), t = blockIdx.x % (ti * tj);
     const uint32_t i0 = t / tj * 64, j0 = t % tj * 64;
     const double* part = w.part + (uint64_t)z * kNsParts;
-    const double sq = sum_block<256>(threadIdx.x < s.parts ? part[threadIdx.x] : 0.0);
-    const double f = (double)s.s / (__builtin_sqrt(sq) + io.eps);
-    const Src src(io, z);
-    const uint32_t lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const Src src(io, s, z);
+    // lane: four neighbours of one of sixteen rows
+    const uint32_t q = (threadIdx.x & 15) * 4, k0 = threadIdx.x >> 4;
     // the tile as the source has it: rows r0.., columns c0..
     const uint32_t r0 = s.tall ? j0 : i0, c0 = s.tall ? i0 : j0;
-#pragma unroll 4
-    for (uint32_t k = wv; k < 64; k += 4) {
-        const uint32_t r = r0 + k, c = c0 + lane;
-        tile[k][lane] = r < s.rows && c < s.cols ? (float)((double)src.load(r, c, s.cols) * f) : 0.0f;
+    tf32x4 v[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        const uint32_t r = r0 + k0 + 16 * k, c = c0 + q;
+        v[k] = tf32x4{0, 0, 0, 0};
+        if (r < s.rows && c < s.cols) {
+            if (src.vec) {
+                v[k] = src.load4(r, c, s.cols);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    if (c + e < s.cols) v[k][e] = src.load(r, c + e, s.cols);
+            }
+        }
     }
+    const double sq = sum_block<256>(threadIdx.x < s.parts ? part[threadIdx.x] : 0.0);
+    const double f = (double)s.s / (__builtin_sqrt(sq) + io.eps);
+    // products in 64 bits: f overflows or vanishes in 32 where the source is tiny or huge
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tile[k0 + 16 * k][q + e] = (float)((double)v[k][e] * f);
     __syncthreads();
     const uint64_t xz = (uint64_t)z * s.mp * s.np;
-#pragma unroll 4
-    for (uint32_t k = wv; k < 64; k += 4) {
-        // row k of the tile in the wide form, and column k of it
-        const float x = s.tall ? tile[lane][k] : tile[k][lane];
-        w.xh[xz + (uint64_t)(i0 + k) * s.np + j0 + lane] = to_f16(x);
-        const float y = s.tall ? tile[k][lane] : tile[lane][k];
-        const uint16_t hi = to_f16(y);
-        const uint64_t at = xz + (uint64_t)(j0 + k) * s.mp + i0 + lane;
-        w.xt[0][at] = hi;
-        w.lt[at] = to_f16((y - f16(hi)) * kLo);
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        // row `row` of the tile in the wide form, and column `row` of it
+        const uint32_t row = k0 + 16 * k;
+        f16x4 across, hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = tile[row][q + e], b = tile[q + e][row];
+            across[e] = (_Float16)(s.tall ? b : a);
+            const float y = s.tall ? a : b;
+            hi[e] = (_Float16)y;
+            lo[e] = (_Float16)((y - (float)hi[e]) * kLo);
+        }
+        *(f16x4*)(w.xh + xz + (uint64_t)(i0 + row) * s.np + j0 + q) = across;
+        const uint64_t at = xz + (uint64_t)(j0 + row) * s.mp + i0 + q;
+        *(f16x4*)(w.xt[0] + at) = hi;
+        *(f16x4*)(w.lt + at) = lo;
     }
 }
 
@@ -249,8 +357,6 @@ __device__ __forceinline__ TileAt place_even(uint32_t mp, uint32_t np) {
 __device__ __forceinline__ TileRows rows_of(const uint16_t* base, uint64_t row, uint32_t len, int block) {
     return TileRows{(const uint8_t*)(base + row * len), nullptr, (uint32_t)block, len * 2u, 0u};
 }
-
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 // A lane of a 16 x 16 result tile holds four consecutive rows of one column.  These are the
 // elements of the same tile that are four consecutive columns of one row (row lane % 16,
@@ -721,7 +827,7 @@ hipError_t enqueue_steps(const NsShape& s, const NsBuf& w, uint32_t count, const
 
 hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const OrthIO& io,
                         const NsCoef* coef, int steps, hipStream_t stream) {
-    orth_norm_kernel<<<s.parts * count, 256, 0, stream>>>(io, s.rows, s.cols, s.parts, w.part);
+    orth_norm_kernel<<<s.parts * count, kNormThreads, 0, stream>>>(io, s.rows, s.cols, s.parts, w.part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return enqueue_steps<OrthIO, OrthSrc, OrthDst>(s, w, count, io, coef, steps, stream);
@@ -729,7 +835,7 @@ hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const 
 
 hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const MuonIO& io,
                         const NsCoef* coef, int steps, hipStream_t stream) {
-    muon_momentum_kernel<<<s.parts * count, 256, 0, stream>>>(io, (uint64_t)s.rows * s.cols, s.parts, w.part);
+    muon_momentum_kernel<<<s.parts * count, kNormThreads, 0, stream>>>(io, (uint64_t)s.rows * s.cols, s.parts, w.part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return enqueue_steps<MuonIO, MuonSrc, MuonDst>(s, w, count, io, coef, steps, stream);

@@ -3,6 +3,9 @@
 #include "matrix_internal.h"
 #include "tile_core.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace nz1 {
 
 namespace {
@@ -24,48 +27,107 @@ __device__ __forceinline__ uint32_t e2m1(float x) {
     return (uint32_t)c | (__float_as_uint(x) >> 28 & 8u);
 }
 
-// a block of 32 elements by one thread: 16 bytes of codes and the scale byte
-__device__ __forceinline__ uint32_t quantize32(const float (&v)[32], uint32_t (&w)[4]) {
+// How the rows of an array are spread over blocks of 256 threads, a thread taking eight
+// elements: `wide` threads side by side (a power of two) on 256 / wide rows.
+struct Spread {
+    uint32_t shift;        // log2(wide)
+    uint32_t across;       // blocks across a row
+    uint64_t blocks;
+};
+Spread spread(uint64_t rows, uint64_t units) {
+    Spread s{};
+    while (s.shift < 8 && (1ull << s.shift) < units) ++s.shift;
+    s.across = (uint32_t)((units + (1ull << s.shift) - 1) >> s.shift);
+    const uint64_t per = 256u >> s.shift;
+    s.blocks = (rows + per - 1) / per * s.across;
+    return s;
+}
+struct Unit {
+    uint64_t row;
+    uint32_t unit;         // eight elements each
+    __device__ explicit Unit(const Spread& s) {
+        const uint32_t down = blockIdx.x / s.across;
+        row = (uint64_t)down * (256u >> s.shift) + (threadIdx.x >> s.shift);
+        unit = ((blockIdx.x - down * s.across) << s.shift) + (threadIdx.x & ((1u << s.shift) - 1));
+    }
+};
+
+__device__ __forceinline__ float decode(int dtype, uint32_t w, int k) {
+    return half_to_float(dtype, (uint16_t)(w >> (16 * k)));
+}
+
+// Memory-bound.  Four neighbouring threads hold a block of 32, eight elements each (16 or 32
+// bytes), find its largest magnitude with two exchanges, and write four bytes of codes each.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restrict__ src, uint64_t R, uint64_t C,
+                                                            uint64_t ld, bool vec, uint8_t* __restrict__ codes,
+                                                            uint8_t* __restrict__ scales, MxShape sh, Spread sp,
+                                                            const DevState* __restrict__ st) {
+    if (st && st->skip) return;
+    const Unit u(sp);
+    // whole groups of four threads leave together (16 units fill 128 elements)
+    if (u.row >= R || u.unit * 4ull >= sh.code_pitch) return;
+    const uint64_t c = u.unit * 8ull, at = u.row * ld + c;
+    float v[8];
+    if (vec && c + 8 <= C) {
+        if constexpr (DT == NEOX_F32) {
+            const tf32x4 a = *(const tf32x4*)((const float*)src + at), b = *(const tf32x4*)((const float*)src + at + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = a[i];
+                v[4 + i] = b[i];
+            }
+        } else {
+            const tu32x4 a = *(const tu32x4*)((const uint16_t*)src + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = decode(DT, a[i / 2], i & 1);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < C ? load_elem(src, DT, at + i) : 0.0f;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+    const uint32_t s = scale_byte(top);
+    const float inv = __uint_as_float((254u - (s == 255u ? 127u : s)) << 23);   // 2^(127 - s)
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= e2m1(v[i] * inv) << (4 * i);
+    *(uint32_t*)(codes + u.row * sh.code_pitch + u.unit * 4ull) = s == 255u ? 0u : w;
+    if ((u.unit & 3) == 0) scales[u.row * sh.scale_pitch + u.unit / 4] = (uint8_t)s;
+}
+
+// The transpose: a thread takes 32 rows of one column of src, a wave 64 neighbouring columns.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_cols_kernel(const void* __restrict__ src, uint64_t R, uint64_t C,
+                                                            uint64_t ld, uint8_t* __restrict__ codes,
+                                                            uint8_t* __restrict__ scales, MxShape sh,
+                                                            uint32_t across, uint32_t b0,
+                                                            const DevState* __restrict__ st) {
+    if (st && st->skip) return;
+    // R, C: the copy's; its row r is src's column r.  b: block of 32 along it
+    const uint32_t down = blockIdx.x / across, b = b0 + down;
+    const uint64_t r = (uint64_t)(blockIdx.x - down * across) * 256 + threadIdx.x;
+    if (r >= R) return;
+    float v[32];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        top = b > top ? b : top;
+        const uint64_t c = b * 32ull + i;
+        v[i] = c < C ? load_elem(src, DT, c * ld + r) : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     const uint32_t s = scale_byte(top);
-    const float inv = __uint_as_float((254u - (s == 255u ? 127u : s)) << 23);   // 2^(127 - s)
+    const float inv = __uint_as_float((254u - (s == 255u ? 127u : s)) << 23);
+    tu32x4 w = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t u = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u |= e2m1(v[8 * j + i] * inv) << (4 * i);
-        w[j] = s == 255u ? 0u : u;
-    }
-    return s;
-}
-
-// one thread per block of 32; the copy is R x C (the source's transpose with T)
-template <bool T>
-__global__ __launch_bounds__(256) void quantize_kernel(const void* __restrict__ src, int dtype,
-                                                       uint64_t R, uint64_t C, uint64_t ld,
-                                                       uint8_t* __restrict__ codes,
-                                                       uint8_t* __restrict__ scales,
-                                                       MxShape sh, const DevState* __restrict__ st) {
-    if (st && st->skip) return;
-    const uint64_t per = sh.scale_pitch;
-    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    uint64_t r, b;
-    if (T) { b = id / R; r = id % R; } else { r = id / per; b = id % per; }
-    if (r >= R || b >= per) return;
-    float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint64_t c = b * 32 + i;
-        v[i] = c < C ? load_elem(src, dtype, T ? c * ld + r : r * ld + c) : 0.0f;
-    }
-    uint32_t w[4];
-    const uint32_t s = quantize32(v, w);
-    *(uint4*)(codes + r * sh.code_pitch + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 32; ++i) w[i / 8] |= e2m1(v[i] * inv) << (4 * (i % 8));
+    if (s == 255u) w = tu32x4{0, 0, 0, 0};
+    *(tu32x4*)(codes + r * sh.code_pitch + b * 16ull) = w;
     scales[r * sh.scale_pitch + b] = (uint8_t)s;
 }
 
@@ -76,22 +138,35 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
     return c & 8u ? -a : a;
 }
 
+template <int DT>
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restrict__ codes,
-                                                         const uint8_t* __restrict__ scales,
-                                                         uint64_t R, uint64_t C, MxShape sh,
-                                                         void* __restrict__ dst, int dtype, uint64_t ld) {
-    const uint64_t blocks = (C + 31) / 32;
-    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    const uint64_t r = id / blocks, b = id % blocks;
-    if (r >= R) return;
-    const uint32_t s = scales[r * sh.scale_pitch + b];
-    const uint4 q = *(const uint4*)(codes + r * sh.code_pitch + b * 16);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                                                         const uint8_t* __restrict__ scales, uint64_t R,
+                                                         uint64_t C, MxShape sh, void* __restrict__ dst,
+                                                         uint64_t ld, bool vec, Spread sp) {
+    const Unit u(sp);
+    const uint64_t c = u.unit * 8ull, at = u.row * ld + c;
+    if (u.row >= R || c >= C) return;
+    const uint32_t s = scales[u.row * sh.scale_pitch + u.unit / 4];
+    const uint32_t w = *(const uint32_t*)(codes + u.row * sh.code_pitch + u.unit * 4ull);
     const float f = s == 255u ? __builtin_nanf("") : s == 0u ? 0x1p-127f : __uint_as_float(s << 23);
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint64_t c = b * 32 + i;
-        if (c < C) store_elem(dst, dtype, r * ld + c, e2m1_value(w[i >> 3] >> (4 * (i & 7))) * f);
+    for (int i = 0; i < 8; ++i) v[i] = e2m1_value(w >> (4 * i)) * f;
+    if (vec && c + 8 <= C) {
+        if constexpr (DT == NEOX_F32) {
+            *(tf32x4*)((float*)dst + at) = tf32x4{v[0], v[1], v[2], v[3]};
+            *(tf32x4*)((float*)dst + at + 4) = tf32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            tu32x4 q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                q[i] = float_to_half(DT, v[2 * i]) | (uint32_t)float_to_half(DT, v[2 * i + 1]) << 16;
+            *(tu32x4*)((uint16_t*)dst + at) = q;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < C) store_elem(dst, DT, at + i, v[i]);
     }
 }
 
@@ -126,26 +201,66 @@ __global__ __launch_bounds__(Core::NT) void product_kernel(const uint8_t* a_code
 
 }  // namespace
 
+// Blocks of one launch: a grid has fewer than 2^32 threads.
+constexpr uint64_t kGrid = 1ull << 23;
+
+// Launches f(first row, rows, their spread) for as many rows at a time as a grid takes.
+template <class F>
+static void rows_in_grids(uint64_t rows, uint64_t units, F f) {
+    const Spread one = spread(256, units);              // blocks for 256 rows
+    const uint64_t most = std::max<uint64_t>(1, kGrid / one.blocks) * 256;
+    for (uint64_t r = 0; r < rows; r += most) {
+        const uint64_t n = std::min(most, rows - r);
+        f(r, n, spread(n, units));
+    }
+}
+
+// whether rows of eight elements can be moved 16 bytes at a time
+static bool eights(const void* p, int dtype, uint64_t ld) {
+    return (uintptr_t)p % 16 == 0 && ld * (dtype == NEOX_F32 ? 4 : 2) % 16 == 0;
+}
+
 hipError_t launch_mx_quantize(const void* src, int dtype, uint64_t rows, uint64_t cols, uint64_t ld,
                               bool transpose, void* codes, void* scales, const DevState* st,
                               hipStream_t stream) {
     const uint64_t R = transpose ? cols : rows, C = transpose ? rows : cols;
     const MxShape sh = mx_shape(C);
-    const uint64_t blocks = (R * sh.scale_pitch + 255) / 256;
-    if (transpose)
-        quantize_kernel<true><<<(uint32_t)blocks, 256, 0, stream>>>(src, dtype, R, C, ld, (uint8_t*)codes,
-                                                                    (uint8_t*)scales, sh, st);
-    else
-        quantize_kernel<false><<<(uint32_t)blocks, 256, 0, stream>>>(src, dtype, R, C, ld, (uint8_t*)codes,
-                                                                     (uint8_t*)scales, sh, st);
+    auto run = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (transpose) {
+            const uint32_t across = (uint32_t)((R + 255) / 256);
+            const uint64_t most = std::max<uint64_t>(1, kGrid / across);
+            for (uint64_t b = 0; b < sh.scale_pitch; b += most)
+                quantize_cols_kernel<DT><<<(uint32_t)(across * std::min(most, sh.scale_pitch - b)), 256, 0, stream>>>(
+                    src, R, C, ld, (uint8_t*)codes, (uint8_t*)scales, sh, across, (uint32_t)b, st);
+        } else {
+            rows_in_grids(R, sh.code_pitch / 4, [&](uint64_t r, uint64_t n, const Spread& sp) {
+                quantize_rows_kernel<DT><<<(uint32_t)sp.blocks, 256, 0, stream>>>(
+                    (const uint8_t*)src + r * ld * (DT == NEOX_F32 ? 4 : 2), n, C, ld, eights(src, dtype, ld),
+                    (uint8_t*)codes + r * sh.code_pitch, (uint8_t*)scales + r * sh.scale_pitch, sh, sp, st);
+            });
+        }
+    };
+    if (dtype == NEOX_F32) run(std::integral_constant<int, NEOX_F32>{});
+    else if (dtype == NEOX_F16) run(std::integral_constant<int, NEOX_F16>{});
+    else run(std::integral_constant<int, NEOX_BF16>{});
     return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const void* codes, const void* scales, uint64_t rows, uint64_t cols,
                                 void* dst, int dtype, uint64_t ld, hipStream_t stream) {
-    const uint64_t blocks = (rows * ((cols + 31) / 32) + 255) / 256;
-    dequantize_kernel<<<(uint32_t)blocks, 256, 0, stream>>>((const uint8_t*)codes, (const uint8_t*)scales,
-                                                            rows, cols, mx_shape(cols), dst, dtype, ld);
+    const MxShape sh = mx_shape(cols);
+    auto run = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        rows_in_grids(rows, (cols + 7) / 8, [&](uint64_t r, uint64_t n, const Spread& sp) {
+            dequantize_kernel<DT><<<(uint32_t)sp.blocks, 256, 0, stream>>>(
+                (const uint8_t*)codes + r * sh.code_pitch, (const uint8_t*)scales + r * sh.scale_pitch, n, cols, sh,
+                (uint8_t*)dst + r * ld * (DT == NEOX_F32 ? 4 : 2), ld, eights(dst, dtype, ld), sp);
+        });
+    };
+    if (dtype == NEOX_F32) run(std::integral_constant<int, NEOX_F32>{});
+    else if (dtype == NEOX_F16) run(std::integral_constant<int, NEOX_F16>{});
+    else run(std::integral_constant<int, NEOX_BF16>{});
     return hipGetLastError();
 }
 
