@@ -170,33 +170,150 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
     }
 }
 
-// D = P Q^T with P the copy b (so that a lane's four results are consecutive columns of c)
+// ------------------------------------------------------------------------------------
+// product: D = P Q^T with P the copy b (its rows are columns of c), Q the copy a, so that a
+// lane's four results are consecutive columns of c
+// ------------------------------------------------------------------------------------
+struct ProductArgs {
+    const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
+    void* c;
+    uint64_t ldc;
+    uint32_t m, n;
+    uint32_t pitch, spitch;    // bytes per row of the codes and the scales
+    int32_t dtype;
+    bool vec;                  // rows of c can be written 16 bytes at a time
+};
+
+__device__ __forceinline__ void store_four(const ProductArgs& a, uint32_t i, uint32_t j, tf32x4 x) {
+    if (i >= a.m) return;
+    const uint64_t at = i * a.ldc + j;
+    if (a.vec && j + 4 <= a.n) {
+        if (a.dtype == NEOX_F32) *(tf32x4*)((float*)a.c + at) = x;
+        else *(ushort4*)((uint16_t*)a.c + at) = make_ushort4(float_to_half(a.dtype, x[0]), float_to_half(a.dtype, x[1]),
+                                                             float_to_half(a.dtype, x[2]), float_to_half(a.dtype, x[3]));
+    } else {
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            if (j + e < a.n) store_elem(a.c, a.dtype, at + e, x[e]);
+    }
+}
+
+// One tile of c: rows at.j .., columns at.i ..
 template <class Core>
-__global__ __launch_bounds__(Core::NT) void product_kernel(const uint8_t* a_codes, const uint8_t* a_scales,
-                                                           uint32_t m, const uint8_t* b_codes,
-                                                           const uint8_t* b_scales, uint32_t n, MxShape sh,
-                                                           void* c, int dtype, uint64_t ldc) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
-    const uint32_t tn = (n + Core::BP - 1) / Core::BP;
-    const uint32_t p0 = blockIdx.x % tn * Core::BP, q0 = blockIdx.x / tn * Core::BQ;
-    const TileRows p{b_codes + (uint64_t)p0 * sh.code_pitch, b_scales + (uint64_t)p0 * sh.scale_pitch,
-                     min((uint32_t)Core::BP, n - p0), (uint32_t)sh.code_pitch, (uint32_t)sh.scale_pitch};
-    const TileRows q{a_codes + (uint64_t)q0 * sh.code_pitch, a_scales + (uint64_t)q0 * sh.scale_pitch,
-                     min((uint32_t)Core::BQ, m - q0), (uint32_t)sh.code_pitch, (uint32_t)sh.scale_pitch};
+__device__ __forceinline__ void product_tile(const ProductArgs& a, const TileAt& at, uint8_t* lds) {
+    const TileRows p{a.b_codes + (uint64_t)at.i * a.pitch, a.b_scales + (uint64_t)at.i * a.spitch,
+                     min((uint32_t)Core::BP, a.n - at.i), a.pitch, a.spitch};
+    const TileRows q{a.a_codes + (uint64_t)at.j * a.pitch, a.a_scales + (uint64_t)at.j * a.spitch,
+                     min((uint32_t)Core::BQ, a.m - at.j), a.pitch, a.spitch};
     Core t;
-    t.run(p, q, (uint32_t)sh.code_pitch, lds);
-    const uint32_t lane = threadIdx.x & 63;
-    const uint32_t jb = p0 + Core::wave_p() + (lane >> 4) * 4;
-    const uint32_t ib = q0 + Core::wave_q() + (lane & 15);
+    t.run(p, q, a.pitch, lds);
+    using P = Piece<Core>;
 #pragma unroll
-    for (int u = 0; u < Core::TP; ++u)
+    for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
+        const P pc(at, u0, lds);
+        if (a.dtype != NEOX_F32 && a.vec && pc.i + 16 * P::kU <= a.n) {
+            // 16-bit results: whole rows through LDS
 #pragma unroll
-        for (int v = 0; v < Core::TQ; ++v)
+            for (int u = 0; u < P::kU; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t i = ib + 16 * v, j = jb + 16 * u + e;
-                if (i < m && j < n) store_elem(c, dtype, i * ldc + j, t.acc[u][v][e]);
-            }
+                for (int v = 0; v < P::kV; ++v) {
+                    const tf32x4 x = t.acc[u0 + u][v];
+                    const ushort4 h = make_ushort4(float_to_half(a.dtype, x[0]), float_to_half(a.dtype, x[1]),
+                                                   float_to_half(a.dtype, x[2]), float_to_half(a.dtype, x[3]));
+                    *(ushort4*)pc.down(pc.l0, u, v) = h;
+                }
+            const uint32_t left = pc.j < a.m ? a.m - pc.j : 0u;
+            P::Down::store(pc.l0, (uint16_t*)a.c + (uint64_t)pc.j * a.ldc + pc.i, a.ldc, left);
+        } else {
+#pragma unroll
+            for (int u = 0; u < P::kU; ++u)
+#pragma unroll
+                for (int v = 0; v < P::kV; ++v)
+                    store_four(a, pc.j + 16 * v + pc.lj, pc.i + 16 * u + pc.li, t.acc[u0 + u][v]);
+        }
+    }
+}
+
+using Mx256 = TileCore<256, 256, 2, 4, true>;
+using Mx128w = TileCore<128, 128, 2, 4, true>;       // quarters, by the same 512 threads
+using Mx128 = TileCore<128, 128, 2, 2, true>;
+
+__global__ __launch_bounds__(512, 2) void product_mixed_kernel(ProductArgs a, TileMap m) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Mx256::kLds];
+    const TileAt at = place<false>(m);
+    if (at.full) product_tile<Mx256>(a, at, lds);
+    else if (!at.none) product_tile<Mx128w>(a, at, lds);
+}
+template <class Core>
+__global__ __launch_bounds__(Core::NT) void product_even_kernel(ProductArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
+    const uint32_t p = (a.n + Core::BP - 1) / Core::BP;
+    TileAt at{};
+    at.i = blockIdx.x % p * Core::BP;
+    at.j = blockIdx.x / p * Core::BQ;
+    product_tile<Core>(a, at, lds);
+}
+
+// Few rows of a (up to 16 MT): bound by reading b once.  A block takes 16 rows of b; its WK
+// waves share K in steps of 512 elements and add their results at the end in wave order.  No
+// LDS on the way: per step a lane reads 64 bytes of its row (four blocks of 32) and their four
+// scale bytes as one dword, so each of the four products of a step picks its scale by byte.
+template <int MT, int WK>
+__global__ __launch_bounds__(WK * 64) void product_thin_kernel(ProductArgs a) {
+    static_assert(WK >= MT, "");
+    __shared__ tf32x4 part[WK][MT][64];
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t n0 = blockIdx.x * 16;
+    const uint32_t rows = min(16u, a.n - n0);
+    const rsrc_t pb = raw_buffer(a.b_codes + (uint64_t)n0 * a.pitch, rows * a.pitch);
+    const rsrc_t ps = raw_buffer(a.b_scales + (uint64_t)n0 * a.spitch, rows * a.spitch);
+    const rsrc_t qb = raw_buffer(a.a_codes, a.m * a.pitch), qs = raw_buffer(a.a_scales, a.m * a.spitch);
+    const uint32_t steps = (a.pitch + 255) / 256;
+    tf32x4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = tf32x4{0, 0, 0, 0};
+    // behind the end of a row: zeros (and scale byte 0)
+    auto code = [&](const rsrc_t& r, uint32_t row, uint32_t s, int k) {
+        const uint32_t at = s * 256 + g * 64 + k * 16;
+        return __builtin_amdgcn_raw_buffer_load_b128(r, at < a.pitch ? row * a.pitch + at : kNowhere, 0, 0);
+    };
+    auto scale = [&](const rsrc_t& r, uint32_t row, uint32_t s) {
+        const uint32_t at = s * 16 + g * 4;
+        return __builtin_amdgcn_raw_buffer_load_b32(r, at < a.spitch ? row * a.spitch + at : kNowhere, 0, 0);
+    };
+    auto wide = [](tu32x4 f) { return ti32x8{(int)f.x, (int)f.y, (int)f.z, (int)f.w, 0, 0, 0, 0}; };
+#pragma unroll 2
+    for (uint32_t s = wave; s < steps; s += WK) {
+        tu32x4 p[4], q[MT][4];
+        uint32_t sp, sq[MT];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = __builtin_bit_cast(tu32x4, code(pb, l16, s, k));
+        sp = scale(ps, l16, s);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[t][k] = __builtin_bit_cast(tu32x4, code(qb, 16 * t + l16, s, k));
+            sq[t] = scale(qs, 16 * t + l16, s);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(p[0]), wide(q[t][0]), acc[t], 4, 4, 0, (int)sp, 0, (int)sq[t]);
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(p[1]), wide(q[t][1]), acc[t], 4, 4, 1, (int)sp, 1, (int)sq[t]);
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(p[2]), wide(q[t][2]), acc[t], 4, 4, 2, (int)sp, 2, (int)sq[t]);
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(p[3]), wide(q[t][3]), acc[t], 4, 4, 3, (int)sp, 3, (int)sq[t]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+    __syncthreads();
+    if (wave < MT) {
+        // wave t finishes result tile t
+        tf32x4 x = part[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) x = x + part[w][wave][lane];
+        store_four(a, 16 * wave + l16, n0 + 4 * g, x);
+    }
 }
 
 }  // namespace
@@ -267,11 +384,34 @@ hipError_t launch_mx_dequantize(const void* codes, const void* scales, uint64_t 
 hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
                              const void* b_scales, uint64_t n, uint64_t k, void* c, int dtype,
                              uint64_t ldc, hipStream_t stream) {
-    using Core = TileCore<128, 128, 2, 2, true>;
-    const uint64_t blocks = ((m + Core::BQ - 1) / Core::BQ) * ((n + Core::BP - 1) / Core::BP);
-    product_kernel<Core><<<(uint32_t)blocks, Core::NT, 0, stream>>>(
-        (const uint8_t*)a_codes, (const uint8_t*)a_scales, (uint32_t)m, (const uint8_t*)b_codes,
-        (const uint8_t*)b_scales, (uint32_t)n, mx_shape(k), c, dtype, ldc);
+    const MxShape sh = mx_shape(k);
+    const uint64_t es = dtype == NEOX_F32 ? 4 : 2;
+    const ProductArgs a{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
+                        (const uint8_t*)b_scales, c, ldc, (uint32_t)m, (uint32_t)n, (uint32_t)sh.code_pitch,
+                        (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
+    if (m <= 64) {
+        const uint32_t blocks = (uint32_t)((n + 15) / 16);
+        auto run = [&](auto mt) {
+            constexpr int MT = decltype(mt)::value;
+            // enough waves for the chip: more of them share K where there are few rows of b
+            if (blocks >= 4 * kCUs) product_thin_kernel<MT, 4><<<blocks, 256, 0, stream>>>(a);
+            else product_thin_kernel<MT, 16><<<blocks, 1024, 0, stream>>>(a);
+        };
+        if (m <= 16) run(std::integral_constant<int, 1>{});
+        else if (m <= 32) run(std::integral_constant<int, 2>{});
+        else run(std::integral_constant<int, 4>{});
+        return hipGetLastError();
+    }
+    // us per slab of 256 elements of K, measured on the full chip: a round of 256 x 256 tiles
+    // 2.0, of quarters in the same kernel 1.0, of 128 x 128 tiles 0.63 with one block a CU and
+    // 1.25 with two
+    double c256 = 0.0;
+    uint64_t blocks = 0;
+    const TileMap map = plan_tiles(false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
+    const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
+    const double c128 = n128 <= kCUs ? 0.63 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
+    if (c256 < c128) product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
+    else product_even_kernel<Mx128><<<(uint32_t)n128, Mx128::NT, 0, stream>>>(a);
     return hipGetLastError();
 }
 

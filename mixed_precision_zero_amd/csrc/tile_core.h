@@ -252,6 +252,198 @@ struct TileCore {
 };
 
 // ------------------------------------------------------------------------------------
+// which tile a block works on
+// ------------------------------------------------------------------------------------
+// Blocks [0, nfull) take whole 256 x 256 tiles; the others take
+// quarters (128 x 128) of what is left: the tiles that would start another, mostly empty round
+// on the chip's 256 CUs, and those that the matrix's edge cuts.  Tiles of a symmetric product
+// lie on and below the diagonal, those on it last (a quarter of them above it is left out).
+struct TileMap {
+    uint32_t nfull;        // blocks with whole tiles
+    uint32_t inner;        // whole tiles per matrix
+    uint32_t edges;        // cut tiles per matrix
+    uint32_t count;        // matrices
+    uint32_t pi, qi;       // whole tiles down and across
+    uint32_t q;            // tiles across, a cut one counted
+    uint32_t mp, np;       // sides
+};
+
+// (i, j), j <= i, number t in row order of a lower triangle
+__device__ __forceinline__ void lower(uint32_t t, uint32_t& ti, uint32_t& tj) {
+    uint32_t i = (uint32_t)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    ti = i;
+    tj = t - i * (i + 1) / 2;
+}
+
+struct TileAt {
+    uint32_t z, i, j;      // matrix, first row and column
+    bool full, none;
+};
+
+template <bool SYM>
+__device__ __forceinline__ TileAt place(const TileMap& m) {
+    TileAt r{};
+    uint32_t k, quarter = 0;
+    r.full = blockIdx.x < m.nfull;
+    if (r.full) {
+        // consecutive blocks go to the eight XCDs in turn: give each XCD, and so each L2, one
+        // run of neighbouring tiles
+        const uint32_t per = m.nfull / 8;
+        k = m.nfull % 8 ? blockIdx.x : blockIdx.x % 8 * per + blockIdx.x / 8;
+    } else {
+        k = m.nfull + (blockIdx.x - m.nfull) / 4;
+        quarter = (blockIdx.x - m.nfull) % 4;
+    }
+    const uint32_t total = m.inner * m.count;
+    uint32_t ti, tj;
+    if (k < total) {
+        r.z = k / m.inner;
+        k -= r.z * m.inner;
+        if (SYM) {
+            const uint32_t below = m.pi * (m.pi - 1) / 2;
+            if (k < below) {
+                lower(k, ti, tj);
+                ++ti;
+            } else {
+                ti = tj = k - below;
+            }
+        } else {
+            // runs of eight tile rows, column by column: 64 tiles in a row share 8 + 8 panels
+            const uint32_t g = k / (8 * m.qi), rows = min(8u, m.pi - 8 * g), in = k - g * 8 * m.qi;
+            ti = 8 * g + in % rows;
+            tj = in / rows;
+        }
+    } else {
+        k -= total;
+        r.z = k / m.edges;
+        k -= r.z * m.edges;
+        if (SYM) {
+            ti = m.pi;
+            tj = k;
+        } else {
+            const uint32_t right = m.q > m.qi ? m.pi : 0;
+            ti = k < right ? k : m.pi;
+            tj = k < right ? m.qi : k - right;
+        }
+    }
+    r.i = ti * 256 + (quarter >> 1) * 128;
+    r.j = tj * 256 + (quarter & 1) * 128;
+    r.none = r.i >= m.mp || r.j >= m.np || (SYM && !r.full && r.j > r.i);
+    return r;
+}
+
+// The launch of one product with `count` p x q results (p = q and sym for symmetric ones; a
+// cut tile reads zeros behind its operands' rows), and its cost per slab of K: `full` for a
+// round of 256 x 256 tiles over the chip's CUs, `quarter` for a round of quarters.
+constexpr uint32_t kCUs = 256;
+inline TileMap plan_tiles(bool sym, uint32_t p, uint32_t q, uint32_t count, double full, double quarter,
+                          double* cost, uint64_t* blocks) {
+    TileMap m{};
+    m.count = count;
+    m.pi = p / 256;
+    m.qi = q / 256;
+    m.q = (q + 255) / 256;
+    m.mp = p;
+    m.np = q;
+    const bool cut_p = p % 256 != 0, cut_q = q % 256 != 0;
+    if (sym) {
+        m.inner = m.pi * (m.pi + 1) / 2;
+        m.edges = cut_p ? m.pi + 1 : 0;
+    } else {
+        m.inner = m.pi * m.qi;
+        m.edges = (cut_q ? m.pi : 0) + (cut_p ? m.q : 0);
+    }
+    const uint64_t total = (uint64_t)m.inner * count, cut = (uint64_t)m.edges * count;
+    auto takes = [&](uint64_t n) {
+        const uint64_t quarters = 4 * (total - n + cut);
+        return full * (double)((n + kCUs - 1) / kCUs) + quarter * (double)((quarters + kCUs - 1) / kCUs);
+    };
+    const uint64_t whole = total / kCUs * kCUs;
+    const uint64_t n = takes(total) <= takes(whole) ? total : whole;
+    m.nfull = (uint32_t)n;
+    *cost = takes(n);
+    *blocks = n + 4 * (total - n + cut);
+    return m;
+}
+
+// ------------------------------------------------------------------------------------
+// results on their way to memory
+// ------------------------------------------------------------------------------------
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+// ROWS x COLS FP16 elements of a row-major array in a wave's own part of LDS, on their way
+// between its result tiles and memory: a lane's four elements are 8 bytes of 16 different rows
+// an instruction, which memory serves at half the rate of whole rows, so rows of COLS elements
+// (64 or 128 bytes) are moved 16 bytes a lane instead.  The 16-byte chunks of a row are
+// permuted by its number so that 16 rows at one column fall on different banks.  Only the wave
+// that owns the part uses it, and its LDS operations execute in order: no barrier is needed.
+template <int ROWS, int COLS>
+struct Patch {
+    static constexpr int kRow = COLS * 2, kChunks = kRow / 16, kBytes = ROWS * kRow;
+    static constexpr int kPass = kBytes / 1024;          // 64 lanes of 16 bytes
+    static_assert((kRow == 64 || kRow == 128) && kBytes % 1024 == 0, "");
+    static __device__ __forceinline__ uint32_t turn(uint32_t row) { return (row >> (kRow == 128 ? 1 : 2)) & (kChunks - 1); }
+    // four elements at (row, col), col a multiple of 4
+    static __device__ __forceinline__ f16x4* at(uint8_t* l, uint32_t row, uint32_t col) {
+        return (f16x4*)(l + row * kRow + (((col >> 3) ^ turn(row)) << 4) + (col & 4) * 2);
+    }
+    // starts loading from g (row r at r * ld); wave_wait() before it is used
+    static __device__ __forceinline__ void load(uint8_t* l, const uint16_t* g, uint32_t ld) {
+        const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+        for (int k = 0; k < kPass; ++k) {
+            const uint32_t row = (k * 64 + lane) / kChunks, c = (lane % kChunks) ^ turn(row);
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(g + (uint64_t)row * ld + c * 8),
+                (__attribute__((address_space(3))) void*)(l + k * 1024), 16, 0, 0);
+        }
+    }
+    // rows [0, left) to g
+    static __device__ __forceinline__ void store(const uint8_t* l, uint16_t* g, uint64_t ld, uint32_t left = ROWS) {
+        const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+        for (int k = 0; k < kPass; ++k) {
+            const uint32_t row = (k * 64 + lane) / kChunks, c = (lane % kChunks) ^ turn(row);
+            if (row < left) *(tu32x4*)(g + (uint64_t)row * ld + c * 8) = *(const tu32x4*)(l + (k * 64 + lane) * 16);
+        }
+    }
+};
+// All of this wave's memory operations so far are done.
+__device__ __forceinline__ void wave_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);         // vmcnt(0) lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A wave's results of a block tile, worked on in pieces of 16 kU x 16 TQ elements.
+template <class Core>
+struct Piece {
+    static constexpr int kU = Core::TP < 4 ? Core::TP : 4, kV = Core::TQ;
+    using Down = Patch<16 * kV, 16 * kU>;       // rows are D's columns: an array [j][i]
+    using Across = Patch<16 * kU, 16 * kV>;     // rows are D's rows: [i][j]
+    static constexpr int kBytes = Down::kBytes;
+    static_assert(2 * kBytes <= Core::kLds / (Core::NT / 64), "two patches per wave");
+    uint32_t i, j;         // first row and column in the matrix
+    uint32_t li, lj;       // this lane's first row and its column within 16 x 16
+    uint8_t *l0, *l1;      // LDS of two patches
+    __device__ Piece(const TileAt& t, int u0, uint8_t* lds) {
+        const uint32_t lane = threadIdx.x & 63;
+        i = t.i + Core::wave_p() + 16 * u0;
+        j = t.j + Core::wave_q();
+        li = (lane >> 4) * 4;
+        lj = lane & 15;
+        l0 = lds + (threadIdx.x >> 6) * (Core::kLds / (Core::NT / 64));
+        l1 = l0 + kBytes;
+    }
+    // The places of tile (u, v)'s elements of this lane, and of their transposes, in a patch.
+    __device__ __forceinline__ f16x4* down(uint8_t* l, int u, int v) const { return Down::at(l, 16 * v + lj, 16 * u + li); }
+    __device__ __forceinline__ f16x4* across(uint8_t* l, int u, int v) const { return Across::at(l, 16 * u + lj, 16 * v + li); }
+};
+
+// ------------------------------------------------------------------------------------
 // element types
 // ------------------------------------------------------------------------------------
 __device__ __forceinline__ float opaque(float x) {

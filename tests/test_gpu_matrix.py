@@ -112,12 +112,15 @@ def test_orthogonalize_zero_and_non_finite():
     assert torch.isnan(M.orthogonalize(one)).all()
 
 
-def test_orthogonalize_large():
-    """More than one wave of tiles, checked by what the polynomial does to singular values:
-    the Gram matrix of the result is p(S)^2, so X X' applied to random vectors agrees."""
-    x = rand((1500, 2900), 51, BF16)
+@pytest.mark.parametrize("rows,cols", [(1500, 2900), (4200, 4400), (5000, 1030), (2304, 2304)])
+def test_orthogonalize_large(rows, cols):
+    """Many tiles of every kind (whole ones, quarters, cut by the edge), against 64 bits on the
+    GPU."""
+    x = rand((rows, cols), 51, BF16)
     got = M.orthogonalize(x, dtype=F32).double()
     g = x.double()
+    if rows > cols:
+        g, got = g.t().contiguous(), got.t()
     g = g / (torch.linalg.vector_norm(g) + 1e-7)
     for a, b, c in R.COEF:
         p = g @ g.t().contiguous()
@@ -212,6 +215,25 @@ def test_dequantize_bits(dtype, rows, cols):
     assert (buf[:, cols:] == 3.0).all()
 
 
+def test_copies_beyond_32_bit_offsets():
+    """A matrix of more than 2^32 elements, by its first and last rows."""
+    rows, cols = 33_000, 131_200
+    x = torch.empty(rows, cols, dtype=F16, device=DEV)
+    x.view(-1)[:1 << 20] = rand((1 << 20,), 1, F16)
+    x[-40:] = rand((40, cols), 2, F16)
+    q = M.mxfp4_quantize(x)
+    back = M.mxfp4_dequantize(q, F16)
+    codes, scales = R.mx_quantize(x[-40:])
+    assert torch.equal(q.codes[-40:].cpu(), codes) and torch.equal(q.scales[-40:].cpu(), scales)
+    assert torch.equal(back[-40:].cpu(), R.mx_values(codes, scales, cols).to(F16))
+    del back
+    t = M.mxfp4_quantize(x, transpose=True)
+    assert torch.equal(t.scales[:, rows // 32].cpu(), R.mx_quantize(x[rows // 32 * 32:].t())[1][:, 0])
+    y = M.mxfp4_product(M.MXFP4(q.codes[-40:], q.scales[-40:], 40, cols), M.MXFP4(q.codes[-9:], q.scales[-9:], 9, cols), F32)
+    a = R.mx_values(q.codes[-40:], q.scales[-40:], cols)
+    assert ((y.double().cpu() - a @ a[-9:].t()).abs() <= product_bound(a, a[-9:], cols)).all()
+
+
 def test_quantize_leaves_what_is_behind():
     x = rand((13, 100), 3)
     nc, ns = M.neox_mxfp4_layout(13, 100)
@@ -252,7 +274,8 @@ def test_product(dtype, m, n, k):
     assert (err <= tol).all(), float((err / tol).max())
 
 
-@pytest.mark.parametrize("m,n,k", [(5, 40, 96), (64, 200, 256), (150, 260, 4000)])
+@pytest.mark.parametrize("m,n,k", [(5, 40, 96), (16, 5000, 1500), (31, 16500, 600), (64, 200, 256), (150, 260, 4000),
+                                   (4200, 4300, 200), (2500, 9000, 130), (700, 700, 64)])
 def test_product_is_exact_on_small_integers(m, n, k):
     """Values of {0, +-1, +-2, +-4} at scales that make every sum an integer below 2^24 have
     one right answer."""
