@@ -44,15 +44,17 @@ double poly_top(double a, double b, double c, double top) {
     return best;
 }
 
-// Validates the steps and rounds the coefficients; fills coef[steps].
-int ns_coefs(const neox_ns_config* c, NsCoef* coef) {
+// Validates the steps and rounds the coefficients; fills coef[steps].  *pairs: the product of
+// two consecutive steps' polynomials fits FP16 too.
+int ns_coefs(const neox_ns_config* c, NsCoef* coef, bool* pairs) {
     if (!c) return set_error(NEOX_EINVAL, "the Newton-Schulz configuration is NULL");
     if (c->steps < 1 || c->steps > NEOX_NS_MAX_STEPS)
         return set_error(NEOX_EINVAL, "steps %d not in [1, %d]", c->steps, NEOX_NS_MAX_STEPS);
     if (c->reserved) return set_error(NEOX_EINVAL, "reserved field %d is not 0", c->reserved);
     if (!(std::isfinite(c->eps) && (float)c->eps > 0.0f && std::isfinite((float)c->eps)))
         return set_error(NEOX_EINVAL, "eps %g: must be > 0 in FP32", c->eps);
-    double top = 1.0;
+    double top = 1.0, before = 0.0;
+    *pairs = true;
     for (int k = 0; k < c->steps; ++k) {
         const double a = c->coef[k][0], b = c->coef[k][1], d = c->coef[k][2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(d))
@@ -60,6 +62,9 @@ int ns_coefs(const neox_ns_config* c, NsCoef* coef) {
         // what the FP16 copies hold: elements of A up to top^2, of b A + c A A up to this
         if (std::fabs(b) * top * top + std::fabs(d) * top * top * top * top > 30000.0)
             return set_error(NEOX_EINVAL, "step %d: coefficients (%g, %g, %g) too large", k, a, b, d);
+        const double size = std::fabs(a) + std::fabs(b) * top * top + std::fabs(d) * top * top * top * top;
+        if (size * std::max(before, 1.0) > 30000.0) *pairs = false;
+        before = size;
         top = 1.01 * poly_top(a, b, d, top);
         if (top > 8.0)
             return set_error(NEOX_EINVAL, "step %d: singular values grow to %g", k, top);
@@ -108,7 +113,8 @@ extern "C" int neox_orthogonalize_workspace(uint64_t count, uint64_t rows, uint6
     if (rc) return rc;
     if (count == 0 || count > kMaxCount)
         return set_error(NEOX_EINVAL, "count %llu not in [1, 2^24]", (unsigned long long)count);
-    const NsShape s = ns_shape(rows, cols);
+    // as with two steps at a time, which needs more, whatever the coefficients will be
+    const NsShape s = ns_shape(rows, cols, true);
     *bytes = ns_bytes(s, std::min(count, launch_count(s)));
     return NEOX_OK;
 }
@@ -119,7 +125,8 @@ extern "C" int neox_orthogonalize(const neox_ns_config* cfg, const void* src, in
                                   uint64_t cols, double scale, void* workspace, uint64_t workspace_bytes,
                                   void* hip_stream) {
     NsCoef coef[NEOX_NS_MAX_STEPS];
-    int rc = ns_coefs(cfg, coef);
+    bool pairs = false;
+    int rc = ns_coefs(cfg, coef, &pairs);
     if (rc) return rc;
     uint64_t need = 0;
     rc = neox_orthogonalize_workspace(count, rows, cols, &need);
@@ -151,7 +158,7 @@ extern "C" int neox_orthogonalize(const neox_ns_config* cfg, const void* src, in
     if (!std::isfinite(scale) || !std::isfinite((float)scale))
         return set_error(NEOX_EINVAL, "scale %g is not finite", scale);
 
-    const NsShape s = ns_shape(rows, cols);
+    const NsShape s = ns_shape(rows, cols, pairs);
     const uint64_t most = std::min(count, launch_count(s));
     const NsBuf w = ns_place(s, most, workspace);
     for (uint64_t z = 0; z < count; z += most) {
@@ -281,7 +288,8 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
         neox_muon* h;
         ~Guard() { free_muon(h); }
     } guard{h};
-    int rc = ns_coefs(&mcfg->ns, h->coef);
+    bool pairs = false;
+    int rc = ns_coefs(&mcfg->ns, h->coef, &pairs);
     if (rc) return rc;
 
     Plan plan;
@@ -309,7 +317,7 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
         for (uint64_t i = 0; i < n; ++i) by[{mats[i].rows, mats[i].cols}].push_back(i);
         const uint64_t cap = mcfg->workspace_bytes ? mcfg->workspace_bytes : kDefaultWorkspace;
         for (const auto& kv : by) {
-            const NsShape s = ns_shape(kv.first.first, kv.first.second);
+            const NsShape s = ns_shape(kv.first.first, kv.first.second, pairs);
             uint64_t most = std::min<uint64_t>(kv.second.size(), launch_count(s));
             most = std::max<uint64_t>(1, std::min<uint64_t>(most, cap / ns_bytes(s, 1)));
             while (most > 1 && ns_bytes(s, most) > cap) --most;

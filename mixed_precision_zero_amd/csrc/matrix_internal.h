@@ -19,10 +19,8 @@ struct NsBuf {
     uint16_t* xh;      // [mp][np] FP16: the iterate, times S, first 11 bits
     uint16_t* xt[2];   // [np][mp] FP16: its transpose (read / written in turn)
     uint16_t* lt;      // [np][mp] FP16: what xh leaves, times 2^11, transposed
-    uint16_t* a;       // [mp][mp] FP16: X X^T without its diagonal
-    uint16_t* b;       // [mp][mp] FP16: b A + c A A without its diagonal
-    float* da;         // [mp] diagonal of A
-    float* db;         // [mp] diagonal of b A + c A A
+    uint16_t* sym[3];  // [mp][mp] FP16: X X^T and polynomials of it, without their diagonals
+    float* diag[3];    // [mp] the diagonals (the third pair with `pairs` only)
     double* part;      // [kNsParts] partial squared norms of the source
 };
 
@@ -32,9 +30,12 @@ struct NsShape {
     uint32_t mp, np;       // padded
     uint32_t parts;        // partial sums per matrix
     bool tall;             // the wide form is the source's transpose
+    bool small;            // one block does it all, without the buffers
+    bool pairs;            // the iterate is updated once for two steps
     float s;               // S, a power of two: the iterate is stored times S
 };
-NsShape ns_shape(uint64_t rows, uint64_t cols);
+// pairs: whether the coefficients allow two steps at a time (FP16 range).
+NsShape ns_shape(uint64_t rows, uint64_t cols, bool pairs);
 // Bytes of the buffers of `count` matrices, and their placement at base.
 uint64_t ns_bytes(const NsShape& s, uint64_t count);
 NsBuf ns_place(const NsShape& s, uint64_t count, void* base);

@@ -2,20 +2,27 @@
 //
 // For each step, with X m x n (m <= n):
 //   gram   A = X X^T                       symmetric: tiles on and below the diagonal only
-//   poly   B = b A + c A A                 symmetric, as A is (A A = A A^T)
-//   apply  X <- a X + B X
+//   sym    P = a I + b A + c A A           symmetric, as A is (A A = A A^T)
+//   apply  X <- P X
 // All three are products of rows with rows once X is kept in both orientations, so they
 // share one tile core.
+//
+// Two steps at a time.  The next A is P A P, without X; so with n >= 2 m two steps go into one
+// X <- (P' P) X at the cost of three more m x m products (they commute and are symmetric: half
+// their tiles): 8.5 units of m^3 instead of 13 at n = 4 m, and X is read and written half as
+// often.  Not more than two: an error of FP16's size in the part of A that belongs to tiny
+// singular values grows by a^2 (12) a step, harmless once (1e-3 of a), not twice.
 //
 // Precision.  Products read FP16.  Rounding the iterate itself to FP16 in each step would
 // put noise into the directions whose singular values are still tiny, and a later step
 // multiplies those by up to a (3.4 per step, ~500 in five): a rank-1 matrix came out 15%
-// off.  So X is carried as two FP16 numbers (22 bits), and only the products B X and X X^T
-// see the first alone: their error is filtered through B or X once more and stays at the
-// FP16 level.  A and B have diagonals far larger than the rest (of similar size along the
+// off.  So X is carried as two FP16 numbers (22 bits), and only the products P X and X X^T
+// see the first alone: their error is filtered through P or X once more and stays at the
+// FP16 level.  A and P have diagonals far larger than the rest (of similar size along the
 // diagonal too, so that their roundings would add up in one direction): the diagonals are
 // kept in FP32, apart, and FP16 holds the rest.  Simulated against 64 bits on Gaussian,
-// decaying and low-rank spectra: 2e-4 .. 1e-3 of the result's norm.
+// decaying and low-rank spectra, 256 rows and more: 2e-4 .. 2e-3 of the result's norm, the
+// larger ones with two steps at a time or rank 1 (64 rows: up to 5e-3 at rank 1).
 #include "matrix_internal.h"
 #include "tile_core.h"
 
@@ -269,12 +276,19 @@ __device__ __forceinline__ TileAt place_even(uint32_t mp, uint32_t np) {
     }
     r.i = ti * Core::BP;
     r.j = tj * Core::BQ;
+    r.settle();
     return r;
 }
 
 __device__ __forceinline__ TileRows rows_of(const uint16_t* base, uint64_t row, uint32_t len, int block) {
     return TileRows{(const uint8_t*)(base + row * len), nullptr, (uint32_t)block, len * 2u, 0u};
 }
+
+// A symmetric matrix: FP16 without its diagonal, and the diagonal.
+struct SymBuf {
+    uint16_t* a;
+    float* d;
+};
 
 // A lane of a 16 x 16 result tile holds four consecutive rows of one column.  These are the
 // elements of the same tile that are four consecutive columns of one row (row lane % 16,
@@ -292,24 +306,26 @@ __device__ __forceinline__ f16x4 pack4(tf32x4 v) {
 }
 
 // An FP16 result on and below the diagonal, to both sides of it, without the diagonal; the
-// diagonal to d.
-template <class Core>
-__device__ __forceinline__ void store_sym(const TileAt& t, const Piece<Core>& p, tf32x4 (&x)[Piece<Core>::kU][Core::TQ],
-                                          uint16_t* out, uint32_t ld, float* d) {
+// diagonal, and more(i) added to it, to d.
+template <class Core, class More>
+__device__ __forceinline__ void store_sym(const TileAt& t, const Piece<Core>& p, tf32x4 (&acc)[Core::TP][Core::TQ],
+                                          int u0, uint16_t* out, uint32_t ld, float* d, More more) {
     using P = Piece<Core>;
 #pragma unroll
     for (int u = 0; u < P::kU; ++u)
 #pragma unroll
         for (int v = 0; v < P::kV; ++v) {
+            tf32x4& x = acc[u0 + u][v];
             if (t.i == t.j) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (p.i + 16 * u + p.li + e == p.j + 16 * v + p.lj) {
-                        d[p.j + 16 * v + p.lj] = x[u][v][e];
-                        x[u][v][e] = 0.0f;
+                        const uint32_t j = p.j + 16 * v + p.lj;
+                        d[j] = x[e] + more(j);
+                        x[e] = 0.0f;
                     }
             }
-            const f16x4 h = pack4(x[u][v]);
+            const f16x4 h = pack4(x);
             *p.down(p.l0, u, v) = h;
             *p.across(p.l1, u, v) = pack4(transposed(h));
         }
@@ -320,96 +336,104 @@ __device__ __forceinline__ void store_sym(const TileAt& t, const Piece<Core>& p,
 // A = X X^T
 struct Gram {
     static constexpr bool SYM = true;
-    NsBuf w;
+    const uint16_t* xh;
+    SymBuf out;
     uint32_t mp, np;
     float inv_s2;
     template <class Core>
     __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
         using P = Piece<Core>;
-        const uint16_t* x = w.xh + (uint64_t)at.z * mp * np;
+        const uint16_t* x = xh + (uint64_t)at.z * mp * np;
         Core t;
         t.run(rows_of(x, at.i, np, Core::BP), rows_of(x, at.j, np, Core::BQ), np * 2, lds);
-        uint16_t* a = w.a + (uint64_t)at.z * mp * mp;
-        float* da = w.da + (uint64_t)at.z * mp;
 #pragma unroll
         for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
-            tf32x4 x[P::kU][Core::TQ];
 #pragma unroll
             for (int u = 0; u < P::kU; ++u)
 #pragma unroll
-                for (int v = 0; v < P::kV; ++v) x[u][v] = t.acc[u0 + u][v] * inv_s2;
-            store_sym<Core>(at, P(at, u0, lds), x, a, mp, da);
+                for (int v = 0; v < P::kV; ++v) t.acc[u0 + u][v] = t.acc[u0 + u][v] * inv_s2;
+            store_sym<Core>(at, P(at, u0, lds), t.acc, u0, out.a + (uint64_t)at.z * mp * mp, mp,
+                            out.d + (uint64_t)at.z * mp, [](uint32_t) { return 0.0f; });
         }
     }
 };
 
-// B = b A + c A A.  A = O + D: A A = O O + (D_i + D_j) O_ij, and D_i^2 on the diagonal, where
-// O is 0.
-struct Poly {
+// Products of symmetric buffers: R = ka I + kb L + kc L L (SAME), or R = L M for L and M that
+// commute.  With L = O + D, M = N + E (diagonals apart): L M = O N + D_i N_ij + O_ij E_j, and
+// D_i E_i on the diagonal, where O and N are 0.
+template <bool SAME>
+struct Sym {
     static constexpr bool SYM = true;
-    NsBuf w;
+    SymBuf l, m, r;
     uint32_t mp, np;
-    float kb, kc;
+    float ka, kb, kc;
     template <class Core>
     __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
         using P = Piece<Core>;
-        const uint16_t* a = w.a + (uint64_t)at.z * mp * mp;
-        const float* da = w.da + (uint64_t)at.z * mp;
+        const uint64_t sz = (uint64_t)at.z * mp * mp, dz = (uint64_t)at.z * mp;
+        const uint16_t *lo = l.a + sz, *mo = SAME ? lo : m.a + sz;
+        const float *ld = l.d + dz, *md = SAME ? ld : m.d + dz;
         Core t;
-        t.run(rows_of(a, at.i, mp, Core::BP), rows_of(a, at.j, mp, Core::BQ), mp * 2, lds);
-        uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
-        float* db = w.db + (uint64_t)at.z * mp;
+        t.run(rows_of(lo, at.i, mp, Core::BP), rows_of(mo, at.j, mp, Core::BQ), mp * 2, lds);
 #pragma unroll
         for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
             const P p(at, u0, lds);
-            P::Down::load(p.l0, a + (uint64_t)p.j * mp + p.i, mp);
+            P::Down::load(p.l0, lo + (uint64_t)p.j * mp + p.i, mp);
+            if (!SAME) P::Down::load(p.l1, mo + (uint64_t)p.j * mp + p.i, mp);
             wave_wait();
-            tf32x4 x[P::kU][Core::TQ];
 #pragma unroll
             for (int u = 0; u < P::kU; ++u) {
-                const tf32x4 di = *(const tf32x4*)(da + p.i + 16 * u + p.li);
+                const tf32x4 di = *(const tf32x4*)(ld + p.i + 16 * u + p.li);
 #pragma unroll
                 for (int v = 0; v < P::kV; ++v) {
-                    const float dj = da[p.j + 16 * v + p.lj];
+                    const float ej = md[p.j + 16 * v + p.lj];
                     const f16x4 o = *p.down(p.l0, u, v);
+                    tf32x4& y = t.acc[u0 + u][v];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const bool diag = p.i + 16 * u + p.li + e == p.j + 16 * v + p.lj;
-                        const float off = (float)o[e];
-                        float sq = __builtin_fmaf(di[e] + dj, off, t.acc[u0 + u][v][e]);
-                        if (diag) sq = __builtin_fmaf(dj, dj, sq);
-                        x[u][v][e] = __builtin_fmaf(kc, sq, kb * (diag ? dj : off));
+                        const float oe = (float)o[e];
+                        y[e] = SAME ? __builtin_fmaf(kc, __builtin_fmaf(di[e] + ej, oe, y[e]), kb * oe)
+                                    : __builtin_fmaf(ej, oe, y[e]);
+                    }
+                    if (!SAME) {
+                        const f16x4 n = *p.down(p.l1, u, v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(di[e], (float)n[e], y[e]);
                     }
                 }
             }
-            store_sym<Core>(at, p, x, b, mp, db);
+            store_sym<Core>(at, p, t.acc, u0, r.a + sz, mp, r.d + dz, [&](uint32_t i) {
+                const float d = ld[i], dd = d * md[i];
+                return SAME ? __builtin_fmaf(kc, dd, __builtin_fmaf(kb, d, ka)) : dd;
+            });
             if (u0 + P::kU < Core::TP) wave_wait();      // the next load overwrites the patches
         }
     }
 };
 
-// X <- a X + B X, to the buffers of the next step
+// X <- B X, B in a symmetric buffer, to the iterate's buffers of the next step.  B's diagonal
+// meets both halves of X, the rest of it the first.
 struct Apply {
     static constexpr bool SYM = false;
-    NsBuf w;
+    SymBuf by;
+    const uint16_t* xin;       // X^T before
+    uint16_t *xout, *xrow, *rest;   // X^T after, X, X^T's second half
     uint32_t mp, np;
-    float ka;
-    int from;
     template <class Core>
     __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
         using P = Piece<Core>;
         const uint64_t xz = (uint64_t)at.z * mp * np;
-        const uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
-        const uint16_t* xt = w.xt[from] + xz;
+        const uint16_t* b = by.a + (uint64_t)at.z * mp * mp;
+        const uint16_t* xt = xin + xz;
         Core t;
         t.run(rows_of(b, at.i, mp, Core::BP), rows_of(xt, at.j, mp, Core::BQ), mp * 2, lds);
-        const float* db = w.db + (uint64_t)at.z * mp;
+        const float* db = by.d + (uint64_t)at.z * mp;
 #pragma unroll
         for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
             const P p(at, u0, lds);
             const uint64_t down = xz + (uint64_t)p.j * mp + p.i;
-            P::Down::load(p.l0, w.xt[from] + down, mp);
-            P::Down::load(p.l1, w.lt + down, mp);
+            P::Down::load(p.l0, xin + down, mp);
+            P::Down::load(p.l1, rest + down, mp);
             wave_wait();
 #pragma unroll
             for (int u = 0; u < P::kU; ++u) {
@@ -421,7 +445,7 @@ struct Apply {
                     tf32x4& y = t.acc[u0 + u][v];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[e] = __builtin_fmaf(ka + d[e], __builtin_fmaf((float)o[e], 1.0f / kLo, (float)h[e]), y[e]);
+                        y[e] = __builtin_fmaf(d[e], __builtin_fmaf((float)o[e], 1.0f / kLo, (float)h[e]), y[e]);
                     const f16x4 nh = pack4(y);
                     f16x4 nl;
 #pragma unroll
@@ -430,13 +454,13 @@ struct Apply {
                     *pl = nl;
                 }
             }
-            P::Down::store(p.l0, w.xt[from ^ 1] + down, mp);
-            P::Down::store(p.l1, w.lt + down, mp);
+            P::Down::store(p.l0, xout + down, mp);
+            P::Down::store(p.l1, rest + down, mp);
 #pragma unroll
             for (int u = 0; u < P::kU; ++u)
 #pragma unroll
                 for (int v = 0; v < P::kV; ++v) *p.across(p.l0, u, v) = pack4(transposed(pack4(t.acc[u0 + u][v])));
-            P::Across::store(p.l0, w.xh + xz + (uint64_t)p.i * np + p.j, np);
+            P::Across::store(p.l0, xrow + xz + (uint64_t)p.i * np + p.j, np);
             if (u0 + P::kU < Core::TP) wave_wait();
         }
     }
@@ -506,19 +530,19 @@ template <class IO, class Dst, bool TALL>
 struct Last {
     static constexpr bool SYM = false;
     IO io;
-    NsBuf w;
+    SymBuf by;
+    const uint16_t *xin, *xrow, *rest;
     NsShape s;
-    float ka, inv_s;
-    int from;
+    float inv_s;
     template <class Core>
     __device__ __forceinline__ void tile(const TileAt& at, uint8_t* lds) const {
         const uint32_t mp = s.mp, np = s.np;
         const uint64_t xz = (uint64_t)at.z * mp * np;
-        const uint16_t* b = w.b + (uint64_t)at.z * mp * mp;
-        const uint16_t* xt = w.xt[from] + xz;
-        const uint16_t* xh = w.xh + xz;
-        const uint16_t* lt = w.lt + xz;
-        const float* db = w.db + (uint64_t)at.z * mp;
+        const uint16_t* b = by.a + (uint64_t)at.z * mp * mp;
+        const uint16_t* xt = xin + xz;
+        const uint16_t* xh = xrow + xz;
+        const uint16_t* lt = rest + xz;
+        const float* db = by.d + (uint64_t)at.z * mp;
         const TileRows br = rows_of(b, TALL ? at.i : at.j, mp, TALL ? Core::BP : Core::BQ);
         const TileRows xr = rows_of(xt, TALL ? at.j : at.i, mp, TALL ? Core::BQ : Core::BP);
         Core t;
@@ -557,7 +581,7 @@ struct Last {
                     tf32x4 y;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[e] = __builtin_fmaf(ka + (TALL ? di[e] : dj), __builtin_fmaf(o[e], 1.0f / kLo, (float)h[e]),
+                        y[e] = __builtin_fmaf(TALL ? di[e] : dj, __builtin_fmaf(o[e], 1.0f / kLo, (float)h[e]),
                                               t.acc[u0 + u][v][e]);
                     const uint32_t rows = TALL ? s.n : s.m, cols = TALL ? s.m : s.n;
                     if (j < rows && i < cols) dst.store(j, i, min(4u, cols - i), y);
@@ -573,13 +597,14 @@ using Core128w = TileCore<128, 128, 2, 4, false>;      // quarters, by the same 
 using Core128 = TileCore<128, 128, 2, 2, false>;
 using Core64 = TileCore<64, 64, 2, 2, false, 4>;
 
-template <class Op>
-__global__ __launch_bounds__(512, 2) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
+template <class Op, class Full, class Quarter>
+__global__ __launch_bounds__(Full::NT, 2) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
+    static_assert(Full::NT == Quarter::NT && Full::kLds >= Quarter::kLds && Full::BP == 2 * Quarter::BP, "");
     if (skipped(st)) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Core256::kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Full::kLds];
     const TileAt at = place<Op::SYM>(m);
-    if (at.full) op.template tile<Core256>(at, lds);
-    else if (!at.none) op.template tile<Core128w>(at, lds);
+    if (at.full) op.template tile<Full>(at, lds);
+    else if (!at.none) op.template tile<Quarter>(at, lds);
 }
 template <class Op, class Core>
 __global__ __launch_bounds__(Core::NT) void ns_even_kernel(Op op, const DevState* st, uint32_t mp, uint32_t np) {
@@ -589,40 +614,272 @@ __global__ __launch_bounds__(Core::NT) void ns_even_kernel(Op op, const DevState
 }
 
 // ------------------------------------------------------------------------------------
+// Small matrices: everything in one launch, one block per matrix
+//
+// Up to 128 x 128 (or 64 x 256) the iterate in both orientations, A and B fit one CU's LDS and
+// the iterate itself, in FP32, the block's registers.  The fifteen launches of the tiled form
+// would each wait for the one before (66 us for 64 matrices of 64 x 64; here one launch).
+// ------------------------------------------------------------------------------------
+struct NsSteps {
+    int32_t n;
+    NsCoef c[NEOX_NS_MAX_STEPS];
+};
+
+// Rows of B bytes in LDS, their 16-byte chunks permuted by the row's number.
+template <int B>
+__device__ __forceinline__ uint8_t* chunk_at(uint8_t* base, uint32_t row, uint32_t chunk) {
+    return base + row * B + ((chunk ^ (row & 7)) << 4);
+}
+// the place of elements (row, col .. col + 3)
+template <int B>
+__device__ __forceinline__ f16x4* quad_at(uint8_t* base, uint32_t row, uint32_t col) {
+    return (f16x4*)(chunk_at<B>(base, row, col >> 3) + (col & 4) * 2);
+}
+
+// acc += P Q^T over rows of B bytes
+template <int TP, int TQ, int B>
+__device__ __forceinline__ void lds_product(tf32x4 (&acc)[TP][TQ], uint8_t* p, uint32_t prow, uint8_t* q, uint32_t qrow) {
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < TP; ++u)
+#pragma unroll
+        for (int v = 0; v < TQ; ++v) acc[u][v] = tf32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < B / 64; ++k) {
+        tf16x8 a[TP], b[TQ];
+#pragma unroll
+        for (int u = 0; u < TP; ++u) a[u] = *(const tf16x8*)chunk_at<B>(p, prow + 16 * u + l16, 4 * k + g);
+#pragma unroll
+        for (int v = 0; v < TQ; ++v) b[v] = *(const tf16x8*)chunk_at<B>(q, qrow + 16 * v + l16, 4 * k + g);
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+            for (int v = 0; v < TQ; ++v) acc[u][v] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[u], b[v], acc[u][v], 0, 0, 0);
+    }
+}
+
+// The source's elements (r, c .. c + n - 1), n <= 4; Muon's momentum is updated on the way.
+struct OrthIn {
+    OrthSrc src;
+    __device__ OrthIn(const OrthIO& io, const NsShape& s, uint32_t z) : src(io, s, z) {}
+    __device__ tf32x4 get(uint32_t r, uint32_t c, uint32_t n, uint32_t cols) const {
+        if (src.vec) return src.load4(r, c, cols);
+        tf32x4 x = {0, 0, 0, 0};
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            if (e < n) x[e] = src.load(r, c + e, cols);
+        return x;
+    }
+};
+struct MuonIn {
+    MuonSrc src;
+    __device__ MuonIn(const MuonIO& io, const NsShape& s, uint32_t z) : src(io, s, z) {}
+    __device__ tf32x4 get(uint32_t r, uint32_t c, uint32_t n, uint32_t cols) const {
+        const uint64_t at = (uint64_t)r * cols + c;
+        tf32x4 x = {0, 0, 0, 0};
+        if (src.vec) {
+            const tf32x4 g = halves4(src.io.dtype, *(const uint2*)(src.mat.grad + at));
+            tf32x4 m = *(const tf32x4*)(src.mat.mom + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                m[e] = __builtin_fmaf(src.io.mu, m[e], g[e] * src.gs);
+                x[e] = direction(src.io, g[e] * src.gs, m[e]);
+            }
+            *(tf32x4*)(src.mat.mom + at) = m;
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+                if (e < n) {
+                    const float g = half_to_float(src.io.dtype, src.mat.grad[at + e]) * src.gs;
+                    const float m = __builtin_fmaf(src.io.mu, src.mat.mom[at + e], g);
+                    src.mat.mom[at + e] = m;
+                    x[e] = direction(src.io, g, m);
+                }
+        }
+        return x;
+    }
+};
+
+template <class IO, class In, class Dst, int MP, int NP, int WP, int WQ>
+__global__ __launch_bounds__(WP * WQ * 64) void ns_small_kernel(IO io, NsShape s, NsSteps steps) {
+    if (skipped(state_of(io))) return;
+    constexpr int NT = WP * WQ * 64;
+    constexpr int XB = NP * 2, TB = MP * 2;            // bytes of a row of X, and of X^T, A and B
+    constexpr int kX = MP * XB, kA = MP * TB;
+    constexpr int PF = NP + 1;                         // floats of a row of the FP32 buffer
+    constexpr int kF = MP * PF * 4 > 2 * kA ? MP * PF * 4 : 2 * kA;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kX + kF + 2 * MP * 4];
+    uint8_t *xh = lds, *xt = lds + kX, *la = lds + 2 * kX, *lb = la + kA;
+    float* f32 = (float*)la;                           // source and result, in A's and B's place
+    float *da = (float*)(lds + 2 * kX + kF), *db = da + MP;
+    const uint32_t z = blockIdx.x, tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+
+    // the source into LDS in its wide form, its norm on the way
+    const In in(io, s, z);
+    const uint32_t w4 = (s.cols + 3) / 4;
+    double sq = 0.0;
+    for (uint32_t k = tid; k < s.rows * w4; k += NT) {
+        const uint32_t r = k / w4, c = (k - r * w4) * 4, n = min(4u, s.cols - c);
+        const tf32x4 x = in.get(r, c, n, s.cols);
+        sq = square4(x, sq);
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            if (e < n) f32[s.tall ? (c + e) * PF + r : r * PF + c + e] = x[e];
+    }
+    sq = sum_block<NT>(sq);                            // (a barrier)
+    const double f = (double)s.s / (__builtin_sqrt(sq) + io.eps);
+
+    // X: this wave's part, four rows of a column a lane as everywhere
+    constexpr int TP = MP / WP / 16, TQ = NP / WQ / 16, SQ = MP / WQ / 16;
+    const uint32_t wave = tid >> 6;
+    const uint32_t pi = wave / WQ * (MP / WP), qj = wave % WQ * (NP / WQ), qs = wave % WQ * (MP / WQ);
+    tf32x4 x[TP][TQ];
+    auto spread_x = [&]() {
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+            for (int v = 0; v < TQ; ++v) {
+                const f16x4 h = pack4(x[u][v]);
+                *quad_at<TB>(xt, qj + 16 * v + l16, pi + 16 * u + 4 * g) = h;
+                *quad_at<XB>(xh, pi + 16 * u + l16, qj + 16 * v + 4 * g) = pack4(transposed(h));
+            }
+    };
+#pragma unroll
+    for (int u = 0; u < TP; ++u)
+#pragma unroll
+        for (int v = 0; v < TQ; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t i = pi + 16 * u + 4 * g + e, j = qj + 16 * v + l16;
+                x[u][v][e] = i < s.m && j < s.n ? (float)((double)f32[i * PF + j] * f) : 0.0f;
+            }
+    spread_x();
+    __syncthreads();
+
+    const float inv_s2 = 1.0f / (s.s * s.s);
+    for (int k = 0; k < steps.n; ++k) {
+        // A = X X^T, whole: its rows are written from its columns, which are the same
+        tf32x4 a[TP][SQ];
+        f16x4 o[TP][SQ];
+        lds_product<TP, SQ, XB>(a, xh, pi, xh, qs);
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+            for (int v = 0; v < SQ; ++v) {
+                const uint32_t i = pi + 16 * u + 4 * g, j = qs + 16 * v + l16;
+                a[u][v] = a[u][v] * inv_s2;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i + e == j) {
+                        da[j] = a[u][v][e];
+                        a[u][v][e] = 0.0f;
+                    }
+                o[u][v] = pack4(a[u][v]);
+                *quad_at<TB>(la, j, i) = o[u][v];
+            }
+        __syncthreads();
+        // B = b A + c A A (see Poly)
+        lds_product<TP, SQ, TB>(a, la, pi, la, qs);
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+            for (int v = 0; v < SQ; ++v) {
+                const uint32_t i = pi + 16 * u + 4 * g, j = qs + 16 * v + l16;
+                const float dj = da[j];
+                tf32x4 b;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool diag = i + e == j;
+                    const float off = (float)o[u][v][e];
+                    float q = __builtin_fmaf(da[i + e] + dj, off, a[u][v][e]);
+                    if (diag) q = __builtin_fmaf(dj, dj, q);
+                    b[e] = __builtin_fmaf(steps.c[k].c, q, steps.c[k].b * (diag ? dj : off));
+                    if (diag) {
+                        db[j] = b[e];
+                        b[e] = 0.0f;
+                    }
+                }
+                *quad_at<TB>(lb, j, i) = pack4(b);
+            }
+        __syncthreads();
+        // X <- a X + B X
+        tf32x4 y[TP][TQ];
+        lds_product<TP, TQ, TB>(y, lb, pi, xt, qj);
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float d = steps.c[k].a + db[pi + 16 * u + 4 * g + e];
+#pragma unroll
+                for (int v = 0; v < TQ; ++v) x[u][v][e] = __builtin_fmaf(d, x[u][v][e], y[u][v][e]);
+            }
+        __syncthreads();                               // everybody has read B and X^T
+        if (k + 1 < steps.n) {
+            spread_x();
+            __syncthreads();
+        }
+    }
+
+    // the result through LDS, to rows of the source's shape
+#pragma unroll
+    for (int u = 0; u < TP; ++u)
+#pragma unroll
+        for (int v = 0; v < TQ; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f32[(pi + 16 * u + 4 * g + e) * PF + qj + 16 * v + l16] = x[u][v][e];
+    __syncthreads();
+    const Dst dst(io, s, z, 1.0f / s.s);
+    for (uint32_t k = tid; k < s.rows * w4; k += NT) {
+        const uint32_t r = k / w4, c = (k - r * w4) * 4, n = min(4u, s.cols - c);
+        tf32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            if (e < n) v[e] = f32[s.tall ? (c + e) * PF + r : r * PF + c + e];
+        dst.store(r, c, n, v);
+    }
+}
+
+template <class IO, class In, class Dst>
+hipError_t launch_small(const NsShape& s, uint32_t count, const IO& io, const NsCoef* coef, int steps,
+                        hipStream_t stream) {
+    NsSteps st{};
+    st.n = steps;
+    for (int k = 0; k < steps; ++k) st.c[k] = coef[k];
+    if (s.m > 64) ns_small_kernel<IO, In, Dst, 128, 128, 2, 4><<<count, 512, 0, stream>>>(io, s, st);
+    else if (s.n > 128) ns_small_kernel<IO, In, Dst, 64, 256, 2, 4><<<count, 512, 0, stream>>>(io, s, st);
+    else if (s.n > 64) ns_small_kernel<IO, In, Dst, 64, 128, 2, 2><<<count, 256, 0, stream>>>(io, s, st);
+    else ns_small_kernel<IO, In, Dst, 64, 64, 2, 2><<<count, 256, 0, stream>>>(io, s, st);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------
 // One product over `count` matrices with mp x np results (mp = np for the symmetric ones).
-// The tile is chosen by what the launch would take per 128 bytes of K, from times measured on
-// the full chip (us per slab): a round of 256 x 256 tiles (one block per CU) 1.45; of quarters
-// in the same kernel 0.55; of 128 x 128 tiles 0.52 with one block per CU and 1.03 with two; of
-// 64 x 64 tiles 0.23 and 0.39.  Results do not depend on the choice: every element's products
-// are added in the same order.
+// The tiles are chosen by what the launch would take per 128 bytes of K, from times measured on
+// the full chip (us per slab): a round of 256 x 256 tiles (one block a CU) 1.45, of their
+// quarters 0.5; a round of 128 x 128 tiles 0.56 (two blocks on a CU take twice that), of their
+// quarters 0.2; 64 x 64 tiles 0.23 where each CU has one, 0.2 a round otherwise.  Results do
+// not depend on the choice: every element's products are added in the same order.
 template <class Op>
 hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_t np, uint32_t count,
                           hipStream_t stream) {
-    auto rounds = [](uint64_t n, double one, double two) {
-        return n <= kCUs ? one : two * (double)((n + 2 * kCUs - 1) / (2 * kCUs));
-    };
     const uint64_t p64 = mp / 64, q64 = np / 64;
     const uint64_t n64 = (Op::SYM ? p64 * (p64 + 1) / 2 : p64 * q64) * count;
-    const double c64 = rounds(n64, 0.23, 0.39);
-    if (mp % 128 || np % 128) {
+    const double c64 = n64 <= kCUs ? 0.23 : 0.2 * (double)((n64 + kCUs - 1) / kCUs);
+    double c128 = 0.0, c256 = 1e300;
+    uint64_t b128 = 0, b256 = 0;
+    TileMap m256{};
+    const TileMap m128 = plan_tiles(128, Op::SYM, mp, np, count, 0.56, 0.2, &c128, &b128);
+    // quarters of the large tile are not cut
+    if (mp % 128 == 0 && np % 128 == 0)
+        m256 = plan_tiles(256, Op::SYM, mp, np, count, 1.45, 0.5, &c256, &b256);
+    if (c64 <= c128 && c64 <= c256)
         ns_even_kernel<Op, Core64><<<(uint32_t)n64, Core64::NT, 0, stream>>>(op, st, mp, np);
-        return hipGetLastError();
-    }
-    const uint64_t p128 = mp / 128, q128 = np / 128;
-    const uint64_t n128 = (Op::SYM ? p128 * (p128 + 1) / 2 : p128 * q128) * count;
-    const double c128 = rounds(n128, 0.52, 1.03);
-    double c256 = 0.0;
-    uint64_t blocks = 0;
-    const TileMap m = plan_tiles(Op::SYM, mp, np, count, 1.45, 0.55, &c256, &blocks);
-    if (c256 < c128 && c256 < c64) {
-        ns_mixed_kernel<Op><<<(uint32_t)blocks, 512, 0, stream>>>(op, st, m);
-    } else if (c128 < c64) {
-        ns_even_kernel<Op, Core128><<<(uint32_t)n128, Core128::NT, 0, stream>>>(op, st, mp, np);
-    } else {
-        ns_even_kernel<Op, Core64><<<(uint32_t)n64, Core64::NT, 0, stream>>>(op, st, mp, np);
-    }
+    else if (c128 < c256)
+        ns_mixed_kernel<Op, Core128, Core64><<<(uint32_t)b128, Core128::NT, 0, stream>>>(op, st, m128);
+    else
+        ns_mixed_kernel<Op, Core256, Core128w><<<(uint32_t)b256, Core256::NT, 0, stream>>>(op, st, m256);
     return hipGetLastError();
 }
 
@@ -634,16 +891,36 @@ hipError_t enqueue_steps(const NsShape& s, const NsBuf& w, uint32_t count, const
     hipError_t e = hipGetLastError();
     const DevState* st = state_of(io);
     const float inv_s2 = 1.0f / (s.s * s.s), inv_s = 1.0f / s.s;
-    for (int k = 0; k < steps && e == hipSuccess; ++k) {
-        e = launch_product(Gram{w, s.mp, s.np, inv_s2}, st, s.mp, s.mp, count, stream);
-        if (e == hipSuccess) e = launch_product(Poly{w, s.mp, s.np, coef[k].b, coef[k].c}, st, s.mp, s.mp, count, stream);
+    int from = 0;
+    SymBuf y[3];
+    for (int k = 0; k < 3; ++k) y[k] = SymBuf{w.sym[k], w.diag[k]};
+    // the products of Sym, by buffer
+    auto sym = [&](int l, int m, int r, float ka, float kb, float kc) {
+        if (e != hipSuccess) return;
+        e = l == m ? launch_product(Sym<true>{y[l], y[m], y[r], s.mp, s.np, ka, kb, kc}, st, s.mp, s.mp, count, stream)
+                   : launch_product(Sym<false>{y[l], y[m], y[r], s.mp, s.np, ka, kb, kc}, st, s.mp, s.mp, count, stream);
+    };
+    for (int k = 0; k < steps && e == hipSuccess;) {
+        e = launch_product(Gram{w.xh, y[0], s.mp, s.np, inv_s2}, st, s.mp, s.mp, count, stream);
+        int by = 1;
+        sym(0, 0, 1, coef[k].a, coef[k].b, coef[k].c);             // P = a I + b A + c A A
+        if (s.pairs && k + 1 < steps) {
+            sym(1, 0, 2, 0.0f, 0.0f, 1.0f);                        // P A
+            sym(2, 1, 0, 0.0f, 0.0f, 1.0f);                        // A of the next step: P A P
+            sym(0, 0, 2, coef[k + 1].a, coef[k + 1].b, coef[k + 1].c);
+            sym(2, 1, 0, 0.0f, 0.0f, 1.0f);                        // both steps' P
+            by = 0;
+            ++k;
+        }
+        ++k;
         if (e != hipSuccess) break;
-        if (k + 1 < steps)
-            e = launch_product(Apply{w, s.mp, s.np, coef[k].a, k & 1}, st, s.mp, s.np, count, stream);
+        if (k < steps)
+            e = launch_product(Apply{y[by], w.xt[from], w.xt[from ^ 1], w.xh, w.lt, s.mp, s.np}, st, s.mp, s.np, count, stream);
         else if (s.tall)
-            e = launch_product(Last<IO, Dst, true>{io, w, s, coef[k].a, inv_s, k & 1}, st, s.mp, s.np, count, stream);
+            e = launch_product(Last<IO, Dst, true>{io, y[by], w.xt[from], w.xh, w.lt, s, inv_s}, st, s.mp, s.np, count, stream);
         else
-            e = launch_product(Last<IO, Dst, false>{io, w, s, coef[k].a, inv_s, k & 1}, st, s.np, s.mp, count, stream);
+            e = launch_product(Last<IO, Dst, false>{io, y[by], w.xt[from], w.xh, w.lt, s, inv_s}, st, s.np, s.mp, count, stream);
+        from ^= 1;
     }
     return e;
 }
@@ -652,6 +929,7 @@ hipError_t enqueue_steps(const NsShape& s, const NsBuf& w, uint32_t count, const
 
 hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const OrthIO& io,
                         const NsCoef* coef, int steps, hipStream_t stream) {
+    if (s.small) return launch_small<OrthIO, OrthIn, OrthDst>(s, count, io, coef, steps, stream);
     orth_norm_kernel<<<s.parts * count, kNormThreads, 0, stream>>>(io, s.rows, s.cols, s.parts, w.part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -660,6 +938,7 @@ hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const 
 
 hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const MuonIO& io,
                         const NsCoef* coef, int steps, hipStream_t stream) {
+    if (s.small) return launch_small<MuonIO, MuonIn, MuonDst>(s, count, io, coef, steps, stream);
     muon_momentum_kernel<<<s.parts * count, kNormThreads, 0, stream>>>(io, (uint64_t)s.rows * s.cols, s.parts, w.part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -669,7 +948,7 @@ hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const 
 // ------------------------------------------------------------------------------------
 // shapes
 // ------------------------------------------------------------------------------------
-NsShape ns_shape(uint64_t rows, uint64_t cols) {
+NsShape ns_shape(uint64_t rows, uint64_t cols, bool pairs) {
     NsShape s{};
     s.rows = (uint32_t)rows;
     s.cols = (uint32_t)cols;
@@ -680,6 +959,8 @@ NsShape ns_shape(uint64_t rows, uint64_t cols) {
     const uint32_t t = s.m <= 512 ? 64 : 128;
     s.mp = (s.m + t - 1) / t * t;
     s.np = (s.n + t - 1) / t * t;
+    s.small = (s.m <= 128 && s.n <= 128) || (s.m <= 64 && s.n <= 256);
+    s.pairs = pairs && s.m > 512 && s.n >= 2 * s.m;
     // one partial sum for each 16K elements, at most one for each row
     const uint64_t want = (rows * cols + 16383) / 16384;
     s.parts = (uint32_t)(want < kNsParts ? want : kNsParts);
@@ -707,17 +988,17 @@ NsBuf ns_place(const NsShape& s, uint64_t count, void* base) {
     w.xt[0] = (uint16_t*)take(x);
     w.xt[1] = (uint16_t*)take(x);
     w.lt = (uint16_t*)take(x);
-    w.a = (uint16_t*)take(a);
-    w.b = (uint16_t*)take(a);
-    w.da = (float*)take(4ull * s.mp * count);
-    w.db = (float*)take(4ull * s.mp * count);
+    for (int k = 0; k < (s.pairs ? 3 : 2); ++k) {
+        w.sym[k] = (uint16_t*)take(a);
+        w.diag[k] = (float*)take(4ull * s.mp * count);
+    }
     w.part = (double*)take(8ull * kNsParts * count);
     return w;
 }
 
 uint64_t ns_bytes(const NsShape& s, uint64_t count) {
     const uint64_t x = 2ull * s.mp * s.np * count, a = 2ull * s.mp * s.mp * count;
-    return 4 * up256(x) + 2 * up256(a) + 2 * up256(4ull * s.mp * count) + up256(8ull * kNsParts * count);
+    return 4 * up256(x) + (s.pairs ? 3 : 2) * (up256(a) + up256(4ull * s.mp * count)) + up256(8ull * kNsParts * count);
 }
 
 }  // namespace nz1

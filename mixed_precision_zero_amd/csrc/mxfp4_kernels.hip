@@ -407,7 +407,7 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
     // 1.25 with two
     double c256 = 0.0;
     uint64_t blocks = 0;
-    const TileMap map = plan_tiles(false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
+    const TileMap map = plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
     const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
     const double c128 = n128 <= kCUs ? 0.63 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
     if (c256 < c128) product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);

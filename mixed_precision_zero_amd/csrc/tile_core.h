@@ -254,9 +254,9 @@ struct TileCore {
 // ------------------------------------------------------------------------------------
 // which tile a block works on
 // ------------------------------------------------------------------------------------
-// Blocks [0, nfull) take whole 256 x 256 tiles; the others take
-// quarters (128 x 128) of what is left: the tiles that would start another, mostly empty round
-// on the chip's 256 CUs, and those that the matrix's edge cuts.  Tiles of a symmetric product
+// Blocks [0, nfull) take whole tiles of unit x unit (256 or 128); the others take quarters of
+// what is left: the tiles that would start another, mostly empty round on the chip's 256 CUs,
+// and those that the matrix's edge cuts.  Tiles of a symmetric product
 // lie on and below the diagonal, those on it last (a quarter of them above it is left out).
 struct TileMap {
     uint32_t nfull;        // blocks with whole tiles
@@ -266,6 +266,7 @@ struct TileMap {
     uint32_t pi, qi;       // whole tiles down and across
     uint32_t q;            // tiles across, a cut one counted
     uint32_t mp, np;       // sides
+    uint32_t unit;
 };
 
 // (i, j), j <= i, number t in row order of a lower triangle
@@ -280,6 +281,14 @@ __device__ __forceinline__ void lower(uint32_t t, uint32_t& ti, uint32_t& tj) {
 struct TileAt {
     uint32_t z, i, j;      // matrix, first row and column
     bool full, none;
+    // Into scalar registers: the same for the whole block, but computed with vector
+    // instructions (a square root); operands addressed through vector registers would turn
+    // every buffer load into a loop over the lanes.
+    __device__ __forceinline__ void settle() {
+        z = __builtin_amdgcn_readfirstlane(z);
+        i = __builtin_amdgcn_readfirstlane(i);
+        j = __builtin_amdgcn_readfirstlane(j);
+    }
 };
 
 template <bool SYM>
@@ -328,26 +337,28 @@ __device__ __forceinline__ TileAt place(const TileMap& m) {
             tj = k < right ? m.qi : k - right;
         }
     }
-    r.i = ti * 256 + (quarter >> 1) * 128;
-    r.j = tj * 256 + (quarter & 1) * 128;
+    r.i = ti * m.unit + (quarter >> 1) * (m.unit / 2);
+    r.j = tj * m.unit + (quarter & 1) * (m.unit / 2);
+    r.settle();
     r.none = r.i >= m.mp || r.j >= m.np || (SYM && !r.full && r.j > r.i);
     return r;
 }
 
 // The launch of one product with `count` p x q results (p = q and sym for symmetric ones; a
 // cut tile reads zeros behind its operands' rows), and its cost per slab of K: `full` for a
-// round of 256 x 256 tiles over the chip's CUs, `quarter` for a round of quarters.
+// round of whole tiles over the chip's CUs, `quarter` for a round of quarters.
 constexpr uint32_t kCUs = 256;
-inline TileMap plan_tiles(bool sym, uint32_t p, uint32_t q, uint32_t count, double full, double quarter,
+inline TileMap plan_tiles(uint32_t unit, bool sym, uint32_t p, uint32_t q, uint32_t count, double full, double quarter,
                           double* cost, uint64_t* blocks) {
     TileMap m{};
     m.count = count;
-    m.pi = p / 256;
-    m.qi = q / 256;
-    m.q = (q + 255) / 256;
+    m.unit = unit;
+    m.pi = p / unit;
+    m.qi = q / unit;
+    m.q = (q + unit - 1) / unit;
     m.mp = p;
     m.np = q;
-    const bool cut_p = p % 256 != 0, cut_q = q % 256 != 0;
+    const bool cut_p = p % unit != 0, cut_q = q % unit != 0;
     if (sym) {
         m.inner = m.pi * (m.pi + 1) / 2;
         m.edges = cut_p ? m.pi + 1 : 0;
@@ -389,25 +400,33 @@ struct Patch {
     static __device__ __forceinline__ f16x4* at(uint8_t* l, uint32_t row, uint32_t col) {
         return (f16x4*)(l + row * kRow + (((col >> 3) ^ turn(row)) << 4) + (col & 4) * 2);
     }
+    // A pass moves kBytes / kPass bytes: rows k * kStep + lane / kChunks.  The lane's part of an
+    // address stays apart from the pass's, which is the same for all lanes (Ld: 32 bits where
+    // kStep rows are less than 4 GB).
+    static constexpr int kStep = 64 / kChunks;
+    template <class Ld>
+    static __device__ __forceinline__ Ld lane_part(int k, Ld ld) {
+        const uint32_t lane = threadIdx.x & 63;
+        const uint32_t row = lane / kChunks, c = (lane % kChunks) ^ turn(k * kStep + row);
+        return row * ld + c * 8;
+    }
     // starts loading from g (row r at r * ld); wave_wait() before it is used
     static __device__ __forceinline__ void load(uint8_t* l, const uint16_t* g, uint32_t ld) {
-        const uint32_t lane = threadIdx.x & 63;
 #pragma unroll
-        for (int k = 0; k < kPass; ++k) {
-            const uint32_t row = (k * 64 + lane) / kChunks, c = (lane % kChunks) ^ turn(row);
+        for (int k = 0; k < kPass; ++k)
             __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(g + (uint64_t)row * ld + c * 8),
+                (const __attribute__((address_space(1))) void*)(g + (uint64_t)(k * kStep) * ld + lane_part<uint32_t>(k, ld)),
                 (__attribute__((address_space(3))) void*)(l + k * 1024), 16, 0, 0);
-        }
     }
     // rows [0, left) to g
-    static __device__ __forceinline__ void store(const uint8_t* l, uint16_t* g, uint64_t ld, uint32_t left = ROWS) {
+    template <class Ld>
+    static __device__ __forceinline__ void store(const uint8_t* l, uint16_t* g, Ld ld, uint32_t left = ROWS) {
         const uint32_t lane = threadIdx.x & 63;
 #pragma unroll
-        for (int k = 0; k < kPass; ++k) {
-            const uint32_t row = (k * 64 + lane) / kChunks, c = (lane % kChunks) ^ turn(row);
-            if (row < left) *(tu32x4*)(g + (uint64_t)row * ld + c * 8) = *(const tu32x4*)(l + (k * 64 + lane) * 16);
-        }
+        for (int k = 0; k < kPass; ++k)
+            if (k * kStep + lane / kChunks < left)
+                *(tu32x4*)(g + (uint64_t)(k * kStep) * ld + lane_part<Ld>(k, ld)) =
+                    *(const tu32x4*)(l + (k * 64 + lane) * 16);
     }
 };
 // All of this wave's memory operations so far are done.
@@ -431,11 +450,13 @@ struct Piece {
     uint8_t *l0, *l1;      // LDS of two patches
     __device__ Piece(const TileAt& t, int u0, uint8_t* lds) {
         const uint32_t lane = threadIdx.x & 63;
-        i = t.i + Core::wave_p() + 16 * u0;
-        j = t.j + Core::wave_q();
+        i = __builtin_amdgcn_readfirstlane(t.i + Core::wave_p() + 16 * u0);
+        j = __builtin_amdgcn_readfirstlane(t.j + Core::wave_q());
         li = (lane >> 4) * 4;
         lj = lane & 15;
-        l0 = lds + (threadIdx.x >> 6) * (Core::kLds / (Core::NT / 64));
+        // (scalar, so that the patches' places and what follows from them are)
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        l0 = lds + wave * (Core::kLds / (Core::NT / 64));
         l1 = l0 + kBytes;
     }
     // The places of tile (u, v)'s elements of this lane, and of their transposes, in a patch.

@@ -9,6 +9,7 @@ that stream, and reject what the operators do not cover; nothing falls back to t
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import dataclasses
 
@@ -214,11 +215,38 @@ def _rows_of(t, name):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _on(t):
-    """(device guard, stream address) for work on t."""
-    import torch
-    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device).cuda_stream
+_HERE = contextlib.nullcontext()
 
+
+def _on(t):
+    """(device guard, stream address) for work on t.  The guard does nothing where t's device is
+    the current one already: entering one costs more than a small launch."""
+    import torch
+    d = t.device
+    guard = _HERE if torch.cuda.current_device() == d.index else torch.cuda.device(d)
+    return guard, torch.cuda.current_stream(d).cuda_stream
+
+
+def _batch(t, name, rows, cols):
+    """t's matrices as one run: (elements from one to the next, elements from row to row)."""
+    if t.is_contiguous():
+        return rows * cols, cols
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: elements of a row must be adjacent")
+    ld = t.stride(-2) if rows > 1 else cols
+    step, n = rows * ld, 1
+    for size, stride in reversed(list(zip(t.shape[:-2], t.stride()[:-2]))):
+        if size == 1:
+            continue
+        if n > 1 and stride != step * n:
+            raise ValueError(f"{name}: the matrices must lie at one distance from each other")
+        if n == 1:
+            step = stride
+        n *= size
+    return step, ld
+
+
+_default_ns = None
 
 def orthogonalize(x, out=None, dtype=None, scale: float = 1.0, cfg: neox_ns_config | None = None):
     """scale * (the orthogonal factor of each matrix of x, approximately).  x: a matrix or a
@@ -231,29 +259,16 @@ def orthogonalize(x, out=None, dtype=None, scale: float = 1.0, cfg: neox_ns_conf
         out = torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
     elif out.shape != x.shape or out.device != x.device or (dtype is not None and out.dtype != dtype):
         raise ValueError("out must have x's shape and device, and the type asked for")
+    global _default_ns
+    if cfg is None:
+        if _default_ns is None:
+            _default_ns = neox_ns_default_config()
+        cfg = _default_ns
     rows, cols = x.shape[-2:]
-
-    def batch(t, name):
-        """t's matrices as (stride between them, stride between rows) of one run."""
-        if cols > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name}: elements of a row must be adjacent")
-        ld = t.stride(-2) if rows > 1 else cols
-        step, n = rows * ld, 1
-        for size, stride in reversed(list(zip(t.shape[:-2], t.stride()[:-2]))):
-            if size == 1:
-                continue
-            if n > 1 and stride != step * n:
-                raise ValueError(f"{name}: the matrices must lie at one distance from each other")
-            if n == 1:
-                step = stride
-            n *= size
-        return step, ld
-
     count = 1
     for size in x.shape[:-2]:
         count *= size
-    cfg = neox_ns_default_config() if cfg is None else cfg
-    (xs, xld), (os_, old) = batch(x, "x"), batch(out, "out")
+    (xs, xld), (os_, old) = _batch(x, "x", rows, cols), _batch(out, "out", rows, cols)
     guard, stream = _on(x)
     with guard:
         need = neox_orthogonalize_workspace(count, rows, cols)
@@ -288,8 +303,11 @@ class MXFP4:
     def empty(rows: int, cols: int, device) -> "MXFP4":
         import torch
         k = -(-cols // 128) * 128
-        return MXFP4(torch.empty(rows, k // 2, dtype=torch.uint8, device=device),
-                     torch.empty(rows, k // 32, dtype=torch.uint8, device=device), rows, cols)
+        q = object.__new__(MXFP4)          # right by construction: nothing to check
+        q.codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((rows, k // 32), dtype=torch.uint8, device=device)
+        q.rows, q.cols = rows, cols
+        return q
 
 
 def mxfp4_quantize(x, transpose: bool = False, out: MXFP4 | None = None) -> MXFP4:

@@ -23,24 +23,39 @@ def newton_schulz(g, coef=COEF, eps=1e-7):
 
 def newton_schulz_rounded(g, coef=COEF, eps=1e-7):
     """The same with every rounding the kernels make (FP16 product operands, the iterate as two
-    FP16 numbers, diagonals apart) and 64-bit sums: its distance from newton_schulz() is what
-    those roundings cost on this input."""
+    FP16 numbers, diagonals apart, two steps at a time where the kernels take them so) and
+    64-bit sums: its distance from newton_schulz() is what those roundings cost on this input."""
     x = g.double().cpu()
-    if x.shape[0] > x.shape[1]:
+    m, n = x.shape
+    if m > n:
         return newton_schulz_rounded(x.t(), coef, eps).t()
     half = lambda t: t.to(torch.float16).double()  # noqa: E731
-    s = 2.0 ** math.floor((math.floor(math.log2(x.shape[1])) + 1) / 2)
+
+    def apart(p):
+        d = torch.diag(p).clone()
+        return d, half(p - torch.diag(d))
+
+    def times(d, o, e, p):
+        return o @ p + d[:, None] * p + o * e[None, :] + torch.diag(d * e)
+
+    def poly(d, o, abc):
+        a, b, c = abc
+        return apart(a * torch.eye(m, dtype=torch.float64) + b * (o + torch.diag(d)) + c * times(d, o, d, o))
+
+    s = 2.0 ** math.floor((math.floor(math.log2(n)) + 1) / 2)
     x = x / (torch.linalg.vector_norm(x) + eps) * s
-    for a, b, c in coef:
+    k = 0
+    while k < len(coef):
         hi = half(x)
         x = hi + half((x - hi) * 2048) / 2048
-        p = hi @ hi.t() / s ** 2
-        d = torch.diag(p).clone()
-        off = half(p - torch.diag(d))
-        sq = off @ off + (d[:, None] + d[None, :]) * off + torch.diag(d * d)
-        q = b * (off + torch.diag(d)) + c * sq
-        dq = torch.diag(q).clone()
-        x = (a + dq)[:, None] * x + half(q - torch.diag(dq)) @ hi
+        gram = apart(hi @ hi.t() / s ** 2)
+        p = poly(*gram, coef[k])
+        if m > 512 and n >= 2 * m and k + 1 < len(coef):
+            gram = apart(times(*apart(times(*p, *gram)), *p))
+            p = apart(times(*poly(*gram, coef[k + 1]), *p))
+            k += 1
+        x = p[0][:, None] * x + p[1] @ hi
+        k += 1
     return x / s
 
 

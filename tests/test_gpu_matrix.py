@@ -32,7 +32,8 @@ def padded(t, extra, fill):
 # ----------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 9), (9, 1), (3, 5), (31, 33), (64, 64), (65, 63), (128, 128),
-                                       (129, 127), (40, 700), (700, 40), (130, 513), (513, 257), (300, 1000)])
+                                       (129, 127), (40, 700), (700, 40), (130, 513), (513, 257), (300, 1000), (520, 1100),
+                                       (1300, 600)])
 def test_orthogonalize_sizes(rows, cols):
     x = rand((rows, cols), rows * 1000 + cols)
     R.check_orth(M.orthogonalize(x), x)
@@ -56,10 +57,11 @@ def test_orthogonalize_spectra(kind):
     R.check_orth(M.orthogonalize(x), x)
 
 
+@pytest.mark.parametrize("shape", [(90, 140), (530, 1065)], ids=["single", "pairs"])
 @pytest.mark.parametrize("coef", [[(1.5, -0.5, 0.0)] * 8, [(3.4445, -4.7750, 2.0315)], [(15 / 8, -10 / 8, 3 / 8)] * 3,
                                   [(4.0, -6.0, 3.0), (2.0, -1.5, 0.5)]])
-def test_orthogonalize_steps(coef):
-    x = rand((90, 140), 3)
+def test_orthogonalize_steps(coef, shape):
+    x = rand(shape, 3)
     R.check_orth(M.orthogonalize(x, cfg=M.neox_ns_default_config(coef=coef)), x, coef=coef)
 
 
@@ -413,7 +415,7 @@ def check_step(before, after, state, cfg, lr, nesterov=1, mode="rms", ns=None):
         assert torch.equal(a["grad"], b["grad"])
 
 
-SETS = [[(64, 64)], [(1, 1), (1, 5), (5, 1)], [(70, 33), (33, 70), (70, 33)], [(128, 384), (200, 130), (257, 129)]]
+SETS = [[(64, 64)], [(1100, 530)], [(1, 1), (1, 5), (5, 1)], [(70, 33), (33, 70), (70, 33)], [(128, 384), (200, 130), (257, 129)]]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
