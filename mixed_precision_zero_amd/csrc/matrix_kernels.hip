@@ -524,7 +524,7 @@ struct MuonDst {
 };
 
 // The last step.  The operands are exchanged where the source is not transposed, so that a
-// lane's four elements always are neighbours in a row of the source: there D's rows are j and
+// lane's four elements always are neighbours in a row of the source (a column of D): there D's rows are j and
 // its columns i, the iterate's first half comes from xh and its second, transposed, from lt.
 template <class IO, class Dst, bool TALL>
 struct Last {
@@ -568,7 +568,6 @@ struct Last {
                 const tf32x4 di = TALL ? *(const tf32x4*)(db + i) : tf32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int v = 0; v < P::kV; ++v) {
-                    const uint32_t j = p.j + 16 * v + p.lj;
                     const f16x4 h = *p.down(p.l0, u, v);
                     tf32x4 o;
                     if constexpr (TALL) {
@@ -577,15 +576,31 @@ struct Last {
                     } else {
                         o = transposed(*p.across(p.l1, u, v));
                     }
-                    const float dj = TALL ? 0.0f : db[j];
-                    tf32x4 y;
+                    const float dj = TALL ? 0.0f : db[p.j + 16 * v + p.lj];
+                    tf32x4& y = t.acc[u0 + u][v];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[e] = __builtin_fmaf(TALL ? di[e] : dj, __builtin_fmaf(o[e], 1.0f / kLo, (float)h[e]),
-                                              t.acc[u0 + u][v][e]);
-                    const uint32_t rows = TALL ? s.n : s.m, cols = TALL ? s.m : s.n;
-                    if (j < rows && i < cols) dst.store(j, i, min(4u, cols - i), y);
+                        y[e] = __builtin_fmaf(TALL ? di[e] : dj, __builtin_fmaf(o[e], 1.0f / kLo, (float)h[e]), y[e]);
                 }
+            }
+            // the source's rows (D's columns) through LDS: 128 or 256 bytes of a row at a time
+            // instead of 64 (four lanes)
+            constexpr uint32_t kRow = 16 * P::kU * 4, kChunks = kRow / 16, kRows = 16 * P::kV;
+            static_assert(kRows * kRow <= 2 * P::kBytes, "the two patches' place");
+#pragma unroll
+            for (int u = 0; u < P::kU; ++u)
+#pragma unroll
+                for (int v = 0; v < P::kV; ++v) {
+                    const uint32_t row = 16 * v + p.lj, c = (16 * u + p.li) / 4;
+                    *(tf32x4*)(p.l0 + row * kRow + ((c ^ (row % kChunks)) << 4)) = t.acc[u0 + u][v];
+                }
+            const uint32_t rows = TALL ? s.n : s.m, cols = TALL ? s.m : s.n, lane = threadIdx.x & 63;
+#pragma unroll 4
+            for (uint32_t k = lane; k < kRows * kChunks; k += 64) {
+                const uint32_t row = k / kChunks, c = (k % kChunks) ^ (row % kChunks);
+                const uint32_t r = p.j + row, q = p.i + 4 * c;
+                const tf32x4 y = *(const tf32x4*)(p.l0 + k * 16);
+                if (r < rows && q < cols) dst.store(r, q, min(4u, cols - q), y);
             }
             if (u0 + P::kU < Core::TP) wave_wait();
         }
