@@ -82,10 +82,11 @@ int check_sides(uint64_t rows, uint64_t cols) {
     return NEOX_OK;
 }
 
-// Matrices one launch may take: block counts stay below the grid limit (the finest grid is
-// the conversion's, one block per 64 x 64 tile, or the norm's, at most kNsParts).
+// Matrices one launch may take: thread counts stay below the grid limit (the largest grids are
+// those of 64 x 64 tiles, the split products' at most twice as many, and the norm's, at most
+// kNsParts blocks of 1,024 threads).
 uint64_t launch_count(const NsShape& s) {
-    const uint64_t per = std::max<uint64_t>((uint64_t)(s.mp / 64) * (s.np / 64), kNsParts);
+    const uint64_t per = std::max<uint64_t>((uint64_t)(s.mp / 64) * (s.np / 64) * 2, 4 * kNsParts);
     return std::max<uint64_t>(1, (kMaxBlocks - 1) / per);
 }
 

@@ -22,6 +22,7 @@ struct NsBuf {
     uint16_t* sym[3];  // [mp][mp] FP16: X X^T and polynomials of it, without their diagonals
     float* diag[3];    // [mp] the diagonals (the third pair with `pairs` only)
     double* part;      // [kNsParts] partial squared norms of the source
+    float* sums;       // [split][lower 64 x 64 tiles][4096] shares of X X^T (split > 1 only)
 };
 
 struct NsShape {
@@ -31,6 +32,7 @@ struct NsShape {
     uint32_t parts;        // partial sums per matrix
     bool tall;             // the wide form is the source's transpose
     bool small;            // one block does it all, without the buffers
+    uint32_t split;        // shares of X X^T's sums
     bool pairs;            // the iterate is updated once for two steps
     float s;               // S, a power of two: the iterate is stored times S
 };

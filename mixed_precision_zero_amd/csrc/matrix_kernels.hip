@@ -26,6 +26,8 @@
 #include "matrix_internal.h"
 #include "tile_core.h"
 
+#include <algorithm>
+
 namespace nz1 {
 
 namespace {
@@ -358,6 +360,66 @@ struct Gram {
     }
 };
 
+// X X^T of a few rows and many columns, K split: block `part` of `parts` sums its share of the
+// columns of one 64 x 64 tile, and a second launch adds the shares in order.  One after the
+// other, the 64-column slabs of 64 x 8192 take 29 us on one CU; in 16 shares 2, and 4 to join.
+struct GramSplit {
+    const uint16_t* xh;
+    SymBuf out;
+    float* sums;               // [matrix][part][tile][64 * 64], in the order of the lanes
+    uint32_t mp, np, parts;
+    float inv_s2;
+};
+using Core64 = TileCore<64, 64, 2, 2, false, 4>;
+__global__ __launch_bounds__(Core64::NT) void gram_part_kernel(GramSplit g, const DevState* st) {
+    if (skipped(st)) return;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Core64::kLds];
+    const uint32_t side = g.mp / 64, tiles = side * (side + 1) / 2;
+    const uint32_t t = blockIdx.x % tiles, zp = blockIdx.x / tiles, z = zp / g.parts, part = zp % g.parts;
+    TileAt at{};
+    lower(t, at.i, at.j);
+    at.settle();
+    // whole slabs of 64 columns
+    const uint32_t slabs = g.np / 64, k0 = slabs * part / g.parts * 64, k1 = slabs * (part + 1) / g.parts * 64;
+    const uint16_t* x = g.xh + (uint64_t)z * g.mp * g.np + k0;
+    Core64 c;
+    c.run(rows_of(x, at.i * 64, g.np, 64), rows_of(x, at.j * 64, g.np, 64), (k1 - k0) * 2, lds);
+    tf32x4* o = (tf32x4*)(g.sums + ((uint64_t)zp * tiles + t) * 4096) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < Core64::TP; ++u)
+#pragma unroll
+        for (int v = 0; v < Core64::TQ; ++v) o[(u * Core64::TQ + v) * Core64::NT] = c.acc[u][v];
+}
+__global__ __launch_bounds__(Core64::NT) void gram_join_kernel(GramSplit g, const DevState* st) {
+    if (skipped(st)) return;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Core64::kLds];
+    const uint32_t side = g.mp / 64, tiles = side * (side + 1) / 2;
+    const uint32_t t = blockIdx.x % tiles, z = blockIdx.x / tiles;
+    TileAt at{};
+    lower(t, at.i, at.j);
+    at.i *= 64;
+    at.j *= 64;
+    at.settle();
+    Core64 c;
+#pragma unroll
+    for (int u = 0; u < Core64::TP; ++u)
+#pragma unroll
+        for (int v = 0; v < Core64::TQ; ++v) c.acc[u][v] = tf32x4{0, 0, 0, 0};
+    for (uint32_t part = 0; part < g.parts; ++part) {
+        const tf32x4* o = (const tf32x4*)(g.sums + (((uint64_t)z * g.parts + part) * tiles + t) * 4096) + threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < Core64::TP; ++u)
+#pragma unroll
+            for (int v = 0; v < Core64::TQ; ++v) c.acc[u][v] = c.acc[u][v] + o[(u * Core64::TQ + v) * Core64::NT];
+    }
+#pragma unroll
+    for (int u = 0; u < Core64::TP; ++u)
+#pragma unroll
+        for (int v = 0; v < Core64::TQ; ++v) c.acc[u][v] = c.acc[u][v] * g.inv_s2;
+    store_sym<Core64>(at, Piece<Core64>(at, 0, lds), c.acc, 0, g.out.a + (uint64_t)z * g.mp * g.mp, g.mp,
+                      g.out.d + (uint64_t)z * g.mp, [](uint32_t) { return 0.0f; });
+}
+
 // Products of symmetric buffers: R = ka I + kb L + kc L L (SAME), or R = L M for L and M that
 // commute.  With L = O + D, M = N + E (diagonals apart): L M = O N + D_i N_ij + O_ij E_j, and
 // D_i E_i on the diagonal, where O and N are 0.
@@ -610,8 +672,6 @@ struct Last {
 using Core256 = TileCore<256, 256, 2, 4, false>;
 using Core128w = TileCore<128, 128, 2, 4, false>;      // quarters, by the same 512 threads
 using Core128 = TileCore<128, 128, 2, 2, false>;
-using Core64 = TileCore<64, 64, 2, 2, false, 4>;
-
 template <class Op, class Full, class Quarter>
 __global__ __launch_bounds__(Full::NT, 2) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
     static_assert(Full::NT == Quarter::NT && Full::kLds >= Quarter::kLds && Full::BP == 2 * Quarter::BP, "");
@@ -916,7 +976,18 @@ hipError_t enqueue_steps(const NsShape& s, const NsBuf& w, uint32_t count, const
                    : launch_product(Sym<false>{y[l], y[m], y[r], s.mp, s.np, ka, kb, kc}, st, s.mp, s.mp, count, stream);
     };
     for (int k = 0; k < steps && e == hipSuccess;) {
-        e = launch_product(Gram{w.xh, y[0], s.mp, s.np, inv_s2}, st, s.mp, s.mp, count, stream);
+        if (s.split > 1) {
+            const GramSplit g{w.xh, y[0], w.sums, s.mp, s.np, s.split, inv_s2};
+            const uint32_t tiles = s.mp / 64 * (s.mp / 64 + 1) / 2 * count;
+            gram_part_kernel<<<tiles * s.split, Core64::NT, 0, stream>>>(g, st);
+            e = hipGetLastError();
+            if (e == hipSuccess) {
+                gram_join_kernel<<<tiles, Core64::NT, 0, stream>>>(g, st);
+                e = hipGetLastError();
+            }
+        } else {
+            e = launch_product(Gram{w.xh, y[0], s.mp, s.np, inv_s2}, st, s.mp, s.mp, count, stream);
+        }
         int by = 1;
         sym(0, 0, 1, coef[k].a, coef[k].b, coef[k].c);             // P = a I + b A + c A A
         if (s.pairs && k + 1 < steps) {
@@ -975,6 +1046,12 @@ NsShape ns_shape(uint64_t rows, uint64_t cols, bool pairs) {
     s.mp = (s.m + t - 1) / t * t;
     s.np = (s.n + t - 1) / t * t;
     s.small = (s.m <= 128 && s.n <= 128) || (s.m <= 64 && s.n <= 256);
+    // Shares of X X^T's sums: enough blocks for the chip where there are few tiles, eight slabs
+    // of 64 columns or more in each, and only where it saves more than the second launch takes
+    // (by the shape alone: the order of the sums must not depend on the batch)
+    const uint32_t tiles = s.mp / 64 * (s.mp / 64 + 1) / 2, slabs = s.np / 64;
+    s.split = 1;
+    if (s.m <= 512 && slabs >= 32) s.split = std::min(std::min(16u, slabs / 8), (96 + tiles - 1) / tiles);
     s.pairs = pairs && s.m > 512 && s.n >= 2 * s.m;
     // one partial sum for each 16K elements, at most one for each row
     const uint64_t want = (rows * cols + 16383) / 16384;
@@ -989,6 +1066,9 @@ NsShape ns_shape(uint64_t rows, uint64_t cols, bool pairs) {
 }
 
 static uint64_t up256(uint64_t x) { return (x + 255) & ~255ull; }
+static uint64_t split_bytes(const NsShape& s) {
+    return s.split > 1 ? 4096ull * 4 * (s.mp / 64) * (s.mp / 64 + 1) / 2 * s.split : 0;
+}
 
 NsBuf ns_place(const NsShape& s, uint64_t count, void* base) {
     uint8_t* p = (uint8_t*)base;
@@ -1008,12 +1088,14 @@ NsBuf ns_place(const NsShape& s, uint64_t count, void* base) {
         w.diag[k] = (float*)take(4ull * s.mp * count);
     }
     w.part = (double*)take(8ull * kNsParts * count);
+    if (s.split > 1) w.sums = (float*)take(split_bytes(s) * count);
     return w;
 }
 
 uint64_t ns_bytes(const NsShape& s, uint64_t count) {
     const uint64_t x = 2ull * s.mp * s.np * count, a = 2ull * s.mp * s.mp * count;
-    return 4 * up256(x) + (s.pairs ? 3 : 2) * (up256(a) + up256(4ull * s.mp * count)) + up256(8ull * kNsParts * count);
+    return 4 * up256(x) + (s.pairs ? 3 : 2) * (up256(a) + up256(4ull * s.mp * count)) + up256(8ull * kNsParts * count) +
+           up256(split_bytes(s) * count);
 }
 
 }  // namespace nz1

@@ -124,7 +124,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
 }
 
 // The transpose: a thread takes 32 rows of one column of src (of two, as one dword, where src
-// has 16-bit elements and lies for it), a wave 64 or 128 neighbouring columns.
+// has 16-bit elements and lies for it), a wave 64 or 128 neighbouring columns, and the block's
+// four waves four blocks of 32 of each: together 64 bytes of codes and four scales of each row
+// of the copy, so that the L2 gets whole sectors from one CU.
 template <int DT, int N>
 __global__ __launch_bounds__(256) void quantize_cols_kernel(const void* __restrict__ src, uint64_t R, uint64_t C,
                                                             uint64_t ld, uint8_t* __restrict__ codes,
@@ -134,7 +136,8 @@ __global__ __launch_bounds__(256) void quantize_cols_kernel(const void* __restri
     if (st && st->skip) return;
     // R, C: the copy's; its row r is src's column r.  b: block of 32 along it
     const uint32_t down = blockIdx.x / across;
-    const uint64_t b = b0 + down, r = ((uint64_t)(blockIdx.x - down * across) * 256 + threadIdx.x) * N;
+    const uint64_t b = (b0 + down) * 4 + (threadIdx.x >> 6);
+    const uint64_t r = ((uint64_t)(blockIdx.x - down * across) * 64 + (threadIdx.x & 63)) * N;
     if (r >= R) return;
     float v[N][32];
 #pragma unroll
@@ -392,8 +395,8 @@ hipError_t launch_mx_quantize(const void* src, int dtype, uint64_t rows, uint64_
         if (transpose) {
             auto cols = [&](auto nn) {
                 constexpr int N = decltype(nn)::value;
-                const uint32_t across = (uint32_t)((R + 256 * N - 1) / (256 * N));
-                const uint64_t down = sh.scale_pitch, most = std::max<uint64_t>(1, kGrid / across);
+                const uint32_t across = (uint32_t)((R + 64 * N - 1) / (64 * N));
+                const uint64_t down = sh.scale_pitch / 4, most = std::max<uint64_t>(1, kGrid / across);
                 for (uint64_t d = 0; d < down; d += most)
                     quantize_cols_kernel<DT, N><<<(uint32_t)(across * std::min(most, down - d)), 256, 0, stream>>>(
                         src, R, C, ld, (uint8_t*)codes, (uint8_t*)scales, sh, across, d, st);

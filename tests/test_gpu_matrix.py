@@ -33,7 +33,7 @@ def padded(t, extra, fill):
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 9), (9, 1), (3, 5), (31, 33), (64, 64), (65, 63), (128, 128),
                                        (129, 127), (40, 700), (700, 40), (130, 513), (513, 257), (300, 1000), (520, 1100),
-                                       (1300, 600)])
+                                       (1300, 600), (60, 2100), (5000, 70), (200, 2500)])
 def test_orthogonalize_sizes(rows, cols):
     x = rand((rows, cols), rows * 1000 + cols)
     R.check_orth(M.orthogonalize(x), x)
