@@ -403,18 +403,23 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
 static hipError_t muon_norm(neox_muon* h, hipStream_t stream) {
     const StepLaunch& s = h->sl;
     return launch_norm(s.dtype, s.norm_nt, s.norm_big, s.norm_chunks, s.nnorm, s.norm_blocks, s.st, s.partial,
-                       nullptr, s.norm_big ? s.lds.norm_big : s.lds.norm, stream);
+                       s.snap, s.norm_big ? s.lds.norm_big : s.lds.norm, stream);
 }
 
 // Everything after the norm pass, from the squared norms of nparts blocks or ranks.
 static hipError_t muon_apply(neox_muon* h, const double* sumsq, uint32_t nparts, float lr, hipStream_t stream) {
-    hipError_t e = launch_finalize(sumsq, nparts, h->sl.st, h->sl.fin, stream);
+    // few enough values: the first group's momentum pass decides, from the state that the norm
+    // pass saved (same bits as the finalize)
+    const FuseIn fuse{sumsq, nparts, h->sl.snap, h->sl.st, h->sl.fin};
+    const bool fused = nparts <= kFuseMaxParts && !h->groups[0].shape.small;
+    hipError_t e = fused ? hipSuccess : launch_finalize(sumsq, nparts, h->sl.st, h->sl.fin, stream);
     for (const Group& g : h->groups) {
         if (e != hipSuccess) return e;
         const NsBuf w = ns_place(g.shape, g.count, h->d_work);
         const MuonIO io{h->d_mats + g.first, h->sl.st, h->sl.dtype, h->nesterov, h->sl.upd.b1, lr,
                         h->sl.upd.wd, g.scale, h->ns_eps};
-        e = enqueue_muon(g.shape, w, g.count, io, h->coef, h->steps, stream);
+        e = enqueue_muon(g.shape, w, g.count, io, fused && &g == &h->groups[0] ? &fuse : nullptr, h->coef, h->steps,
+                         stream);
     }
     for (const neox_muon_matrix& m : h->mats) {
         for (int t = 0; t < 2 && e == hipSuccess; ++t) {

@@ -25,6 +25,7 @@
 // larger ones with two steps at a time or rank 1 (64 rows: up to 5e-3 at rank 1).
 #include "matrix_internal.h"
 #include "tile_core.h"
+#include "zero1_decide.h"
 
 #include <algorithm>
 
@@ -121,10 +122,22 @@ __device__ __forceinline__ float direction(const MuonIO& io, float g, float m) {
     return io.nesterov ? __builtin_fmaf(io.mu, m, g) : m;
 }
 
-__global__ __launch_bounds__(kNormThreads) void muon_momentum_kernel(MuonIO io, uint64_t numel,
+// DECIDE: every block takes the step's decisions itself, from at most kFuseMaxParts squared
+// norms, and block 0 writes the state for the launches behind (saves the finalize launch, 4.7
+// of the 91 us that four 256 x 256 matrices take).
+template <bool DECIDE>
+__global__ __launch_bounds__(kNormThreads) void muon_momentum_kernel(MuonIO io, Fuse fuse, uint64_t numel,
                                                                      uint32_t parts, double* __restrict__ part) {
-    if (io.st->skip) return;
-    const float gs = io.st->gscale;
+    float gs;
+    if constexpr (DECIDE) {
+        const Decision d = fused_decide(fuse);
+        if (blockIdx.x == 0 && threadIdx.x == 0) write_state(fuse.st, d.next);
+        if (d.next.skip) return;
+        gs = d.next.gscale;
+    } else {
+        if (io.st->skip) return;
+        gs = io.st->gscale;
+    }
     const uint32_t z = blockIdx.x / parts, p = blockIdx.x % parts;
     const MuonMat mat = io.mats[z];
     double s = 0.0;
@@ -373,7 +386,7 @@ struct GramSplit {
 using Core64 = TileCore<64, 64, 2, 2, false, 4>;
 __global__ __launch_bounds__(Core64::NT) void gram_part_kernel(GramSplit g, const DevState* st) {
     if (skipped(st)) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Core64::kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[room<Core64>()];
     const uint32_t side = g.mp / 64, tiles = side * (side + 1) / 2;
     const uint32_t t = blockIdx.x % tiles, zp = blockIdx.x / tiles, z = zp / g.parts, part = zp % g.parts;
     TileAt at{};
@@ -392,7 +405,7 @@ __global__ __launch_bounds__(Core64::NT) void gram_part_kernel(GramSplit g, cons
 }
 __global__ __launch_bounds__(Core64::NT) void gram_join_kernel(GramSplit g, const DevState* st) {
     if (skipped(st)) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Core64::kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[room<Core64>()];
     const uint32_t side = g.mp / 64, tiles = side * (side + 1) / 2;
     const uint32_t t = blockIdx.x % tiles, z = blockIdx.x / tiles;
     TileAt at{};
@@ -435,20 +448,30 @@ struct Sym {
         const uint64_t sz = (uint64_t)at.z * mp * mp, dz = (uint64_t)at.z * mp;
         const uint16_t *lo = l.a + sz, *mo = SAME ? lo : m.a + sz;
         const float *ld = l.d + dz, *md = SAME ? ld : m.d + dz;
+        auto fetch = [&](const P& p) {
+            P::Down::load(p.l0, lo + (uint64_t)p.j * mp + p.i, mp);
+            if (!SAME) P::Down::load(p.l1, mo + (uint64_t)p.j * mp + p.i, mp);
+        };
         Core t;
+        if constexpr (P::kEarly) fetch(P(at, 0, lds));
         t.run(rows_of(lo, at.i, mp, Core::BP), rows_of(mo, at.j, mp, Core::BQ), mp * 2, lds);
 #pragma unroll
         for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
             const P p(at, u0, lds);
-            P::Down::load(p.l0, lo + (uint64_t)p.j * mp + p.i, mp);
-            if (!SAME) P::Down::load(p.l1, mo + (uint64_t)p.j * mp + p.i, mp);
-            wave_wait();
+            if constexpr (!P::kEarly) fetch(p);
+            tf32x4 dd[P::kU];
+            float ee[P::kV];
+#pragma unroll
+            for (int u = 0; u < P::kU; ++u) dd[u] = *(const tf32x4*)(ld + p.i + 16 * u + p.li);
+#pragma unroll
+            for (int v = 0; v < P::kV; ++v) ee[v] = md[p.j + 16 * v + p.lj];
+            if constexpr (!P::kEarly) wave_wait();
 #pragma unroll
             for (int u = 0; u < P::kU; ++u) {
-                const tf32x4 di = *(const tf32x4*)(ld + p.i + 16 * u + p.li);
+                const tf32x4 di = dd[u];
 #pragma unroll
                 for (int v = 0; v < P::kV; ++v) {
-                    const float ej = md[p.j + 16 * v + p.lj];
+                    const float ej = ee[v];
                     const f16x4 o = *p.down(p.l0, u, v);
                     tf32x4& y = t.acc[u0 + u][v];
 #pragma unroll
@@ -487,19 +510,27 @@ struct Apply {
         const uint64_t xz = (uint64_t)at.z * mp * np;
         const uint16_t* b = by.a + (uint64_t)at.z * mp * mp;
         const uint16_t* xt = xin + xz;
+        auto fetch = [&](const P& p) {
+            const uint64_t down = xz + (uint64_t)p.j * mp + p.i;
+            P::Down::load(p.l0, xin + down, mp);
+            P::Down::load(p.l1, rest + down, mp);
+        };
         Core t;
+        if constexpr (P::kEarly) fetch(P(at, 0, lds));
         t.run(rows_of(b, at.i, mp, Core::BP), rows_of(xt, at.j, mp, Core::BQ), mp * 2, lds);
         const float* db = by.d + (uint64_t)at.z * mp;
 #pragma unroll
         for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
             const P p(at, u0, lds);
             const uint64_t down = xz + (uint64_t)p.j * mp + p.i;
-            P::Down::load(p.l0, xin + down, mp);
-            P::Down::load(p.l1, rest + down, mp);
-            wave_wait();
+            if constexpr (!P::kEarly) fetch(p);
+            tf32x4 dd[P::kU];
+#pragma unroll
+            for (int u = 0; u < P::kU; ++u) dd[u] = *(const tf32x4*)(db + p.i + 16 * u + p.li);
+            if constexpr (!P::kEarly) wave_wait();
 #pragma unroll
             for (int u = 0; u < P::kU; ++u) {
-                const tf32x4 d = *(const tf32x4*)(db + p.i + 16 * u + p.li);
+                const tf32x4 d = dd[u];
 #pragma unroll
                 for (int v = 0; v < P::kV; ++v) {
                     f16x4 *ph = p.down(p.l0, u, v), *pl = p.down(p.l1, u, v);
@@ -607,13 +638,8 @@ struct Last {
         const float* db = by.d + (uint64_t)at.z * mp;
         const TileRows br = rows_of(b, TALL ? at.i : at.j, mp, TALL ? Core::BP : Core::BQ);
         const TileRows xr = rows_of(xt, TALL ? at.j : at.i, mp, TALL ? Core::BQ : Core::BP);
-        Core t;
-        t.run(TALL ? br : xr, TALL ? xr : br, mp * 2, lds);
-        const Dst dst(io, s, at.z, inv_s);
         using P = Piece<Core>;
-#pragma unroll
-        for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
-            const P p(at, u0, lds);
+        auto fetch = [&](const P& p) {
             if constexpr (TALL) {
                 // D rows are i: four i of one j
                 P::Down::load(p.l0, xt + (uint64_t)p.j * mp + p.i, mp);
@@ -623,7 +649,18 @@ struct Last {
                 P::Down::load(p.l0, xh + (uint64_t)p.j * np + p.i, np);
                 P::Across::load(p.l1, lt + (uint64_t)p.i * mp + p.j, mp);
             }
-            wave_wait();
+        };
+        Core t;
+        if constexpr (P::kEarly) fetch(P(at, 0, lds));
+        t.run(TALL ? br : xr, TALL ? xr : br, mp * 2, lds);
+        const Dst dst(io, s, at.z, inv_s);
+#pragma unroll
+        for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
+            const P p(at, u0, lds);
+            if constexpr (!P::kEarly) {
+                fetch(p);
+                wave_wait();
+            }
 #pragma unroll
             for (int u = 0; u < P::kU; ++u) {
                 const uint32_t i = p.i + 16 * u + p.li;
@@ -672,11 +709,13 @@ struct Last {
 using Core256 = TileCore<256, 256, 2, 4, false>;
 using Core128w = TileCore<128, 128, 2, 4, false>;      // quarters, by the same 512 threads
 using Core128 = TileCore<128, 128, 2, 2, false>;
+using Core32 = TileCore<32, 32, 1, 1, false, 4>;
+
 template <class Op, class Full, class Quarter>
 __global__ __launch_bounds__(Full::NT, 2) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
     static_assert(Full::NT == Quarter::NT && Full::kLds >= Quarter::kLds && Full::BP == 2 * Quarter::BP, "");
     if (skipped(st)) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Full::kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[room<Full>() > room<Quarter>() ? room<Full>() : room<Quarter>()];
     const TileAt at = place<Op::SYM>(m);
     if (at.full) op.template tile<Full>(at, lds);
     else if (!at.none) op.template tile<Quarter>(at, lds);
@@ -684,7 +723,7 @@ __global__ __launch_bounds__(Full::NT, 2) void ns_mixed_kernel(Op op, const DevS
 template <class Op, class Core>
 __global__ __launch_bounds__(Core::NT) void ns_even_kernel(Op op, const DevState* st, uint32_t mp, uint32_t np) {
     if (skipped(st)) return;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[room<Core>()];
     op.template tile<Core>(place_even<Core, Op::SYM>(mp, np), lds);
 }
 
@@ -934,7 +973,9 @@ hipError_t launch_small(const NsShape& s, uint32_t count, const IO& io, const Ns
 // The tiles are chosen by what the launch would take per 128 bytes of K, from times measured on
 // the full chip (us per slab): a round of 256 x 256 tiles (one block a CU) 1.45, of their
 // quarters 0.5; a round of 128 x 128 tiles 0.56 (two blocks on a CU take twice that), of their
-// quarters 0.2; 64 x 64 tiles 0.23 where each CU has one, 0.2 a round otherwise.  Results do
+// quarters 0.2; 64 x 64 tiles 0.23 where each CU has one, 0.2 a round otherwise.  Below one
+// block a CU the time is a block's own, which goes by the bytes it loads: 32 x 32 tiles of one
+// wave while each has a CU (512 x 512 x 1024: 5.3 us, 6.3 with 64 x 64 ones).  Results do
 // not depend on the choice: every element's products are added in the same order.
 template <class Op>
 hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_t np, uint32_t count,
@@ -945,11 +986,14 @@ hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_
     double c128 = 0.0, c256 = 1e300;
     uint64_t b128 = 0, b256 = 0;
     TileMap m256{};
-    const TileMap m128 = plan_tiles(128, Op::SYM, mp, np, count, 0.56, 0.2, &c128, &b128);
+    const TileMap m128 = plan_tiles(128, Op::SYM, mp, np, count, 0.56, 0.24, &c128, &b128);
     // quarters of the large tile are not cut
     if (mp % 128 == 0 && np % 128 == 0)
         m256 = plan_tiles(256, Op::SYM, mp, np, count, 1.45, 0.5, &c256, &b256);
-    if (c64 <= c128 && c64 <= c256)
+    const uint64_t p32 = mp / 32, q32 = np / 32, n32 = (Op::SYM ? p32 * (p32 + 1) / 2 : p32 * q32) * count;
+    if (n32 <= kCUs)
+        ns_even_kernel<Op, Core32><<<(uint32_t)n32, Core32::NT, 0, stream>>>(op, st, mp, np);
+    else if (c64 <= c128 && c64 <= c256)
         ns_even_kernel<Op, Core64><<<(uint32_t)n64, Core64::NT, 0, stream>>>(op, st, mp, np);
     else if (c128 < c256)
         ns_mixed_kernel<Op, Core128, Core64><<<(uint32_t)b128, Core128::NT, 0, stream>>>(op, st, m128);
@@ -1023,9 +1067,15 @@ hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const 
 }
 
 hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const MuonIO& io,
-                        const NsCoef* coef, int steps, hipStream_t stream) {
+                        const FuseIn* decide, const NsCoef* coef, int steps, hipStream_t stream) {
     if (s.small) return launch_small<MuonIO, MuonIn, MuonDst>(s, count, io, coef, steps, stream);
-    muon_momentum_kernel<<<s.parts * count, kNormThreads, 0, stream>>>(io, (uint64_t)s.rows * s.cols, s.parts, w.part);
+    const uint64_t numel = (uint64_t)s.rows * s.cols;
+    if (decide) {
+        const Fuse f{decide->partial, decide->nparts, decide->snap, decide->st, decide->fin};
+        muon_momentum_kernel<true><<<s.parts * count, kNormThreads, 0, stream>>>(io, f, numel, s.parts, w.part);
+    } else {
+        muon_momentum_kernel<false><<<s.parts * count, kNormThreads, 0, stream>>>(io, Fuse{}, numel, s.parts, w.part);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return enqueue_steps<MuonIO, MuonSrc, MuonDst>(s, w, count, io, coef, steps, stream);

@@ -443,8 +443,12 @@ struct Piece {
     static constexpr int kU = Core::TP < 4 ? Core::TP : 4, kV = Core::TQ;
     using Down = Patch<16 * kV, 16 * kU>;       // rows are D's columns: an array [j][i]
     using Across = Patch<16 * kU, 16 * kV>;     // rows are D's rows: [i][j]
-    static constexpr int kBytes = Down::kBytes;
-    static_assert(2 * kBytes <= Core::kLds / (Core::NT / 64), "two patches per wave");
+    static constexpr int kBytes = Down::kBytes, kWaves = Core::NT / 64;
+    // Small tiles' patches have LDS of their own behind the tile's, so that they can be loaded
+    // before the products instead of after them.
+    static constexpr bool kEarly = Core::BP <= 64 && !Core::FP4;
+    static constexpr int kPart = kEarly ? 2 * kBytes : Core::kLds / kWaves;
+    static_assert(kEarly || 2 * kBytes <= kPart, "two patches per wave");
     uint32_t i, j;         // first row and column in the matrix
     uint32_t li, lj;       // this lane's first row and its column within 16 x 16
     uint8_t *l0, *l1;      // LDS of two patches
@@ -456,7 +460,7 @@ struct Piece {
         lj = lane & 15;
         // (scalar, so that the patches' places and what follows from them are)
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        l0 = lds + wave * (Core::kLds / (Core::NT / 64));
+        l0 = lds + (kEarly ? Core::kLds : 0) + wave * kPart;
         l1 = l0 + kBytes;
     }
     // The places of tile (u, v)'s elements of this lane, and of their transposes, in a patch.
@@ -487,6 +491,12 @@ __device__ __forceinline__ float load_elem(const void* p, int dtype, uint64_t i)
 __device__ __forceinline__ void store_elem(void* p, int dtype, uint64_t i, float x) {
     if (dtype == NEOX_F32) ((float*)p)[i] = x;
     else ((uint16_t*)p)[i] = float_to_half(dtype, x);
+}
+
+// LDS of a block that works on Core's tiles.
+template <class Core>
+constexpr int room() {
+    return Core::kLds + (Piece<Core>::kEarly ? Piece<Core>::kWaves * Piece<Core>::kPart : 0);
 }
 
 }  // namespace nz1
