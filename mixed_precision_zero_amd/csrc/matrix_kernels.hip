@@ -814,6 +814,18 @@ struct MuonIn {
     }
 };
 
+// A 16 x 16 result tile on the diagonal: the diagonal to d[0 .. 15], zeros in its place.
+__device__ __forceinline__ void take_diagonal(tf32x4& x, float* d) {
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15;
+    if (l16 / 4 != lane >> 4) return;
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e)
+        if (l16 % 4 == e) {
+            d[l16] = x[e];
+            x[e] = 0.0f;
+        }
+}
+
 template <class IO, class In, class Dst, int MP, int NP, int WP, int WQ>
 __global__ __launch_bounds__(WP * WQ * 64) void ns_small_kernel(IO io, NsShape s, NsSteps steps) {
     if (skipped(state_of(io))) return;
@@ -882,12 +894,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ns_small_kernel(IO io, NsShape s
             for (int v = 0; v < SQ; ++v) {
                 const uint32_t i = pi + 16 * u + 4 * g, j = qs + 16 * v + l16;
                 a[u][v] = a[u][v] * inv_s2;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (i + e == j) {
-                        da[j] = a[u][v][e];
-                        a[u][v][e] = 0.0f;
-                    }
+                if (pi + 16 * u == qs + 16 * v) take_diagonal(a[u][v], da + qs + 16 * v);
                 o[u][v] = pack4(a[u][v]);
                 *quad_at<TB>(la, j, i) = o[u][v];
             }
@@ -899,18 +906,20 @@ __global__ __launch_bounds__(WP * WQ * 64) void ns_small_kernel(IO io, NsShape s
 #pragma unroll
             for (int v = 0; v < SQ; ++v) {
                 const uint32_t i = pi + 16 * u + 4 * g, j = qs + 16 * v + l16;
+                const tf32x4 di = *(const tf32x4*)(da + i);
                 const float dj = da[j];
                 tf32x4 b;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const bool diag = i + e == j;
                     const float off = (float)o[u][v][e];
-                    float q = __builtin_fmaf(da[i + e] + dj, off, a[u][v][e]);
-                    if (diag) q = __builtin_fmaf(dj, dj, q);
-                    b[e] = __builtin_fmaf(steps.c[k].c, q, steps.c[k].b * (diag ? dj : off));
-                    if (diag) {
-                        db[j] = b[e];
-                        b[e] = 0.0f;
+                    b[e] = __builtin_fmaf(steps.c[k].c, __builtin_fmaf(di[e] + dj, off, a[u][v][e]), steps.c[k].b * off);
+                }
+                if (pi + 16 * u == qs + 16 * v) {
+                    // on the diagonal O is 0 and D_i^2, b D_i and a are to be added
+                    take_diagonal(b, db + qs + 16 * v);
+                    if (l16 / 4 == g) {
+                        const float more = __builtin_fmaf(steps.c[k].c * dj, dj, steps.c[k].b * dj) + steps.c[k].a;
+                        db[j] += more;
                     }
                 }
                 *quad_at<TB>(lb, j, i) = pack4(b);
@@ -920,13 +929,13 @@ __global__ __launch_bounds__(WP * WQ * 64) void ns_small_kernel(IO io, NsShape s
         tf32x4 y[TP][TQ];
         lds_product<TP, TQ, TB>(y, lb, pi, xt, qj);
 #pragma unroll
-        for (int u = 0; u < TP; ++u)
+        for (int u = 0; u < TP; ++u) {
+            const tf32x4 d = *(const tf32x4*)(db + pi + 16 * u + 4 * g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float d = steps.c[k].a + db[pi + 16 * u + 4 * g + e];
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-                for (int v = 0; v < TQ; ++v) x[u][v][e] = __builtin_fmaf(d, x[u][v][e], y[u][v][e]);
-            }
+                for (int v = 0; v < TQ; ++v) x[u][v][e] = __builtin_fmaf(d[e], x[u][v][e], y[u][v][e]);
+        }
         __syncthreads();                               // everybody has read B and X^T
         if (k + 1 < steps.n) {
             spread_x();
