@@ -40,8 +40,10 @@ extern "C" {
  * Arithmetic: products of FP16 operands summed in FP32.  The iterate is carried as a pair
  * of FP16 numbers (22 bits) of which only the product terms see the first alone, and the
  * diagonals of A and of b A + c A A are kept in FP32.  The result differs from the
- * polynomial in exact arithmetic by about 1e-3 of its norm, whatever the singular values
- * of G are (the sum X Y of a rank-1 G too), besides the rounding to the output type.
+ * polynomial in exact arithmetic by 2e-4 to 2e-3 of its norm, besides the rounding to the
+ * output type, whether G's singular values are alike, decay or mostly vanish; by up to 5e-3
+ * where a matrix of 64 rows or less has rank 1.  The order of all sums depends on the shape
+ * and the coefficients only, not on the batch: each matrix gets the same bits as alone.
  * ------------------------------------------------------------------------------------ */
 #define NEOX_NS_MAX_STEPS 16
 typedef struct neox_ns_config {
@@ -54,21 +56,27 @@ typedef struct neox_ns_config {
 /* 5 steps of (3.4445, -4.7750, 2.0315), eps 1e-7.  Host only. */
 int neox_ns_default_config(neox_ns_config* cfg);
 
-/* Bytes of device workspace neox_orthogonalize needs for `count` rows x cols matrices
- * (about 8 per element and 4 per element of a smaller-side square, each side rounded up to
- * a tile).  Host only. */
+/* Bytes of device workspace neox_orthogonalize needs for `count` rows x cols matrices, for
+ * any coefficients: 8 per element and 4 per element of a smaller-side square (6 where the
+ * larger side is at least twice the smaller one and that is above 512), each side rounded
+ * up to a multiple of 64 or 128, and the partial sums: 2 KB a matrix, with a smaller side of
+ * up to 512 and a larger one of 2,048 or more up to 3 MB.  Host only. */
 int neox_orthogonalize_workspace(uint64_t count, uint64_t rows, uint64_t cols, uint64_t* bytes);
 
 /* Orthogonalise `count` rows x cols matrices.  Matrix i starts at element i * src_stride
  * of src and i * dst_stride of dst; element (r, c) of it is r * ld + c further.  Types are
- * NEOX_F16, NEOX_BF16 or NEOX_F32.  dst may be src (same type, ld and stride) and must not
- * overlap it otherwise.  The workspace (256-byte aligned, at least the size above) holds
- * nothing between calls; two calls that may run at the same time need two.
+ * NEOX_F16, NEOX_BF16 or NEOX_F32.  The matrices may lie one behind the other or side by
+ * side in rows of ld (src's may also overlap, or be one matrix with stride 0).  dst may be
+ * src (same type, ld and stride); otherwise the memory from its first to its last element
+ * must not meet src's, nor either the workspace.  The workspace (256-byte aligned, at least
+ * the size above) holds nothing between calls; two calls that may run at the same time,
+ * replays of graphs that hold them too, need two.
  * Errors: NEOX_EINVAL (null or misaligned pointer, a size of 0 or above 2^20 rows or cols,
- * count above 2^24, ld < cols, matrices of dst that overlap (dst_stride too small with
- * count > 1), unknown type, non-finite scale, workspace too small, coefficients that are
- * not finite or take a singular value in (0, 1] above 8 in magnitude on the way),
- * NEOX_EHIP. */
+ * count above 2^24, ld < cols, an ld or stride that passes 2^60 elements in all, matrices
+ * of dst that overlap, memory that meets where it must not, unknown type, non-finite scale,
+ * workspace too small, steps or eps out of range, coefficients that are not finite in FP32,
+ * make |b| t^2 + |c| t^4 larger than 30000 for the largest singular value t a step can
+ * meet, or take a singular value in (0, 1] above 8 in magnitude on the way), NEOX_EHIP. */
 int neox_orthogonalize(const neox_ns_config* cfg, const void* src, int32_t src_dtype,
                        uint64_t src_ld, uint64_t src_stride, void* dst, int32_t dst_dtype,
                        uint64_t dst_ld, uint64_t dst_stride, uint64_t count, uint64_t rows,
@@ -83,7 +91,7 @@ int neox_orthogonalize(const neox_ns_config* cfg, const void* src, int32_t src_d
  *     U = g + beta1 M (nesterov) or M
  *     W <- W - lr (s NS(U) + wd W)          (wd on matrices with NEOX_SEG_DECAY)
  *     half = W rounded, MXFP4 copies = W quantised
- * with the loss scaling, skip on inf/NaN, pre-divide, clipping, counters and resume fields
+ * (NS: neox_orthogonalize's polynomial of U) with the loss scaling, skip on inf/NaN, pre-divide, clipping, counters and resume fields
  * of neox_zero1_step, taken from the same configuration struct, and s by scale_mode.  A
  * skipped step writes nothing but the state.
  * ------------------------------------------------------------------------------------ */
@@ -125,10 +133,11 @@ typedef struct neox_muon neox_muon;
 int neox_muon_default_config(neox_muon_config* cfg);
 
 /* Create a step handle.  cfg's beta1 is the momentum; its beta2, eps, optimizer,
- * chunk_elems, norm_blocks and chunked_update are checked as neox_zero1_create does and
- * otherwise unused; segment_norms must be 0.  Arrays stay the caller's; the rules of
+ * norm_blocks and chunked_update are checked as neox_zero1_create does and otherwise unused
+ * (chunk_elems shapes the norm pass only); segment_norms must be 0.  Arrays stay the caller's; the rules of
  * neox_zero1_create on overlap and lifetime hold, for the MXFP4 copies too.  The handle
- * owns its workspace, so one handle's steps must not run at the same time as one another.
+ * owns its workspace, so one handle's steps, replays of graphs that captured them among
+ * them, must not run at the same time as one another.
  * Waits for hip_stream.
  * Errors: as neox_zero1_create and neox_orthogonalize; NEOX_EINVAL for half a pair of
  * MXFP4 pointers or a misaligned one (codes 16 bytes, scales 4). */
@@ -143,7 +152,9 @@ int neox_muon_step(neox_muon* h, float lr, void* hip_stream);
  * neox_zero1_step_local / neox_zero1_step_apply: over data-parallel ranks, or over the
  * handles of one rank (its matrices here, its other parameters in a neox_zero1 handle), or
  * both.  Handles with the same configuration that are given the same values in the same
- * order skip together and clip alike. */
+ * order skip together and clip alike.  As there, the step's scaler state is the one its
+ * step_local started from: give every step_apply its own step_local, and call
+ * neox_muon_scaler_set between steps. */
 int neox_muon_step_local(neox_muon* h, double* local_sumsq, void* hip_stream);
 int neox_muon_step_apply(neox_muon* h, const double* rank_sumsq, uint32_t nranks, float lr,
                          void* hip_stream);
@@ -172,28 +183,33 @@ int neox_muon_destroy(neox_muon* h);
  * of a row consists of the row's last cols % 32 elements and zeros.
  * ------------------------------------------------------------------------------------ */
 
-/* Bytes of the codes and the scales of a rows x cols copy.  Host only. */
+/* Bytes of the codes and the scales of a rows x cols copy.  Host only.  Errors: NEOX_EINVAL
+ * (null, a size of 0 or above 2^31 - 1, codes of more than 2^40 bytes). */
 int neox_mxfp4_layout(uint64_t rows, uint64_t cols, uint64_t* code_bytes, uint64_t* scale_bytes);
 
 /* Quantise the rows x cols matrix src (element (r, c) at r * ld + c), or with transpose = 1
  * its transpose: then the copy is cols x rows, with blocks along src's columns.
- * codes 16-byte aligned, scales 4-byte aligned; neither may overlap src.
- * Errors: NEOX_EINVAL (null, misaligned, a size of 0 or above 2^31 - 1, ld < cols, unknown
- * type, transpose not 0 or 1), NEOX_EHIP. */
+ * codes 16-byte aligned, scales 4-byte aligned.
+ * Errors: NEOX_EINVAL (null, misaligned, a size of 0 or above 2^31 - 1, codes of more than
+ * 2^40 bytes, ld < cols or above 2^60 / rows, unknown type, transpose not 0 or 1, codes,
+ * scales and the memory from src's first to its last element not apart), NEOX_EHIP. */
 int neox_mxfp4_quantize(const void* src, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t ld,
                         int32_t transpose, void* codes, void* scales, void* hip_stream);
 
 /* The values of a rows x cols copy, rounded to dtype, to dst (element (r, c) at r * ld + c).
- * Errors: as neox_mxfp4_quantize. */
+ * Values above the type's range become infinite.  Errors: as neox_mxfp4_quantize. */
 int neox_mxfp4_dequantize(const void* codes, const void* scales, uint64_t rows, uint64_t cols,
                           void* dst, int32_t dtype, uint64_t ld, void* hip_stream);
 
 /* c[i][j] = sum over k of a[i][k] b[j][k] for an m x k copy a and an n x k copy b, summed in
  * FP32 in an order that depends on the sizes only, rounded to dtype (NEOX_F16, NEOX_BF16,
- * NEOX_F32) and written to c[i * ldc + j].  With W of shape (out, in): y = x W^T is
+ * NEOX_F32) and written to c[i * ldc + j].  Elements between k and the next multiple of 128
+ * are read: zeros, as quantisation writes them, in copies made elsewhere too.  A block that
+ * reads as NaN makes its row's or column's results NaN.  With W of shape (out, in): y = x W^T is
  * (x, W); dx = dy W is (dy, transpose copy of W); dW = dy^T x is (transpose copies of dy
- * and x).  Errors: NEOX_EINVAL (null, misaligned, a size of 0 or above 2^31 - 1, ldc < n,
- * unknown type), NEOX_EHIP. */
+ * and x).  Errors: NEOX_EINVAL (null, misaligned, a size of 0 or above 2^31 - 1, k above
+ * 2^24, codes of more than 2^40 bytes, 2^24 or more 128 x 128 tiles of c, ldc < n, unknown
+ * type, c meeting an operand), NEOX_EHIP. */
 int neox_mxfp4_product(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
                        const void* b_scales, uint64_t n, uint64_t k, void* c, int32_t dtype,
                        uint64_t ldc, void* hip_stream);

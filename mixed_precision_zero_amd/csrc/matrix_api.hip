@@ -57,7 +57,7 @@ int ns_coefs(const neox_ns_config* c, NsCoef* coef, bool* pairs) {
     *pairs = true;
     for (int k = 0; k < c->steps; ++k) {
         const double a = c->coef[k][0], b = c->coef[k][1], d = c->coef[k][2];
-        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(d))
+        if (!std::isfinite((float)a) || !std::isfinite((float)b) || !std::isfinite((float)d))
             return set_error(NEOX_EINVAL, "step %d: coefficients are not finite", k);
         // what the FP16 copies hold: elements of A up to top^2, of b A + c A A up to this
         if (std::fabs(b) * top * top + std::fabs(d) * top * top * top * top > 30000.0)
@@ -147,7 +147,9 @@ extern "C" int neox_orthogonalize(const neox_ns_config* cfg, const void* src, in
     if (src_ld > lim / rows || dst_ld > lim / rows || src_stride > lim / count || dst_stride > lim / count)
         return set_error(NEOX_EINVAL, "ld or stride too large");
     const uint64_t span = (rows - 1) * dst_ld + cols, sspan = (rows - 1) * src_ld + cols;
-    if (count > 1 && dst_stride < span) return set_error(NEOX_EINVAL, "matrices of dst overlap");
+    // one behind the other, or side by side in rows of dst_ld
+    const bool beside = dst_stride >= cols && (rows == 1 || dst_stride <= (dst_ld - cols) / (count > 1 ? count - 1 : 1));
+    if (count > 1 && dst_stride < span && !beside) return set_error(NEOX_EINVAL, "matrices of dst overlap");
     const uint64_t slen = ((count - 1) * src_stride + sspan) * sb, dlen = ((count - 1) * dst_stride + span) * db;
     const uintptr_t s0 = (uintptr_t)src, d0 = (uintptr_t)dst, w0 = (uintptr_t)workspace;
     const bool same = s0 == d0 && src_dtype == dst_dtype && src_ld == dst_ld &&

@@ -368,12 +368,14 @@ __global__ __launch_bounds__(WK * 64) void product_thin_kernel(ProductArgs a) {
 
 // Blocks of one launch: a grid has fewer than 2^32 threads.
 constexpr uint64_t kGrid = 1ull << 23;
+// Rows of a transposed copy, or of b in the product of few rows, that a launch takes.
+constexpr uint64_t kMostRows = 1ull << 22;
 
 // Launches f(first row, rows, their spread) for as many rows at a time as a grid takes.
 template <class F>
 static void rows_in_grids(uint64_t rows, uint64_t units, uint32_t deep, F f) {
-    const Spread one = spread(1024, units, deep);       // blocks for 1,024 rows
-    const uint64_t most = std::max<uint64_t>(1, kGrid / one.blocks) * 1024;
+    const Spread one = spread(1, units, deep);          // (at most 2^20 blocks across)
+    const uint64_t most = kGrid / one.across * ((256u >> one.shift) * deep);
     for (uint64_t r = 0; r < rows; r += most) {
         const uint64_t n = std::min(most, rows - r);
         f(r, n, spread(n, units, deep));
@@ -395,11 +397,15 @@ hipError_t launch_mx_quantize(const void* src, int dtype, uint64_t rows, uint64_
         if (transpose) {
             auto cols = [&](auto nn) {
                 constexpr int N = decltype(nn)::value;
-                const uint32_t across = (uint32_t)((R + 64 * N - 1) / (64 * N));
-                const uint64_t down = sh.scale_pitch / 4, most = std::max<uint64_t>(1, kGrid / across);
-                for (uint64_t d = 0; d < down; d += most)
-                    quantize_cols_kernel<DT, N><<<(uint32_t)(across * std::min(most, down - d)), 256, 0, stream>>>(
-                        src, R, C, ld, (uint8_t*)codes, (uint8_t*)scales, sh, across, d, st);
+                for (uint64_t r = 0; r < R; r += kMostRows) {
+                    const uint64_t n = std::min(kMostRows, R - r);
+                    const uint32_t across = (uint32_t)((n + 64 * N - 1) / (64 * N));
+                    const uint64_t down = sh.scale_pitch / 4, most = kGrid / across;
+                    for (uint64_t d = 0; d < down; d += most)
+                        quantize_cols_kernel<DT, N><<<(uint32_t)(across * std::min(most, down - d)), 256, 0, stream>>>(
+                            (const uint8_t*)src + r * (DT == NEOX_F32 ? 4 : 2), n, C, ld,
+                            (uint8_t*)codes + r * sh.code_pitch, (uint8_t*)scales + r * sh.scale_pitch, sh, across, d, st);
+                }
             };
             if (DT != NEOX_F32 && R % 2 == 0 && ld % 2 == 0 && (uintptr_t)src % 4 == 0)
                 cols(std::integral_constant<int, DT == NEOX_F32 ? 1 : 2>{});
@@ -441,16 +447,23 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
                              uint64_t ldc, hipStream_t stream) {
     const MxShape sh = mx_shape(k);
     const uint64_t es = dtype == NEOX_F32 ? 4 : 2;
-    const ProductArgs a{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
+    ProductArgs a{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
                         (const uint8_t*)b_scales, c, ldc, (uint32_t)m, (uint32_t)n, (uint32_t)sh.code_pitch,
                         (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
     if (m <= 64) {
-        const uint32_t blocks = (uint32_t)((n + 15) / 16);
+        // enough waves for the chip: more of them share K where there are few rows of b
+        const bool many = n > 16 * (4 * kCUs - 1);
         auto run = [&](auto mt) {
             constexpr int MT = decltype(mt)::value;
-            // enough waves for the chip: more of them share K where there are few rows of b
-            if (blocks >= 4 * kCUs) product_thin_kernel<MT, 4><<<blocks, 256, 0, stream>>>(a);
-            else product_thin_kernel<MT, 16><<<blocks, 1024, 0, stream>>>(a);
+            for (uint64_t r = 0; r < n; r += kMostRows) {
+                a.n = (uint32_t)std::min(kMostRows, n - r);
+                const uint32_t blocks = (a.n + 15) / 16;
+                if (many) product_thin_kernel<MT, 4><<<blocks, 256, 0, stream>>>(a);
+                else product_thin_kernel<MT, 16><<<blocks, 1024, 0, stream>>>(a);
+                a.b_codes += kMostRows * sh.code_pitch;
+                a.b_scales += kMostRows * sh.scale_pitch;
+                a.c = (uint8_t*)a.c + kMostRows * es;
+            }
         };
         if (m <= 16) run(std::integral_constant<int, 1>{});
         else if (m <= 32) run(std::integral_constant<int, 2>{});

@@ -94,6 +94,18 @@ def test_orthogonalize_strides_and_surroundings():
     assert (rest == 9.0).all() and flat[0] == 9.0
 
 
+@pytest.mark.parametrize("rows,heads,width", [(48, 6, 16), (300, 3, 130), (700, 2, 75)])
+def test_orthogonalize_side_by_side_in_place(rows, heads, width):
+    """A projection's heads: column blocks of one matrix, whose rows lie between each other's."""
+    w = rand((rows, heads * width + 5), rows, BF16)
+    keep = w.clone()
+    blocks = w[:, :heads * width].view(rows, heads, width).transpose(0, 1)
+    want = M.orthogonalize(blocks.contiguous())
+    M.orthogonalize(blocks, out=blocks)
+    assert torch.equal(blocks, want)
+    assert torch.equal(w[:, heads * width:], keep[:, heads * width:])
+
+
 def test_orthogonalize_in_place():
     x = rand((4, 150, 90), 31)
     want = M.orthogonalize(x)
@@ -234,6 +246,27 @@ def test_copies_beyond_32_bit_offsets():
     y = M.mxfp4_product(M.MXFP4(q.codes[-40:], q.scales[-40:], 40, cols), M.MXFP4(q.codes[-9:], q.scales[-9:], 9, cols), F32)
     a = R.mx_values(q.codes[-40:], q.scales[-40:], cols)
     assert ((y.double().cpu() - a @ a[-9:].t()).abs() <= product_bound(a, a[-9:], cols)).all()
+
+
+def test_more_rows_than_one_launch_takes():
+    """A transposed copy and a product of few rows with 2^22 and some rows: the rows of each
+    launch, its first and last ones, against the same rows alone."""
+    n = (1 << 22) + 19
+    x = rand((3, 4099), 6, BF16).repeat(1, n // 4099 + 1)[:, :n].contiguous()
+    t = M.mxfp4_quantize(x, transpose=True)
+    for r0, r1 in ((0, 300), ((1 << 22) - 150, (1 << 22) + 19)):
+        codes, scales = R.mx_quantize(x[:, r0:r1].t())
+        assert torch.equal(t.codes[r0:r1].cpu(), codes) and torch.equal(t.scales[r0:r1].cpu(), scales)
+    a = M.mxfp4_quantize(rand((2, 3), 8, BF16))
+    y = M.mxfp4_product(a, t, dtype=F32)
+    for r0, r1 in ((0, 300), ((1 << 22) - 150, (1 << 22) + 19)):
+        part = M.MXFP4(t.codes[r0:r1].contiguous(), t.scales[r0:r1].contiguous(), r1 - r0, 3)
+        assert torch.equal(y[:, r0:r1], M.mxfp4_product(a, part, dtype=F32))
+        want = R.mx_values(a.codes, a.scales, 3) @ R.mx_values(part.codes, part.scales, 3).t()
+        # three products of numbers with two significant bits each: exact unless scales differ by
+        # more than 2^20, else three FP32 roundings of at most the sum of magnitudes
+        top = R.mx_values(a.codes, a.scales, 3).abs() @ R.mx_values(part.codes, part.scales, 3).abs().t()
+        assert ((y[:, r0:r1].double().cpu() - want).abs() <= 3 * 2.0 ** -24 * top).all()
 
 
 def test_quantize_leaves_what_is_behind():
@@ -482,6 +515,65 @@ def test_muon_scaler_matches_the_elementwise_step():
                 assert all(torch.equal(x[n], y[n]) for n in ("half", "master", "momentum"))
         else:
             check_step(before, ws, a, cfg, 1e-3)
+
+
+@pytest.mark.parametrize("count,shape", [(1, (130, 140)), (3, (257, 300)), (260, (130, 129))],
+                         ids=["one", "three", "many"])
+def test_muon_decisions_of_larger_matrices(count, shape):
+    """The same where the momentum pass takes the decisions (few partial norms) and where the
+    finalize does (more than 256): scaler state as neox_zero1_step's, weights as the formulas',
+    MXFP4 copies rewritten by applied steps only."""
+    kw = dict(growth_interval=2, clip_norm=0.01)
+    cfg, ws = zcfg(F16, **kw), weights([shape] * count, F16, 13)
+    copies = [(M.MXFP4.empty(*shape, DEV), M.MXFP4.empty(*shape[::-1], DEV)) for _ in ws[:2]]
+    for c, t in copies:
+        for a in (c.codes, c.scales, t.codes, t.scales):
+            a.fill_(77)
+    sgd_ws = copy_of(ws)
+    sgd = Z.Zero1(zcfg(F16, optimizer=Z.NEOX_OPT_SGD, **kw),
+                  [Z.segment(w["grad"].view(-1), w["half"].view(-1), w["master"].view(-1),
+                             w["momentum"].view(-1), None, w["decay"]) for w in sgd_ws])
+    opt = M.Muon(cfg, [M.muon_matrix(**w, **(dict(copy=copies[i][0], copy_t=copies[i][1]) if i < 2 and i < len(copies) else {}))
+                       for i, w in enumerate(ws)])
+    for k in range(4):
+        for i, (w, v) in enumerate(zip(ws, sgd_ws)):
+            g = rand(shape, 100 * k + i, sigma=1e-4) * opt.state().loss_scale
+            if k in (0, 2) and i == count - 1:
+                g[-1, -1] = math.inf
+            w["grad"].copy_(g)
+            v["grad"].copy_(w["grad"])
+        before = {"scale": opt.state().loss_scale, "w": copy_of(ws)}
+        old = [[a.clone() for a in (c.codes, c.scales, t.codes, t.scales)] for c, t in copies]
+        opt.step(1e-3)
+        sgd.step(1e-3)
+        a, b = opt.state(), sgd.state()
+        for f in ("loss_scale", "good_steps", "step", "skipped_total", "consecutive_overflows", "last_skipped",
+                  "last_grad_norm", "last_clip_coef", "last_sumsq"):
+            assert getattr(a, f) == getattr(b, f), (k, f)
+        assert a.last_skipped == (k in (0, 2))
+        if a.last_skipped:
+            for x, y in zip(ws, before["w"]):
+                assert all(torch.equal(x[n], y[n]) for n in ("half", "master", "momentum"))
+            for (c, t), o in zip(copies, old):
+                assert all(torch.equal(x, y) for x, y in zip((c.codes, c.scales, t.codes, t.scales), o))
+        else:
+            some = [0, count - 1] if count > 1 else [0]
+            check_step({"scale": before["scale"], "w": [before["w"][i] for i in some]}, [ws[i] for i in some], a, cfg, 1e-3)
+            for (c, t), w in zip(copies, ws):
+                codes, scales = R.mx_quantize(w["master"])
+                assert torch.equal(c.codes.cpu(), codes) and torch.equal(c.scales.cpu(), scales)
+                codes, scales = R.mx_quantize(w["master"].t())
+                assert torch.equal(t.codes.cpu(), codes) and torch.equal(t.scales.cpu(), scales)
+
+
+@pytest.mark.parametrize("shape", [(70, 2100), (2500, 130), (1300, 700), (1030, 2200)])
+def test_muon_step_of_other_shapes(shape):
+    """Few rows and many columns (shares of the sums), either side longer, two steps at a time."""
+    cfg, ws = zcfg(BF16), weights([shape], BF16, 17)
+    opt = M.Muon(cfg, [M.muon_matrix(**w) for w in ws])
+    before = {"scale": opt.state().loss_scale, "w": copy_of(ws)}
+    opt.step(1e-3)
+    check_step(before, ws, opt.state(), cfg, 1e-3)
 
 
 def test_muon_and_adamw_share_one_decision():

@@ -69,7 +69,8 @@ def orth(cfg=None, src=A, st=M.NEOX_F32, sld=40, ss=4000, dst=A + GAP, dt=M.NEOX
     ("types", dict(st=0)), ("types", dict(dt=4)), ("misaligned", dict(src=A + 2)),
     ("misaligned", dict(dst=A + GAP + 1)), ("256-byte", dict(work=A + 2 * GAP + 128)),
     ("needed", dict(nbytes=1000)), ("smaller than cols", dict(sld=39)), ("smaller than cols", dict(dld=39)),
-    ("overlap", dict(ds=1199)), ("a matrix of", dict(rows=0)), ("a matrix of", dict(cols=0)),
+    ("overlap", dict(ds=1199)), ("overlap", dict(dld=100, ds=39)), ("overlap", dict(dld=100, ds=61)),
+    ("overlap", dict(dld=130, ds=60, count=3)), ("a matrix of", dict(rows=0)), ("a matrix of", dict(cols=0)),
     ("a matrix of", dict(rows=(1 << 20) + 1)), ("count", dict(count=0)), ("count", dict(count=(1 << 24) + 1)),
     ("scale", dict(scale=math.inf)), ("scale", dict(scale=math.nan)), ("scale", dict(scale=1e39)),
     ("overlaps src", dict(dst=A)), ("overlaps src", dict(dst=A, dt=M.NEOX_F32, ds=4001)),
@@ -85,7 +86,7 @@ def test_orthogonalize_refuses(text, kw):
     ("steps", dict(steps=0)), ("steps", dict(steps=17)), ("eps", dict(eps=0.0)), ("eps", dict(eps=math.nan)),
     ("eps", dict(eps=1e-60)), ("not finite", dict(coef=(math.inf, 0.0, 0.0))),
     ("grow", dict(coef=(9.0, 0.0, 0.0))), ("grow", dict(coef=(2.1, 0.0, 0.0))),
-    ("too large", dict(coef=(1.0, 1e6, 0.0))),
+    ("too large", dict(coef=(1.0, 1e6, 0.0))), ("not finite", dict(coef=[(0.0, 0.0, 0.0), (1.0, 1e60, 0.0)])),
 ])
 def test_orthogonalize_refuses_steps(text, change):
     refuses(text, orth, cfg=M.neox_ns_default_config(**change))
@@ -115,6 +116,11 @@ def test_coefficients_that_stay_bounded_are_taken():
     """Known step polynomials pass the coefficients' check (the call stops at the workspace)."""
     for coef in ((3.4445, -4.7750, 2.0315), (1.5, -0.5, 0.0), (15 / 8, -10 / 8, 3 / 8), (2.0, -1.5, 0.5)):
         refuses("needed", orth, cfg=M.neox_ns_default_config(coef=coef), nbytes=0)
+
+
+def test_matrices_side_by_side_are_taken():
+    for kw in (dict(dld=100, ds=60), dict(dld=120, ds=40, count=3), dict(dld=40, ds=40, rows=1)):
+        refuses("scale", orth, scale=math.inf, **kw)          # (the check behind those of the layout)
 
 
 @pytest.mark.parametrize("count,rows,cols", [(1, 1, 1), (3, 1000, 37), (1, 1 << 20, 5), (64, 64, 64)])
