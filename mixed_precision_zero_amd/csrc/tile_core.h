@@ -13,6 +13,12 @@
 // load writes LDS in lane order, so the swizzle is applied to the global address instead.
 // Which K elements meet in which instruction is free as long as both operands agree: the
 // lane group g takes chunks 2g and 2g + 1 of a slab, so its two MXFP4 scales are adjacent.
+//
+// Measured, all tiles whole: FP16 8192 x 8192 x 4096 on 256 x 256 tiles 1.28 to 1.38 PFLOP/s
+// (a library product of 8192^3 reaches 1.43, products from registers alone 2.13), on 128 x 128
+// ones 1.1; MXFP4 8192 x 8192 x 16384 4.2 to 4.4 and 3.5.  The matrix units are busy 64% of the
+// time in FP16; LDS, from which each wave reads 8 + 4 fragments for 32 products and into which
+// the loads write, is busy nearly as long, and the two do not overlap in full.
 #pragma once
 
 #include "neox_matrix.h"
@@ -52,9 +58,13 @@ constexpr uint32_t kNowhere = 0x80000000u;      // an offset behind every operan
 // overwritten by the next half's, and the Q fragments alternate between two sets.  The reads of
 // slab s + 1 need it to have landed, so the block's one barrier per slab sits in the second
 // half of slab s, behind the first row of products (which covers the latency of slab s's last
-// reads; behind the second or third row it measured 2-3% slower).  Behind it slab s's buffer is free, and the load of slab s + NS goes there.
-// Row by row the order is pinned: left to itself the compiler reads all fragments at once,
-// which needs 252 registers instead of 240 for FP16 and spills for MXFP4.
+// reads; behind the second or third row it measured 2-3% slower).  Behind it slab s's buffer is
+// free, and the load of slab s + NS goes there.  Row by row the order is pinned: left to itself
+// the compiler reads all fragments at once and spills.  256 x 256 tiles take 8 waves of 236 to
+// 256 registers; 4 waves of twice the part would keep results in the accumulation registers
+// and copy them at each product (10 times slower).  Tried as well, of no use: slabs of 64 bytes
+// in four stages (equal, 128 x 128 tiles 20% slower), more stages, the Q fragments a row
+// earlier, waves 4 x 2, a higher wave priority in the products.
 template <int BP_, int BQ_, int WP_, int WQ_, bool FP4_, int NS_ = 2>
 struct TileCore {
     static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NS = NS_;
@@ -256,8 +266,9 @@ struct TileCore {
 // ------------------------------------------------------------------------------------
 // Blocks [0, nfull) take whole tiles of unit x unit (256 or 128); the others take quarters of
 // what is left: the tiles that would start another, mostly empty round on the chip's 256 CUs,
-// and those that the matrix's edge cuts.  Tiles of a symmetric product
-// lie on and below the diagonal, those on it last (a quarter of them above it is left out).
+// and those that the matrix's edge cuts.  Tiles of a symmetric product lie on and below the
+// diagonal, those on it last (a quarter of them above it is left out).  Neighbouring tiles on
+// one XCD: an X <- P X of 6144 x 6144 on 128 x 128 tiles took 602 us in plain order, 486 so.
 struct TileMap {
     uint32_t nfull;        // blocks with whole tiles
     uint32_t inner;        // whole tiles per matrix
@@ -346,7 +357,9 @@ __device__ __forceinline__ TileAt place(const TileMap& m) {
 
 // The launch of one product with `count` p x q results (p = q and sym for symmetric ones; a
 // cut tile reads zeros behind its operands' rows), and its cost per slab of K: `full` for a
-// round of whole tiles over the chip's CUs, `quarter` for a round of quarters.
+// round of whole tiles over the chip's CUs, `quarter` for a round of quarters.  Quarters that
+// the edge or the diagonal leaves empty are counted: they fall on the XCDs unevenly, and a cost
+// without them chose launches that took 15 to 24% longer (7 of 4096 x 1024, 6 of 1920 x 1920).
 constexpr uint32_t kCUs = 256;
 inline TileMap plan_tiles(uint32_t unit, bool sym, uint32_t p, uint32_t q, uint32_t count, double full, double quarter,
                           double* cost, uint64_t* blocks) {
