@@ -362,21 +362,20 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
     const uint32_t nnorm = (uint32_t)plan.norm_table.size();
     e = hipMalloc(&h->d_norm_chunks, nnorm * sizeof(Chunk));
     if (e == hipSuccess) e = hipMalloc(&h->d_partial, nnorm * sizeof(double));
-    if (e == hipSuccess) e = hipMalloc(&h->d_state, 2 * sizeof(DevState));
+    if (e == hipSuccess) e = hipMalloc(&h->d_state, sizeof(DevState));
     if (e == hipSuccess) e = hipMalloc(&h->d_mats, table.size() * sizeof(MuonMat));
     if (e == hipSuccess) e = hipMalloc(&h->d_work, work);
     if (e != hipSuccess)
         return e == hipErrorOutOfMemory ? set_error(NEOX_ENOMEM, "hipMalloc of library scratch (%llu bytes)",
                                                     (unsigned long long)work)
                                         : set_hip_error(e, "hipMalloc");
-    const DevState st[2] = {initial_state(*cfg, (float)cfg->init_scale, cfg->init_good_steps, cfg->init_step,
-                                          cfg->init_skipped, cfg->init_consecutive_overflows),
-                            DevState{}};
+    const DevState st = initial_state(*cfg, (float)cfg->init_scale, cfg->init_good_steps, cfg->init_step,
+                                      cfg->init_skipped, cfg->init_consecutive_overflows);
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     e = hipMemcpyAsync(h->d_norm_chunks, plan.norm_table.data(), nnorm * sizeof(Chunk), hipMemcpyHostToDevice, stream);
     if (e == hipSuccess)
         e = hipMemcpyAsync(h->d_mats, table.data(), table.size() * sizeof(MuonMat), hipMemcpyHostToDevice, stream);
-    if (e == hipSuccess) e = hipMemcpyAsync(h->d_state, st, sizeof st, hipMemcpyHostToDevice, stream);
+    if (e == hipSuccess) e = hipMemcpyAsync(h->d_state, &st, sizeof st, hipMemcpyHostToDevice, stream);
     const hipError_t es = hipStreamSynchronize(stream);
     if (e != hipSuccess || es != hipSuccess)
         return set_hip_error(e != hipSuccess ? e : es, "upload of the matrix table");
@@ -390,7 +389,6 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
     sl.norm_blocks = nnorm;
     sl.partial = h->d_partial;
     sl.st = h->d_state;
-    sl.snap = h->d_state + 1;
     sl.fin = finalize_args(*cfg);
     sl.upd = update_args(*cfg);
     h->ns_eps = mcfg->ns.eps;
@@ -405,23 +403,18 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
 static hipError_t muon_norm(neox_muon* h, hipStream_t stream) {
     const StepLaunch& s = h->sl;
     return launch_norm(s.dtype, s.norm_nt, s.norm_big, s.norm_chunks, s.nnorm, s.norm_blocks, s.st, s.partial,
-                       s.snap, s.norm_big ? s.lds.norm_big : s.lds.norm, stream);
+                       nullptr, s.norm_big ? s.lds.norm_big : s.lds.norm, stream);
 }
 
 // Everything after the norm pass, from the squared norms of nparts blocks or ranks.
 static hipError_t muon_apply(neox_muon* h, const double* sumsq, uint32_t nparts, float lr, hipStream_t stream) {
-    // few enough values: the first group's momentum pass decides, from the state that the norm
-    // pass saved (same bits as the finalize)
-    const FuseIn fuse{sumsq, nparts, h->sl.snap, h->sl.st, h->sl.fin};
-    const bool fused = nparts <= kFuseMaxParts && !h->groups[0].shape.small;
-    hipError_t e = fused ? hipSuccess : launch_finalize(sumsq, nparts, h->sl.st, h->sl.fin, stream);
+    hipError_t e = launch_finalize(sumsq, nparts, h->sl.st, h->sl.fin, stream);
     for (const Group& g : h->groups) {
         if (e != hipSuccess) return e;
         const NsBuf w = ns_place(g.shape, g.count, h->d_work);
         const MuonIO io{h->d_mats + g.first, h->sl.st, h->sl.dtype, h->nesterov, h->sl.upd.b1, lr,
                         h->sl.upd.wd, g.scale, h->ns_eps};
-        e = enqueue_muon(g.shape, w, g.count, io, fused && &g == &h->groups[0] ? &fuse : nullptr, h->coef, h->steps,
-                         stream);
+        e = enqueue_muon(g.shape, w, g.count, io, h->coef, h->steps, stream);
     }
     for (const neox_muon_matrix& m : h->mats) {
         for (int t = 0; t < 2 && e == hipSuccess; ++t) {

@@ -77,10 +77,8 @@ struct NsCoef {
 // epilogue (store, or weight update).
 hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const OrthIO& io,
                         const NsCoef* coef, int steps, hipStream_t stream);
-// decide: null, or what the momentum pass takes the step's decisions from (a shape that is not
-// small; io.st is then written by it).
 hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const MuonIO& io,
-                        const FuseIn* decide, const NsCoef* coef, int steps, hipStream_t stream);
+                        const NsCoef* coef, int steps, hipStream_t stream);
 
 // ------------------------------------------------------------------------------------
 // MXFP4

@@ -25,7 +25,6 @@
 // larger ones with two steps at a time or rank 1 (64 rows: up to 5e-3 at rank 1).
 #include "matrix_internal.h"
 #include "tile_core.h"
-#include "zero1_decide.h"
 
 #include <algorithm>
 
@@ -124,22 +123,10 @@ __device__ __forceinline__ float direction(const MuonIO& io, float g, float m) {
     return io.nesterov ? __builtin_fmaf(io.mu, m, g) : m;
 }
 
-// DECIDE: every block takes the step's decisions itself, from at most kFuseMaxParts squared
-// norms, and block 0 writes the state for the launches behind (saves the finalize launch, 4.7
-// of the 91 us that four 256 x 256 matrices take).
-template <bool DECIDE>
-__global__ __launch_bounds__(kNormThreads) void muon_momentum_kernel(MuonIO io, Fuse fuse, uint64_t numel,
-                                                                     uint32_t parts, double* __restrict__ part) {
-    float gs;
-    if constexpr (DECIDE) {
-        const Decision d = fused_decide(fuse);
-        if (blockIdx.x == 0 && threadIdx.x == 0) write_state(fuse.st, d.next);
-        if (d.next.skip) return;
-        gs = d.next.gscale;
-    } else {
-        if (io.st->skip) return;
-        gs = io.st->gscale;
-    }
+__global__ __launch_bounds__(kNormThreads) void muon_momentum_kernel(MuonIO io, uint64_t numel, uint32_t parts,
+                                                                     double* __restrict__ part) {
+    if (io.st->skip) return;
+    const float gs = io.st->gscale;
     const uint32_t z = blockIdx.x / parts, p = blockIdx.x % parts;
     const MuonMat mat = io.mats[z];
     double s = 0.0;
@@ -1091,15 +1078,10 @@ hipError_t enqueue_orth(const NsShape& s, const NsBuf& w, uint32_t count, const 
 }
 
 hipError_t enqueue_muon(const NsShape& s, const NsBuf& w, uint32_t count, const MuonIO& io,
-                        const FuseIn* decide, const NsCoef* coef, int steps, hipStream_t stream) {
+                        const NsCoef* coef, int steps, hipStream_t stream) {
     if (s.small) return launch_small<MuonIO, MuonIn, MuonDst>(s, count, io, coef, steps, stream);
     const uint64_t numel = (uint64_t)s.rows * s.cols;
-    if (decide) {
-        const Fuse f{decide->partial, decide->nparts, decide->snap, decide->st, decide->fin};
-        muon_momentum_kernel<true><<<s.parts * count, kNormThreads, 0, stream>>>(io, f, numel, s.parts, w.part);
-    } else {
-        muon_momentum_kernel<false><<<s.parts * count, kNormThreads, 0, stream>>>(io, Fuse{}, numel, s.parts, w.part);
-    }
+    muon_momentum_kernel<<<s.parts * count, kNormThreads, 0, stream>>>(io, numel, s.parts, w.part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return enqueue_steps<MuonIO, MuonSrc, MuonDst>(s, w, count, io, coef, steps, stream);

@@ -520,9 +520,9 @@ def test_muon_scaler_matches_the_elementwise_step():
 @pytest.mark.parametrize("count,shape", [(1, (130, 140)), (3, (257, 300)), (260, (130, 129))],
                          ids=["one", "three", "many"])
 def test_muon_decisions_of_larger_matrices(count, shape):
-    """The same where the momentum pass takes the decisions (few partial norms) and where the
-    finalize does (more than 256): scaler state as neox_zero1_step's, weights as the formulas',
-    MXFP4 copies rewritten by applied steps only."""
+    """The same for matrices that take many launches each, from one to more than 256 partial norms
+    (neox_zero1_step decides in its update up to there): scaler state as neox_zero1_step's,
+    weights as the formulas', MXFP4 copies rewritten by applied steps only."""
     kw = dict(growth_interval=2, clip_norm=0.01)
     cfg, ws = zcfg(F16, **kw), weights([shape] * count, F16, 13)
     copies = [(M.MXFP4.empty(*shape, DEV), M.MXFP4.empty(*shape[::-1], DEV)) for _ in ws[:2]]
