@@ -732,9 +732,9 @@ __global__ __launch_bounds__(Core::NT) void ns_even_kernel(Op op, const DevState
 //
 // Up to 128 x 128 (or 64 x 256) the iterate in both orientations, A and B fit one CU's LDS and
 // the iterate itself, in FP32, the block's registers.  The fifteen launches of the tiled form
-// would each wait for the one before (66 us for 64 matrices of 64 x 64; here 14.8 in one
-// launch).  Bound by latency: five steps of three products with a barrier behind each, about
-// 2 us a step at 64 x 64; up to 256 matrices take the same time.
+// would each wait for the one before (66 us for 64 matrices of 64 x 64; here 11.7 in one
+// launch).  Bound by latency and by how fast a wave issues: five steps of three products with
+// a barrier behind each; up to 256 matrices take the same time.
 // ------------------------------------------------------------------------------------
 struct NsSteps {
     int32_t n;
@@ -970,10 +970,14 @@ hipError_t launch_small(const NsShape& s, uint32_t count, const IO& io, const Ns
     NsSteps st{};
     st.n = steps;
     for (int k = 0; k < steps; ++k) st.c[k] = coef[k];
-    if (s.m > 64) ns_small_kernel<IO, In, Dst, 128, 128, 2, 4><<<count, 512, 0, stream>>>(io, s, st);
-    else if (s.n > 128) ns_small_kernel<IO, In, Dst, 64, 256, 2, 4><<<count, 512, 0, stream>>>(io, s, st);
-    else if (s.n > 64) ns_small_kernel<IO, In, Dst, 64, 128, 2, 2><<<count, 256, 0, stream>>>(io, s, st);
-    else ns_small_kernel<IO, In, Dst, 64, 64, 2, 2><<<count, 256, 0, stream>>>(io, s, st);
+    // Threads, us for 64 and for 2,000 matrices: 64 x 64 with 256 15.1 and 48, 512 11.7 and 48,
+    // 1,024 11.1 and 54; 64 x 128 with 256 20.6 and 96, 512 15.8 and 77, 1,024 14.6 and 107; 64 x
+    // 256 with 512 23.9 and 199, 1,024 21.8 and 175; 128 x 128 with 512 33.8 and 281, 1,024 32.2
+    // and 261.  (Not by the number of matrices: the order of the norm's sum goes with it.)
+    if (s.m > 64) ns_small_kernel<IO, In, Dst, 128, 128, 4, 4><<<count, 1024, 0, stream>>>(io, s, st);
+    else if (s.n > 128) ns_small_kernel<IO, In, Dst, 64, 256, 4, 4><<<count, 1024, 0, stream>>>(io, s, st);
+    else if (s.n > 64) ns_small_kernel<IO, In, Dst, 64, 128, 2, 4><<<count, 512, 0, stream>>>(io, s, st);
+    else ns_small_kernel<IO, In, Dst, 64, 64, 2, 4><<<count, 512, 0, stream>>>(io, s, st);
     return hipGetLastError();
 }
 
