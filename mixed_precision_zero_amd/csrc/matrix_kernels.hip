@@ -709,7 +709,7 @@ struct Last {
 using Core256 = TileCore<256, 256, 2, 4, false>;
 using Core128w = TileCore<128, 128, 2, 4, false>;      // quarters, by the same 512 threads
 using Core128 = TileCore<128, 128, 2, 2, false>;
-using Core32 = TileCore<32, 32, 1, 1, false, 4>;
+using Core32 = TileCore<32, 32, 2, 2, false, 4>;
 
 template <class Op, class Full, class Quarter>
 __global__ __launch_bounds__(Full::NT, 2) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
@@ -988,9 +988,11 @@ hipError_t launch_small(const NsShape& s, uint32_t count, const IO& io, const Ns
 // The tiles are chosen by what the launch would take per 128 bytes of K, from times measured on
 // the full chip (us per slab): a round of 256 x 256 tiles (one block a CU) 1.45, of their
 // quarters 0.5; a round of 128 x 128 tiles 0.56 (two blocks on a CU take twice that), of their
-// quarters 0.24; 64 x 64 tiles 0.23 where each CU has one, 0.2 a round otherwise.  Below one
-// block a CU the time is a block's own, which goes by the bytes it loads: 32 x 32 tiles of one
-// wave while each has a CU (512 x 512 x 1024: 5.3 us, 6.3 with 64 x 64 ones).  Results do
+// quarters 0.24; 64 x 64 tiles 0.23 where each CU has one, 0.2 a round otherwise.  Few
+// tiles take a block's own time, which goes by the bytes it loads and the instructions a wave
+// issues: 32 x 32 tiles of four waves while a CU has at most two of them (387 x 1001 orthogonalised
+// in 91 us, 98 with one wave a tile, 106 with 64 x 64 ones; with up to four a CU 1000 x 1000
+// takes 136 us instead of 118).  Results do
 // not depend on the choice: every element's products are added in the same order.
 template <class Op>
 hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_t np, uint32_t count,
@@ -1006,7 +1008,7 @@ hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_
     if (mp % 128 == 0 && np % 128 == 0)
         m256 = plan_tiles(256, Op::SYM, mp, np, count, 1.45, 0.5, &c256, &b256);
     const uint64_t p32 = mp / 32, q32 = np / 32, n32 = (Op::SYM ? p32 * (p32 + 1) / 2 : p32 * q32) * count;
-    if (n32 <= kCUs)
+    if (n32 <= 2 * kCUs)
         ns_even_kernel<Op, Core32><<<(uint32_t)n32, Core32::NT, 0, stream>>>(op, st, mp, np);
     else if (c64 <= c128 && c64 <= c256)
         ns_even_kernel<Op, Core64><<<(uint32_t)n64, Core64::NT, 0, stream>>>(op, st, mp, np);

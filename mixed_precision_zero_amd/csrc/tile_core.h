@@ -400,15 +400,15 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 // ROWS x COLS FP16 elements of a row-major array in a wave's own part of LDS, on their way
 // between its result tiles and memory: a lane's four elements are 8 bytes of 16 different rows
 // an instruction, which memory serves at half the rate of whole rows, so rows of COLS elements
-// (64 or 128 bytes) are moved 16 bytes a lane instead.  The 16-byte chunks of a row are
+// (32 to 128 bytes) are moved 16 bytes a lane instead.  The 16-byte chunks of a row are
 // permuted by its number so that 16 rows at one column fall on different banks.  Only the wave
 // that owns the part uses it, and its LDS operations execute in order: no barrier is needed.
 template <int ROWS, int COLS>
 struct Patch {
     static constexpr int kRow = COLS * 2, kChunks = kRow / 16, kBytes = ROWS * kRow;
-    static constexpr int kPass = kBytes / 1024;          // 64 lanes of 16 bytes
-    static_assert((kRow == 64 || kRow == 128) && kBytes % 1024 == 0, "");
-    static __device__ __forceinline__ uint32_t turn(uint32_t row) { return (row >> (kRow == 128 ? 1 : 2)) & (kChunks - 1); }
+    static constexpr int kPass = (kBytes + 1023) / 1024; // 64 lanes of 16 bytes, or 32 of one pass
+    static_assert(kRow >= 32 && kRow <= 128 && (kBytes % 1024 == 0 || kBytes == 512), "");
+    static __device__ __forceinline__ uint32_t turn(uint32_t row) { return row * kRow / 256 & (kChunks - 1); }
     // four elements at (row, col), col a multiple of 4
     static __device__ __forceinline__ f16x4* at(uint8_t* l, uint32_t row, uint32_t col) {
         return (f16x4*)(l + row * kRow + (((col >> 3) ^ turn(row)) << 4) + (col & 4) * 2);
@@ -425,6 +425,7 @@ struct Patch {
     }
     // starts loading from g (row r at r * ld); wave_wait() before it is used
     static __device__ __forceinline__ void load(uint8_t* l, const uint16_t* g, uint32_t ld) {
+        if (kBytes < 1024 && (threadIdx.x & 63) * 16 >= kBytes) return;
 #pragma unroll
         for (int k = 0; k < kPass; ++k)
             __builtin_amdgcn_global_load_lds(
