@@ -707,12 +707,13 @@ struct Last {
 };
 
 using Core256 = TileCore<256, 256, 2, 4, false>;
-using Core128w = TileCore<128, 128, 2, 4, false>;      // quarters, by the same 512 threads
-using Core128 = TileCore<128, 128, 2, 2, false>;
+using Core128 = TileCore<128, 128, 2, 4, false>;       // (quarters are by the same 512 threads)
+using Core64q = TileCore<64, 64, 4, 2, false, 4>;      // quarters of those
 using Core32 = TileCore<32, 32, 2, 2, false, 4>;
 
+// (two blocks of 128 x 128 tiles share a CU, and so a SIMD's registers four waves)
 template <class Op, class Full, class Quarter>
-__global__ __launch_bounds__(Full::NT, 2) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
+__global__ __launch_bounds__(Full::NT, Full::BP == 256 ? 2 : 4) void ns_mixed_kernel(Op op, const DevState* st, TileMap m) {
     static_assert(Full::NT == Quarter::NT && Full::kLds >= Quarter::kLds && Full::BP == 2 * Quarter::BP, "");
     if (skipped(st)) return;
     __shared__ __attribute__((aligned(16))) uint8_t lds[room<Full>() > room<Quarter>() ? room<Full>() : room<Quarter>()];
@@ -986,14 +987,14 @@ hipError_t launch_small(const NsShape& s, uint32_t count, const IO& io, const Ns
 // ------------------------------------------------------------------------------------
 // One product over `count` matrices with mp x np results (mp = np for the symmetric ones).
 // The tiles are chosen by what the launch would take per 128 bytes of K, from times measured on
-// the full chip (us per slab): a round of 256 x 256 tiles (one block a CU) 1.45, of their
-// quarters 0.5; a round of 128 x 128 tiles 0.56 (two blocks on a CU take twice that), of their
-// quarters 0.24; 64 x 64 tiles 0.23 where each CU has one, 0.2 a round otherwise.  Few
-// tiles take a block's own time, which goes by the bytes it loads and the instructions a wave
-// issues: 32 x 32 tiles of four waves while a CU has at most two of them (387 x 1001 orthogonalised
-// in 91 us, 98 with one wave a tile, 106 with 64 x 64 ones; with up to four a CU 1000 x 1000
-// takes 136 us instead of 118).  Results do
-// not depend on the choice: every element's products are added in the same order.
+// the full chip (us per slab): a round of 256 x 256 tiles (one block a CU) 1.45, of 128 x 128
+// ones 0.5 (two blocks on a CU take twice that; by 8 waves, 8 matrices of 4096 x 1024 are
+// orthogonalised in 769 us, by 4 waves in 786), of quarters of those 0.24; 64 x 64 tiles 0.23
+// where each CU has one, 0.2 a round otherwise.  Few tiles take a block's own time, which goes
+// by the bytes it loads and the instructions a wave issues: 32 x 32 tiles of four waves while a
+// CU has at most two of them (387 x 1001 orthogonalised in 91 us, 98 with one wave a tile, 106
+// with 64 x 64 ones; with up to four a CU 1000 x 1000 takes 136 us instead of 118).  Results
+// do not depend on the choice: every element's products are added in the same order.
 template <class Op>
 hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_t np, uint32_t count,
                           hipStream_t stream) {
@@ -1003,7 +1004,7 @@ hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_
     double c128 = 0.0, c256 = 1e300;
     uint64_t b128 = 0, b256 = 0;
     TileMap m256{};
-    const TileMap m128 = plan_tiles(128, Op::SYM, mp, np, count, 0.56, 0.24, &c128, &b128);
+    const TileMap m128 = plan_tiles(128, Op::SYM, mp, np, count, 0.5, 0.24, &c128, &b128);
     // quarters of the large tile are not cut
     if (mp % 128 == 0 && np % 128 == 0)
         m256 = plan_tiles(256, Op::SYM, mp, np, count, 1.45, 0.5, &c256, &b256);
@@ -1013,9 +1014,9 @@ hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_
     else if (c64 <= c128 && c64 <= c256)
         ns_even_kernel<Op, Core64><<<(uint32_t)n64, Core64::NT, 0, stream>>>(op, st, mp, np);
     else if (c128 < c256)
-        ns_mixed_kernel<Op, Core128, Core64><<<(uint32_t)b128, Core128::NT, 0, stream>>>(op, st, m128);
+        ns_mixed_kernel<Op, Core128, Core64q><<<(uint32_t)b128, Core128::NT, 0, stream>>>(op, st, m128);
     else
-        ns_mixed_kernel<Op, Core256, Core128w><<<(uint32_t)b256, Core256::NT, 0, stream>>>(op, st, m256);
+        ns_mixed_kernel<Op, Core256, Core128><<<(uint32_t)b256, Core256::NT, 0, stream>>>(op, st, m256);
     return hipGetLastError();
 }
 
