@@ -228,8 +228,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
 // Large results are bound by the matrix units and LDS together: 8192 x 24576 x 6144 582 us,
 // 4.25 PFLOP/s.  A slab takes 1.95 us on a CU; its products alone, from registers, 1.1 (7.9
 // PFLOP/s on all CUs), its LDS traffic 0.9, and the scales' share of that is 10% of the time.
-// A few hundred rows take 128 x 128 tiles, one a CU: 333 x 4096 x 1024 8.8 us, launch and
-// latency mostly.
+// A few hundred rows take 128 x 128 tiles, one a CU: 333 x 4096 x 1024 7 us, launch and latency
+// mostly.
 // ------------------------------------------------------------------------------------
 struct ProductArgs {
     const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
@@ -292,17 +292,18 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const TileAt&
 }
 
 using Mx256 = TileCore<256, 256, 2, 4, true>;
-using Mx128w = TileCore<128, 128, 2, 4, true>;       // quarters, by the same 512 threads
-using Mx128 = TileCore<128, 128, 2, 2, true>;
+using Mx128 = TileCore<128, 128, 2, 4, true>;        // by the same 512 threads: its quarters too
 
 __global__ __launch_bounds__(512, 2) void product_mixed_kernel(ProductArgs a, TileMap m) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Mx256::kLds];
     const TileAt at = place<false>(m);
     if (at.full) product_tile<Mx256>(a, at, lds);
-    else if (!at.none) product_tile<Mx128w>(a, at, lds);
+    else if (!at.none) product_tile<Mx128>(a, at, lds);
 }
+// Two blocks share a CU, and so a SIMD's registers four waves.  Eight waves a tile instead of
+// four: 700 x 5000 x 4096 18.6 -> 14.5 us, 512 x 6144 x 6144 23.1 -> 19.4.
 template <class Core>
-__global__ __launch_bounds__(Core::NT) void product_even_kernel(ProductArgs a) {
+__global__ __launch_bounds__(Core::NT, 4) void product_even_kernel(ProductArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
     const uint32_t p = (a.n + Core::BP - 1) / Core::BP;
     TileAt at{};
@@ -482,13 +483,13 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
         return hipGetLastError();
     }
     // us per slab of 256 elements of K, measured on the full chip: a round of 256 x 256 tiles
-    // 2.0, of quarters in the same kernel 1.0, of 128 x 128 tiles 0.63 with one block a CU and
+    // 2.0, of quarters in the same kernel 1.0, of 128 x 128 tiles 0.6 with one block a CU and
     // 1.25 with two
     double c256 = 0.0;
     uint64_t blocks = 0;
     const TileMap map = plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
     const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
-    const double c128 = n128 <= kCUs ? 0.63 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
+    const double c128 = n128 <= kCUs ? 0.6 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
     if (c256 < c128) product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
     else product_even_kernel<Mx128><<<(uint32_t)n128, Mx128::NT, 0, stream>>>(a);
     return hipGetLastError();
