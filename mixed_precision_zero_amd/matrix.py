@@ -11,7 +11,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
-import dataclasses
 
 import mixed_precision_zero_amd as Z
 from mixed_precision_zero_amd import (NEOX_BF16, NEOX_F16, NeoxError, _check,  # noqa: F401
@@ -285,35 +284,55 @@ def orthogonalize(x, out=None, dtype=None, scale: float = 1.0, cfg: neox_ns_conf
     return out
 
 
-@dataclasses.dataclass
 class MXFP4:
     """A rows x cols matrix in MXFP4: codes (rows, K/2) and scales (rows, K/32), uint8, K
-    being cols rounded up to a multiple of 128."""
-    codes: object
-    scales: object
-    rows: int
-    cols: int
+    being cols rounded up to a multiple of 128.  Copies that the operators make are one
+    allocation; its two tensors are made when they are asked for."""
 
-    def __post_init__(self):
+    __slots__ = ("rows", "cols", "device", "_memory", "_codes", "_scales", "_at")
+
+    def __init__(self, codes, scales, rows: int, cols: int):
         import torch
-        k = -(-self.cols // 128) * 128
-        for t, width, name in ((self.codes, k // 2, "codes"), (self.scales, k // 32, "scales")):
+        k = -(-cols // 128) * 128
+        for t, width, name in ((codes, k // 2, "codes"), (scales, k // 32, "scales")):
             if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous() or \
-                    tuple(t.shape) != (self.rows, width):
+                    tuple(t.shape) != (rows, width):
                 raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of "
-                                 f"({self.rows}, {width})")
-        if self.codes.device != self.scales.device:
+                                 f"({rows}, {width})")
+        if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
+        self.rows, self.cols, self.device = rows, cols, codes.device
+        self._codes, self._scales = codes, scales
+        self._at = codes.data_ptr(), scales.data_ptr()
 
     @staticmethod
     def empty(rows: int, cols: int, device) -> "MXFP4":
         import torch
         k = -(-cols // 128) * 128
         q = object.__new__(MXFP4)          # right by construction: nothing to check
-        q.codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=device)
-        q.scales = torch.empty((rows, k // 32), dtype=torch.uint8, device=device)
-        q.rows, q.cols = rows, cols
+        q._memory = torch.empty(rows * (k // 2 + k // 32), dtype=torch.uint8, device=device)
+        q.rows, q.cols, q.device = rows, cols, q._memory.device
+        q._codes = q._scales = None
+        at = q._memory.data_ptr()
+        q._at = at, at + rows * (k // 2)
         return q
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            k = -(-self.cols // 128) * 128
+            self._codes = self._memory[:self.rows * (k // 2)].view(self.rows, k // 2)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            k = -(-self.cols // 128) * 128
+            self._scales = self._memory[self.rows * (k // 2):].view(self.rows, k // 32)
+        return self._scales
+
+    def __repr__(self):
+        return f"MXFP4({self.rows} x {self.cols}, {self.device})"
 
 
 def mxfp4_quantize(x, transpose: bool = False, out: MXFP4 | None = None) -> MXFP4:
@@ -323,12 +342,12 @@ def mxfp4_quantize(x, transpose: bool = False, out: MXFP4 | None = None) -> MXFP
     want = (cols, rows) if transpose else (rows, cols)
     if out is None:
         out = MXFP4.empty(*want, x.device)
-    elif (out.rows, out.cols) != want or out.codes.device != x.device:
+    elif (out.rows, out.cols) != want or out.device != x.device:
         raise ValueError(f"out must be a {want[0]} x {want[1]} copy on x's device")
     guard, stream = _on(x)
     with guard:
         neox_mxfp4_quantize(x.data_ptr(), _code(x.dtype), rows, cols, ld, int(transpose),
-                            out.codes.data_ptr(), out.scales.data_ptr(), stream)
+                            *out._at, stream)
     return out
 
 
@@ -336,14 +355,15 @@ def mxfp4_dequantize(q: MXFP4, dtype=None, out=None):
     """The values of a copy, as a new matrix of type `dtype` (bfloat16 by default) or in out."""
     import torch
     if out is None:
-        out = torch.empty(q.rows, q.cols, dtype=dtype or torch.bfloat16, device=q.codes.device)
-    elif tuple(out.shape) != (q.rows, q.cols) or out.device != q.codes.device or \
+        out, ld = torch.empty((q.rows, q.cols), dtype=dtype or torch.bfloat16, device=q.device), q.cols
+    elif tuple(out.shape) != (q.rows, q.cols) or out.device != q.device or \
             (dtype is not None and out.dtype != dtype):
         raise ValueError("out must have the copy's shape and device, and the type asked for")
-    ld = _rows_of(out, "out")
+    else:
+        ld = _rows_of(out, "out")
     guard, stream = _on(out)
     with guard:
-        neox_mxfp4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
+        neox_mxfp4_dequantize(*q._at, q.rows, q.cols,
                               out.data_ptr(), _code(out.dtype), ld, stream)
     return out
 
@@ -352,19 +372,19 @@ def mxfp4_product(a: MXFP4, b: MXFP4, dtype=None, out=None):
     """a b^T of an m x k and an n x k copy, as an m x n matrix of type `dtype` (bfloat16 by
     default) or in out."""
     import torch
-    if a.cols != b.cols or a.codes.device != b.codes.device:
+    if a.cols != b.cols or a.device != b.device:
         raise ValueError("a and b must have the same number of columns, on one device")
     if out is None:
-        out = torch.empty(a.rows, b.rows, dtype=dtype or torch.bfloat16, device=a.codes.device)
-    elif tuple(out.shape) != (a.rows, b.rows) or out.device != a.codes.device or \
+        out, ld = torch.empty((a.rows, b.rows), dtype=dtype or torch.bfloat16, device=a.device), b.rows
+    elif tuple(out.shape) != (a.rows, b.rows) or out.device != a.device or \
             (dtype is not None and out.dtype != dtype):
         raise ValueError("out must have the product's shape and device, and the type asked for")
-    ld = _rows_of(out, "out")
+    else:
+        ld = _rows_of(out, "out")
     guard, stream = _on(out)
     with guard:
-        neox_mxfp4_product(a.codes.data_ptr(), a.scales.data_ptr(), a.rows, b.codes.data_ptr(),
-                           b.scales.data_ptr(), b.rows, a.cols, out.data_ptr(), _code(out.dtype),
-                           ld, stream)
+        neox_mxfp4_product(*a._at, a.rows, *b._at, b.rows, a.cols, out.data_ptr(),
+                           _code(out.dtype), ld, stream)
     return out
 
 
@@ -385,11 +405,10 @@ def muon_matrix(grad, half, master, momentum, decay: bool, copy: MXFP4 | None = 
     for q, want in ((copy, shape), (copy_t, shape[::-1])):
         if q is not None and (q.rows, q.cols) != want:
             raise ValueError(f"the copy must be {want[0]} x {want[1]}")
-    ptr = lambda q, f: None if q is None else getattr(q, f).data_ptr()  # noqa: E731
     return neox_muon_matrix(grad.data_ptr(), half.data_ptr(), master.data_ptr(), momentum.data_ptr(),
                             shape[0], shape[1], Z.NEOX_SEG_DECAY if decay else 0, 0,
-                            ptr(copy, "codes"), ptr(copy, "scales"),
-                            ptr(copy_t, "codes"), ptr(copy_t, "scales"))
+                            *((None, None) if copy is None else copy._at),
+                            *((None, None) if copy_t is None else copy_t._at))
 
 
 class Muon:
