@@ -462,7 +462,20 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
     ProductArgs a{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
                         (const uint8_t*)b_scales, c, ldc, (uint32_t)m, (uint32_t)n, (uint32_t)sh.code_pitch,
                         (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
-    if (m <= 64) {
+    // us per slab of 256 elements of K, measured on the full chip: a round of 256 x 256 tiles
+    // 2.0, of quarters in the same kernel 1.0, of 128 x 128 tiles 0.6 with one block a CU and
+    // 1.25 with two
+    double c256 = 0.0;
+    uint64_t blocks = 0;
+    const TileMap map = plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
+    const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
+    const double c128 = n128 <= kCUs ? 0.6 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
+    // Up to 16 rows the streaming kernel (one row by 24576 x 6144 16 us, 128 x 128 tiles 21), up to
+    // 64 where it takes less by its own cost, 0.12 a slab for 16 rows of a and each 256 blocks:
+    // 32 rows by 6144 x 8192 16.5 us, by tiles 19.7; 64 rows 27 and 19.7, by 24576 x 6144 57 and 21,
+    // by 1024 x 16384 24 and 35.
+    const double thin = 0.12 * (double)((m + 15) / 16) * std::max(1.0, (double)n / (16 * kCUs));
+    if (m <= 16 || (m <= 64 && thin <= c128)) {
         // enough waves for the chip: more of them share K where there are few rows of b
         const bool many = n > 16 * (4 * kCUs - 1);
         auto run = [&](auto mt) {
@@ -482,14 +495,6 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
         else run(std::integral_constant<int, 4>{});
         return hipGetLastError();
     }
-    // us per slab of 256 elements of K, measured on the full chip: a round of 256 x 256 tiles
-    // 2.0, of quarters in the same kernel 1.0, of 128 x 128 tiles 0.6 with one block a CU and
-    // 1.25 with two
-    double c256 = 0.0;
-    uint64_t blocks = 0;
-    const TileMap map = plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
-    const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
-    const double c128 = n128 <= kCUs ? 0.6 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
     if (c256 < c128) product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
     else product_even_kernel<Mx128><<<(uint32_t)n128, Mx128::NT, 0, stream>>>(a);
     return hipGetLastError();
