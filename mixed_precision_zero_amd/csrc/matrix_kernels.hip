@@ -109,10 +109,15 @@ __global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(OrthIO io, uint
             next();
         }
     } else {
-        for (uint32_t r = r0; r < r1; ++r)
+        // element by element, eight rows in flight
+        for (uint32_t r = r0; r < r1; r += 8)
             for (uint32_t c = threadIdx.x; c < cols; c += kNormThreads) {
-                const double x = load_elem(io.src, io.src_dtype, at + r * io.src_ld + c);
-                s = __builtin_fma(x, x, s);
+                float x[8];
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    x[k] = r + k < r1 ? load_elem(io.src, io.src_dtype, at + (r + k) * io.src_ld + c) : 0.0f;
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) s = __builtin_fma((double)x[k], (double)x[k], s);
             }
     }
     s = sum_block<kNormThreads>(s + t);
