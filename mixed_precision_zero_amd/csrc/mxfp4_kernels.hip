@@ -470,12 +470,12 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
     const TileMap map = plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
     const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
     const double c128 = n128 <= kCUs ? 0.6 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
-    // Up to 16 rows the streaming kernel (one row by 24576 x 6144 16 us, 128 x 128 tiles 21), up to
-    // 64 where it takes less by its own cost, 0.12 a slab for 16 rows of a and each 256 blocks:
-    // 32 rows by 6144 x 8192 16.5 us, by tiles 19.7; 64 rows 27 and 19.7, by 24576 x 6144 57 and 21,
-    // by 1024 x 16384 24 and 35.
-    const double thin = 0.12 * (double)((m + 15) / 16) * std::max(1.0, (double)n / (16 * kCUs));
-    if (m <= 16 || (m <= 64 && thin <= c128)) {
+    // Up to 64 rows the streaming kernel where it takes less by its own cost, for each 256 blocks
+    // 0.07 a slab and 0.09 for 16 rows of a.  Streaming and tiles, us: 1 row by 24576 x 6144 15.6
+    // and 18.8, 8 rows 18.9 and 18.8, 64 rows 57 and 21; 16 rows by 6144 x 8192 11.3 and 19.6, 64
+    // rows 27.0 and 19.7; 64 rows by 1024 x 16384 24 and 35.
+    const double thin = (0.07 + 0.09 * (double)m / 16) * std::max(1.0, (double)n / (16 * kCUs));
+    if (m <= 64 && thin <= c128) {
         // enough waves for the chip: more of them share K where there are few rows of b
         const bool many = n > 16 * (4 * kCUs - 1);
         auto run = [&](auto mt) {

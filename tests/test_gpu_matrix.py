@@ -309,7 +309,7 @@ def test_product(dtype, m, n, k):
     assert (err <= tol).all(), float((err / tol).max())
 
 
-@pytest.mark.parametrize("m,n,k", [(5, 40, 96), (16, 5000, 1500), (31, 16500, 600), (64, 200, 256), (150, 260, 4000),
+@pytest.mark.parametrize("m,n,k", [(5, 40, 96), (12, 40000, 300), (60, 9000, 700), (16, 5000, 1500), (31, 16500, 600), (64, 200, 256), (150, 260, 4000),
                                    (4200, 4300, 200), (2500, 9000, 130), (700, 700, 64)])
 def test_product_is_exact_on_small_integers(m, n, k):
     """Values of {0, +-1, +-2, +-4} at scales that make every sum an integer below 2^24 have
