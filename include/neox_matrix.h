@@ -208,7 +208,7 @@ int neox_mxfp4_dequantize(const void* codes, const void* scales, uint64_t rows, 
  * reads as NaN makes its row's or column's results NaN.  With W of shape (out, in): y = x W^T is
  * (x, W); dx = dy W is (dy, transpose copy of W); dW = dy^T x is (transpose copies of dy
  * and x).  Errors: NEOX_EINVAL (null, misaligned, a size of 0 or above 2^31 - 1, k above
- * 2^24, codes of more than 2^40 bytes, 2^24 or more 128 x 128 tiles of c, ldc < n, unknown
+ * 2^24, codes of more than 2^40 bytes, 2^23 or more 128 x 128 tiles of c, ldc < n, unknown
  * type, c meeting an operand), NEOX_EHIP. */
 int neox_mxfp4_product(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
                        const void* b_scales, uint64_t n, uint64_t k, void* c, int32_t dtype,

@@ -19,6 +19,7 @@ constexpr uint64_t kMaxCount = 1ull << 24;
 constexpr uint64_t kMaxMx = (1ull << 31) - 1;   // rows or cols of an MXFP4 copy
 constexpr uint64_t kMaxK = 1ull << 24;          // k of a product (32-bit offsets in a tile)
 constexpr uint64_t kMaxBlocks = 1ull << 24;     // grid limit: 2^32 threads at 256 per block
+constexpr uint64_t kMaxTiles = 1ull << 23;      // 128 x 128 tiles of a product: 512 threads each
 constexpr uint64_t kDefaultWorkspace = 4ull << 30;
 
 bool known_type(int32_t t) { return t == NEOX_F16 || t == NEOX_BF16 || t == NEOX_F32; }
@@ -596,7 +597,7 @@ extern "C" int neox_mxfp4_product(const void* a_codes, const void* a_scales, uin
     if (k > kMaxK) return set_error(NEOX_EINVAL, "k %llu: at most 2^24", (unsigned long long)k);
     rc = mx_dense(c, dtype, m, n, ldc);
     if (rc) return rc;
-    if (((m + 127) / 128) * ((n + 127) / 128) >= kMaxBlocks)
+    if (((m + 127) / 128) * ((n + 127) / 128) >= kMaxTiles)
         return set_error(NEOX_EINVAL, "a result of %llu x %llu is too large", (unsigned long long)m,
                          (unsigned long long)n);
     const MxShape s = mx_shape(k);

@@ -293,6 +293,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const TileAt&
 
 using Mx256 = TileCore<256, 256, 2, 4, true>;
 using Mx128 = TileCore<128, 128, 2, 4, true>;        // by the same 512 threads: its quarters too
+using Mx64 = TileCore<64, 64, 2, 2, true>;
 
 __global__ __launch_bounds__(512, 2) void product_mixed_kernel(ProductArgs a, TileMap m) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Mx256::kLds];
@@ -464,18 +465,21 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
                         (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
     // us per slab of 256 elements of K, measured on the full chip: a round of 256 x 256 tiles
     // 2.0, of quarters in the same kernel 1.0, of 128 x 128 tiles 0.6 with one block a CU and
-    // 1.25 with two
+    // 1.25 with two, of 64 x 64 tiles 0.28 (65 x 6144 x 8192 12 us, by 128 x 128 ones 20; 65 x 1024
+    // x 16384 20.5 and 35)
     double c256 = 0.0;
     uint64_t blocks = 0;
     const TileMap map = plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
     const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
     const double c128 = n128 <= kCUs ? 0.6 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
+    const uint64_t n64 = ((m + 63) / 64) * ((n + 63) / 64);
+    const double c64 = n64 <= kGrid ? 0.28 * (double)((n64 + kCUs - 1) / kCUs) : 1e300;
     // Up to 64 rows the streaming kernel where it takes less by its own cost, for each 256 blocks
-    // 0.07 a slab and 0.09 for 16 rows of a.  Streaming and tiles, us: 1 row by 24576 x 6144 15.6
-    // and 18.8, 8 rows 18.9 and 18.8, 64 rows 57 and 21; 16 rows by 6144 x 8192 11.3 and 19.6, 64
-    // rows 27.0 and 19.7; 64 rows by 1024 x 16384 24 and 35.
+    // 0.07 a slab and 0.09 for 16 rows of a.  Streaming and tiles, us: 16 rows by 24576 x 6144 23.7
+    // and 15.1 (1 row streaming 15.6, the same for tiles as 16), 64 rows 57 and 16.3; 16 rows by
+    // 6144 x 8192 11.3 and 11.6, 64 rows 27.0 and 12.2; 64 rows by 1024 x 16384 24.0 and 20.3.
     const double thin = (0.07 + 0.09 * (double)m / 16) * std::max(1.0, (double)n / (16 * kCUs));
-    if (m <= 64 && thin <= c128) {
+    if (m <= 64 && thin <= std::min(c64, c128)) {
         // enough waves for the chip: more of them share K where there are few rows of b
         const bool many = n > 16 * (4 * kCUs - 1);
         auto run = [&](auto mt) {
@@ -495,7 +499,8 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
         else run(std::integral_constant<int, 4>{});
         return hipGetLastError();
     }
-    if (c256 < c128) product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
+    if (c64 < c128 && c64 < c256) product_even_kernel<Mx64><<<(uint32_t)n64, Mx64::NT, 0, stream>>>(a);
+    else if (c256 < c128) product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
     else product_even_kernel<Mx128><<<(uint32_t)n128, Mx128::NT, 0, stream>>>(a);
     return hipGetLastError();
 }
