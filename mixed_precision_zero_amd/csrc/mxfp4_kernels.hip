@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
 // Large results are bound by the matrix units and LDS together: 8192 x 24576 x 6144 582 us,
 // 4.25 PFLOP/s.  A slab takes 1.95 us on a CU; its products alone, from registers, 1.1 (7.9
 // PFLOP/s on all CUs), its LDS traffic 0.9, and the scales' share of that is 10% of the time.
-// A few hundred rows take 128 x 128 tiles, one a CU: 333 x 4096 x 1024 7 us, launch and latency
+// Smaller ones take 128 x 128 or 64 x 64 tiles: 333 x 4096 x 1024 6.3 us, launch and latency
 // mostly.
 // ------------------------------------------------------------------------------------
 struct ProductArgs {
