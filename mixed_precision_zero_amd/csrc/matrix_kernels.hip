@@ -325,31 +325,54 @@ __device__ __forceinline__ f16x4 pack4(tf32x4 v) {
 }
 
 // An FP16 result on and below the diagonal, to both sides of it, without the diagonal; the
-// diagonal, and more(i) added to it, to d.
+// diagonal, and more(i) added to it, to d.  What lies above the diagonal always is what lies
+// below it, inside a tile too: L M and M L of commuting matrices are one matrix but not one sum
+// of rounded products, so an element computed above the diagonal would depend on how far its
+// tile reaches over it, and a matrix's bits on the launch's choice of tiles.
 template <class Core, class More>
-__device__ __forceinline__ void store_sym(const TileAt& t, const Piece<Core>& p, tf32x4 (&acc)[Core::TP][Core::TQ],
-                                          int u0, uint16_t* out, uint32_t ld, float* d, More more) {
+__device__ __forceinline__ void store_sym(const Piece<Core>& p, tf32x4 (&acc)[Core::TP][Core::TQ], int u0,
+                                          uint16_t* out, uint32_t ld, float* d, More more) {
     using P = Piece<Core>;
+    if (p.i >= p.j + 16 * P::kV) {
+        // all of it below the diagonal
+#pragma unroll
+        for (int u = 0; u < P::kU; ++u)
+#pragma unroll
+            for (int v = 0; v < P::kV; ++v) {
+                const f16x4 h = pack4(acc[u0 + u][v]);
+                *p.down(p.l0, u, v) = h;
+                *p.across(p.l1, u, v) = pack4(transposed(h));
+            }
+        P::Down::store(p.l0, out + (uint64_t)p.j * ld + p.i, ld);
+        P::Across::store(p.l1, out + (uint64_t)p.i * ld + p.j, ld);
+        return;
+    }
+    // a piece of a tile on the diagonal: 16 x 16 at a time, eight bytes a lane
 #pragma unroll
     for (int u = 0; u < P::kU; ++u)
 #pragma unroll
         for (int v = 0; v < P::kV; ++v) {
-            tf32x4& x = acc[u0 + u][v];
-            if (t.i == t.j) {
+            const uint32_t i = p.i + 16 * u, j = p.j + 16 * v;
+            if (i < j) continue;
+            tf32x4 x = acc[u0 + u][v];
+            if (i == j) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (p.i + 16 * u + p.li + e == p.j + 16 * v + p.lj) {
-                        const uint32_t j = p.j + 16 * v + p.lj;
-                        d[j] = x[e] + more(j);
+                    if (p.li + e == p.lj) {
+                        d[j + p.lj] = x[e] + more(j + p.lj);
                         x[e] = 0.0f;
                     }
             }
             const f16x4 h = pack4(x);
-            *p.down(p.l0, u, v) = h;
-            *p.across(p.l1, u, v) = pack4(transposed(h));
+            f16x4 a = pack4(transposed(h));
+            if (i == j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = p.li + e > p.lj ? h[e] : a[e];
+            } else {
+                *(f16x4*)(out + (uint64_t)(j + p.lj) * ld + i + p.li) = h;
+            }
+            *(f16x4*)(out + (uint64_t)(i + p.lj) * ld + j + p.li) = a;
         }
-    if (t.i != t.j) P::Down::store(p.l0, out + (uint64_t)p.j * ld + p.i, ld);
-    P::Across::store(p.l1, out + (uint64_t)p.i * ld + p.j, ld);
 }
 
 // A = X X^T
@@ -371,7 +394,7 @@ struct Gram {
             for (int u = 0; u < P::kU; ++u)
 #pragma unroll
                 for (int v = 0; v < P::kV; ++v) t.acc[u0 + u][v] = t.acc[u0 + u][v] * inv_s2;
-            store_sym<Core>(at, P(at, u0, lds), t.acc, u0, out.a + (uint64_t)at.z * mp * mp, mp,
+            store_sym<Core>(P(at, u0, lds), t.acc, u0, out.a + (uint64_t)at.z * mp * mp, mp,
                             out.d + (uint64_t)at.z * mp, [](uint32_t) { return 0.0f; });
         }
     }
@@ -433,7 +456,7 @@ __global__ __launch_bounds__(Core64::NT) void gram_join_kernel(GramSplit g, cons
     for (int u = 0; u < Core64::TP; ++u)
 #pragma unroll
         for (int v = 0; v < Core64::TQ; ++v) c.acc[u][v] = c.acc[u][v] * g.inv_s2;
-    store_sym<Core64>(at, Piece<Core64>(at, 0, lds), c.acc, 0, g.out.a + (uint64_t)z * g.mp * g.mp, g.mp,
+    store_sym<Core64>(Piece<Core64>(at, 0, lds), c.acc, 0, g.out.a + (uint64_t)z * g.mp * g.mp, g.mp,
                       g.out.d + (uint64_t)z * g.mp, [](uint32_t) { return 0.0f; });
 }
 
@@ -491,7 +514,7 @@ struct Sym {
                     }
                 }
             }
-            store_sym<Core>(at, p, t.acc, u0, r.a + sz, mp, r.d + dz, [&](uint32_t i) {
+            store_sym<Core>(p, t.acc, u0, r.a + sz, mp, r.d + dz, [&](uint32_t i) {
                 const float d = ld[i], dd = d * md[i];
                 return SAME ? __builtin_fmaf(kc, dd, __builtin_fmaf(kb, d, ka)) : dd;
             });
@@ -999,7 +1022,8 @@ hipError_t launch_small(const NsShape& s, uint32_t count, const IO& io, const Ns
 // by the bytes it loads and the instructions a wave issues: 32 x 32 tiles of four waves while a
 // CU has at most two of them (387 x 1001 orthogonalised in 91 us, 98 with one wave a tile, 106
 // with 64 x 64 ones; with up to four a CU 1000 x 1000 takes 136 us instead of 118).  Results
-// do not depend on the choice: every element's products are added in the same order.
+// do not depend on the choice: every element's products are added in the same order, and
+// store_sym mirrors what lies below the diagonal.
 template <class Op>
 hipError_t launch_product(const Op& op, const DevState* st, uint32_t mp, uint32_t np, uint32_t count,
                           hipStream_t stream) {
