@@ -27,6 +27,7 @@
 #include "tile_core.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace nz1 {
 
@@ -52,7 +53,7 @@ __device__ __forceinline__ double sum_block(double v) {
     return r;
 }
 
-// Four or eight consecutive elements, as one or two 16-byte loads (8 bytes for four halves).
+// Four consecutive elements, as one load of 16 bytes (8 for halves).
 __device__ __forceinline__ tf32x4 halves4(int dtype, uint2 q) {
     return tf32x4{half_to_float(dtype, (uint16_t)q.x), half_to_float(dtype, (uint16_t)(q.x >> 16)),
                   half_to_float(dtype, (uint16_t)q.y), half_to_float(dtype, (uint16_t)(q.y >> 16))};
@@ -69,6 +70,9 @@ __device__ __forceinline__ tf32x4 vec4(const void* p, int dtype, uint64_t i) {
 // matrix still has a block on every CU with two vectors in flight a thread.  Sums in 64 bits.
 // Measured: the momentum of 24576 x 6144 (10 B an element) 263 us, 5.7 TB/s; the norm of 8 of
 // 4096 x 1024 in BF16 20 us, of 6144 x 6144 35 us (2.1 TB/s, 0.8% of that call).
+// Which elements a thread adds, and in which order, goes by the shape alone: where the arrays'
+// alignment or strides keep four neighbours from one load they are loaded one by one, in the
+// same places, so that a matrix's norm has the same bits wherever it lies.
 // ------------------------------------------------------------------------------------
 constexpr int kNormThreads = 1024;
 
@@ -85,8 +89,8 @@ __global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(OrthIO io, uint
     const uint32_t r0 = p * per, r1 = min(rows, r0 + per);
     const uint64_t at = z * io.src_stride;
     double s = 0.0, t = 0.0;
-    if (io.vec_src && cols % 4 == 0) {
-        // this block's rows as one run of vectors, two in flight
+    if (cols % 4 == 0) {
+        // this block's rows as one run of fours, two in flight
         const uint32_t w = cols / 4;
         uint32_t r = r0 + threadIdx.x / w, c = threadIdx.x % w;
         const uint32_t dr = kNormThreads / w, dc = kNormThreads % w;
@@ -98,11 +102,19 @@ __global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(OrthIO io, uint
                 ++r;
             }
         };
+        auto four = [&]() {
+            const uint64_t i = at + r * io.src_ld + 4 * c;
+            if (io.vec_src) return vec4(io.src, io.src_dtype, i);
+            tf32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = load_elem(io.src, io.src_dtype, i + e);
+            return x;
+        };
         while (r < r1) {
-            const tf32x4 v = vec4(io.src, io.src_dtype, at + r * io.src_ld + 4 * c);
+            const tf32x4 v = four();
             next();
             if (r < r1) {
-                const tf32x4 q = vec4(io.src, io.src_dtype, at + r * io.src_ld + 4 * c);
+                const tf32x4 q = four();
                 t = square4(q, t);
             }
             s = square4(v, s);
@@ -135,17 +147,25 @@ __global__ __launch_bounds__(kNormThreads) void muon_momentum_kernel(MuonIO io, 
     const uint32_t z = blockIdx.x / parts, p = blockIdx.x % parts;
     const MuonMat mat = io.mats[z];
     double s = 0.0;
-    uint64_t done = 0;
-    if (mat.vec) {
-        const uint64_t n4 = numel / 4, step = (uint64_t)parts * kNormThreads;
-        done = n4 * 4;
-        for (uint64_t i = (uint64_t)p * kNormThreads + threadIdx.x; i < n4; i += 2 * step) {
+    const uint64_t n4 = numel / 4, step = (uint64_t)parts * kNormThreads, first = (uint64_t)p * kNormThreads + threadIdx.x;
+    auto fours = [&](auto vec) {
+        auto load = [&](uint64_t i, tf32x4& g, tf32x4& m) {
+            if constexpr (vec) {
+                g = halves4(io.dtype, *(const uint2*)(mat.grad + i));
+                m = *(const tf32x4*)(mat.mom + i);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    g[e] = half_to_float(io.dtype, mat.grad[i + e]);
+                    m[e] = mat.mom[i + e];
+                }
+            }
+        };
+        for (uint64_t i = first; i < n4; i += 2 * step) {
             const uint64_t j = i + step < n4 ? i + step : i;        // the same again at the end
             tf32x4 g[2], m[2];
-            g[0] = halves4(io.dtype, *(const uint2*)(mat.grad + 4 * i));
-            g[1] = halves4(io.dtype, *(const uint2*)(mat.grad + 4 * j));
-            m[0] = *(const tf32x4*)(mat.mom + 4 * i);
-            m[1] = *(const tf32x4*)(mat.mom + 4 * j);
+            load(4 * i, g[0], m[0]);
+            load(4 * j, g[1], m[1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (k == 1 && j == i) break;
@@ -156,12 +176,20 @@ __global__ __launch_bounds__(kNormThreads) void muon_momentum_kernel(MuonIO io, 
                     m[k][e] = __builtin_fmaf(io.mu, m[k][e], x);
                     u[e] = direction(io, x, m[k][e]);
                 }
-                *(tf32x4*)(mat.mom + 4 * (k ? j : i)) = m[k];
+                float* to = mat.mom + 4 * (k ? j : i);
+                if constexpr (vec) {
+                    *(tf32x4*)to = m[k];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) to[e] = m[k][e];
+                }
                 s = square4(u, s);
             }
         }
-    }
-    for (uint64_t i = done + (uint64_t)p * kNormThreads + threadIdx.x; i < numel; i += (uint64_t)parts * kNormThreads) {
+    };
+    if (mat.vec) fours(std::true_type{});
+    else fours(std::false_type{});
+    for (uint64_t i = 4 * n4 + first; i < numel; i += step) {
         const float g = half_to_float(io.dtype, mat.grad[i]) * gs;
         const float m = __builtin_fmaf(io.mu, mat.mom[i], g);
         mat.mom[i] = m;

@@ -1,7 +1,5 @@
 """What include/neox_matrix.h promises about bits: a matrix of a batch has the bits it has alone,
 and neither workspace_bytes nor where the arrays lie changes a result."""
-import math
-
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -58,3 +56,68 @@ def test_muon_workspace_cap_keeps_the_bits(count, shape):
         got.append(ws)
     for a, b in zip(*got):
         assert all(torch.equal(a[k], b[k]) for k in ("half", "master", "momentum"))
+
+
+# The next two tests look at X0 = source / (norm + eps) itself: one step of (a, b, c) = (1, 0, 0)
+# gives it back.  Half of the source's elements are 1, and eps is swept over the doubles at which
+# S / (norm + eps) passes a tie of FP32, 2^-5 (1 + 2^-24): there the last bit of the norm decides
+# how all of them are rounded, so that another order of its sum shows.  S = 16 at 260 columns.
+SIDE = 260
+ULP = 2.0 ** -44                 # of norm + eps, just below 512
+
+
+def ties(seed):
+    x = rand((SIDE, SIDE), seed)
+    x.view(-1)[::2] = 1.0
+    return x
+
+
+def swept(x):
+    eps = 512.0 / (1 + 2.0 ** -24) - float(x.double().square().sum().sqrt())
+    for k in range(-24, 25):
+        yield M.neox_ns_default_config(coef=[(1.0, 0.0, 0.0)], eps=eps + k * ULP)
+
+
+def off_by_one(t):
+    """t's values in memory that starts one element behind a vector's boundary."""
+    buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device=t.device)
+    buf[1:] = t.reshape(-1)
+    return buf[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_norm_does_not_depend_on_strides_and_alignment(seed):
+    x = ties(seed)
+    wide = torch.zeros(SIDE, SIDE + 3, device=DEV)
+    wide[:, :SIDE] = x
+    odd = torch.zeros(2 * SIDE * SIDE + 1, device=DEV).as_strided((2, SIDE, SIDE), (SIDE * SIDE + 1, SIDE, 1))
+    odd[0] = x
+    ups = 0
+    for cfg in swept(x):
+        want = M.orthogonalize(x, cfg=cfg)
+        ups += int((want.view(-1)[0] > 2.0 ** -9).item())
+        assert torch.equal(M.orthogonalize(wide[:, :SIDE], cfg=cfg), want)
+        assert torch.equal(M.orthogonalize(off_by_one(x), cfg=cfg), want)
+        assert torch.equal(M.orthogonalize(odd, cfg=cfg)[0], want)
+    assert 0 < ups < 49          # the sweep passed the tie
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_muon_norm_does_not_depend_on_alignment(seed):
+    cfg = Z.neox_zero1_default_config(beta1=0.95, weight_decay=0.0, clip_norm=0.0, init_scale=1.0,
+                                      scaler_mode=Z.NEOX_SCALER_STATIC, dtype=Z.NEOX_F16)
+    m0 = rand((SIDE, SIDE), seed)
+    m0.view(-1)[::2] = 0.0
+    grad = torch.zeros(SIDE, SIDE, dtype=torch.float16, device=DEV)
+    grad.view(-1)[::2] = 1.0
+    ups = 0
+    for ns in swept(m0 * 0.95 + grad.float()):
+        got = []
+        for place in (torch.clone, off_by_one):
+            w = {k: place(t) for k, t in dict(grad=grad, half=grad * 0, master=m0 * 0, momentum=m0).items()}
+            muon([dict(w, decay=False)], cfg, ns=ns, nesterov=0, scale_mode=M.NEOX_MUON_SCALE_SHAPE).step(1.0)
+            got.append(w)
+        torch.cuda.synchronize()
+        ups += int((got[0]["master"].view(-1)[0] < -(2.0 ** -9)).item())
+        assert all(torch.equal(got[0][k], got[1][k]) for k in ("master", "half", "momentum"))
+    assert 0 < ups < 49
