@@ -390,7 +390,8 @@ def mxfp4_product(a: MXFP4, b: MXFP4, dtype=None, out=None):
 
 def muon_matrix(grad, half, master, momentum, decay: bool, copy: MXFP4 | None = None,
                 copy_t: MXFP4 | None = None) -> neox_muon_matrix:
-    """neox_muon_matrix over four contiguous CUDA matrices of one shape (no copies made).
+    """neox_muon_matrix over four contiguous CUDA matrices of one shape on one device (no copies
+    made).
     copy / copy_t: MXFP4 copies of the weights / of their transpose that each applied step
     rewrites."""
     import torch
@@ -398,6 +399,8 @@ def muon_matrix(grad, half, master, momentum, decay: bool, copy: MXFP4 | None = 
     for t, dt in ((grad, None), (half, None), (master, torch.float32), (momentum, torch.float32)):
         if not t.is_cuda or t.dim() != 2 or tuple(t.shape) != shape or not t.is_contiguous():
             raise ValueError("arrays must be contiguous 2-D CUDA tensors of one shape")
+        if t.device != grad.device:
+            raise ValueError("the arrays must be on one device")
         if dt is not None and t.dtype != dt:
             raise ValueError("master / momentum must be float32")
     if grad.dtype not in (torch.float16, torch.bfloat16) or half.dtype != grad.dtype:
@@ -405,6 +408,8 @@ def muon_matrix(grad, half, master, momentum, decay: bool, copy: MXFP4 | None = 
     for q, want in ((copy, shape), (copy_t, shape[::-1])):
         if q is not None and (q.rows, q.cols) != want:
             raise ValueError(f"the copy must be {want[0]} x {want[1]}")
+        if q is not None and q.device != grad.device:
+            raise ValueError("the copies must be on the arrays' device")
     return neox_muon_matrix(grad.data_ptr(), half.data_ptr(), master.data_ptr(), momentum.data_ptr(),
                             shape[0], shape[1], Z.NEOX_SEG_DECAY if decay else 0, 0,
                             *((None, None) if copy is None else copy._at),

@@ -237,3 +237,38 @@ def test_kernel_assembly(src, tmp_path):
     assert not re.search(r"^\s*scratch_", asm, re.M) and not PACKED_FP32.search(asm)
     odd = sorted(m for m in set(re.findall(r"^\s+(s_[a-z0-9_]+)", asm, re.M)) if not m.startswith(SCALAR_OK))
     assert not odd, odd
+
+
+class OnDevice:
+    """What muon_matrix asks of a tensor (or of an MXFP4 copy), on a device of the test's choice."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device, at):
+        self.shape, self.dtype, self.device, self.at = shape, dtype, device, at
+        self.rows, self.cols = shape
+        self._at = at, at + GAP
+
+    def dim(self):
+        return 2
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+@pytest.mark.parametrize("other", [None, "half", "master", "momentum", "copy", "copy_t"])
+def test_muon_matrix_is_on_one_device(other):
+    torch = pytest.importorskip("torch")
+    kinds = dict(grad=torch.bfloat16, half=torch.bfloat16, master=torch.float32, momentum=torch.float32,
+                 copy=None, copy_t=None)
+    parts = {k: OnDevice((40, 24) if k == "copy_t" else (24, 40), dt, f"cuda:{int(k == other)}", A + 2 * i * GAP)
+             for i, (k, dt) in enumerate(kinds.items())}
+    if other is None:
+        m = M.muon_matrix(**parts, decay=True)
+        assert (m.grad, m.mx_codes, m.mx_scales_t, m.rows, m.cols) == (A, A + 8 * GAP, A + 11 * GAP, 24, 40)
+        return
+    with pytest.raises(ValueError, match="device"):
+        M.muon_matrix(**parts, decay=True)
