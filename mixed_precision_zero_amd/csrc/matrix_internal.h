@@ -99,5 +99,11 @@ hipError_t launch_mx_dequantize(const void* codes, const void* scales, uint64_t 
 hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t m,
                              const void* b_codes, const void* b_scales, uint64_t n, uint64_t k,
                              void* c, int dtype, uint64_t ldc, hipStream_t stream);
+// Which kernel launch_mx_product takes for an m x n result (the choice does not depend on k).
+enum MxKernel : int32_t {
+    kMxTiles64, kMxTiles128, kMxTiles256,
+    kMxStream1x4, kMxStream1x16, kMxStream2x16, kMxStream4x16,   // 16 rows of a each, waves
+};
+MxKernel mx_product_kernel(uint64_t m, uint64_t n);
 
 }  // namespace nz1

@@ -381,7 +381,7 @@ __global__ __launch_bounds__(WK * 64) void product_thin_kernel(ProductArgs a) {
 
 // Blocks of one launch: a grid has fewer than 2^32 threads.
 constexpr uint64_t kGrid = 1ull << 23;
-// Rows of a transposed copy, or of b in the product of few rows, that a launch takes.
+// Rows of a transposed copy that a launch takes.
 constexpr uint64_t kMostRows = 1ull << 22;
 
 // Launches f(first row, rows, their spread) for as many rows at a time as a grid takes.
@@ -455,53 +455,63 @@ hipError_t launch_mx_dequantize(const void* codes, const void* scales, uint64_t 
     return hipGetLastError();
 }
 
-hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
-                             const void* b_scales, uint64_t n, uint64_t k, void* c, int dtype,
-                             uint64_t ldc, hipStream_t stream) {
-    const MxShape sh = mx_shape(k);
-    const uint64_t es = dtype == NEOX_F32 ? 4 : 2;
-    ProductArgs a{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
-                        (const uint8_t*)b_scales, c, ldc, (uint32_t)m, (uint32_t)n, (uint32_t)sh.code_pitch,
-                        (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
+// The launch of 256 x 256 tiles, and its cost.
+static TileMap mx_tiles256(uint64_t m, uint64_t n, double* cost, uint64_t* blocks) {
+    return plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, cost, blocks);
+}
+static uint64_t tiles(uint64_t m, uint64_t n, uint64_t unit) { return ((m + unit - 1) / unit) * ((n + unit - 1) / unit); }
+
+MxKernel mx_product_kernel(uint64_t m, uint64_t n) {
     // us per slab of 256 elements of K, measured on the full chip: a round of 256 x 256 tiles
     // 2.0, of quarters in the same kernel 1.0, of 128 x 128 tiles 0.6 with one block a CU and
     // 1.25 with two, of 64 x 64 tiles 0.28 (65 x 6144 x 8192 12 us, by 128 x 128 ones 20; 65 x 1024
     // x 16384 20.5 and 35)
     double c256 = 0.0;
     uint64_t blocks = 0;
-    const TileMap map = plan_tiles(256, false, (uint32_t)n, (uint32_t)m, 1, 2.0, 1.0, &c256, &blocks);
-    const uint64_t n128 = ((m + 127) / 128) * ((n + 127) / 128);
+    mx_tiles256(m, n, &c256, &blocks);
+    const uint64_t n128 = tiles(m, n, 128), n64 = tiles(m, n, 64);
     const double c128 = n128 <= kCUs ? 0.6 : 1.25 * (double)((n128 + 2 * kCUs - 1) / (2 * kCUs));
-    const uint64_t n64 = ((m + 63) / 64) * ((n + 63) / 64);
     const double c64 = n64 <= kGrid ? 0.28 * (double)((n64 + kCUs - 1) / kCUs) : 1e300;
     // Up to 64 rows the streaming kernel where it takes less by its own cost, for each 256 blocks
     // 0.07 a slab and 0.09 for 16 rows of a.  Streaming and tiles, us: 16 rows by 24576 x 6144 23.7
     // and 15.1 (1 row streaming 15.6, the same for tiles as 16), 64 rows 57 and 16.3; 16 rows by
     // 6144 x 8192 11.3 and 11.6, 64 rows 27.0 and 12.2; 64 rows by 1024 x 16384 24.0 and 20.3.
+    // (Above 2^29 rows of b a grid holds no 64 x 64 tiles any more, and 128 x 128 ones cost what
+    // streaming does: they take those, in one launch.)
     const double thin = (0.07 + 0.09 * (double)m / 16) * std::max(1.0, (double)n / (16 * kCUs));
-    if (m <= 64 && thin <= std::min(c64, c128)) {
-        // enough waves for the chip: more of them share K where there are few rows of b
-        const bool many = n > 16 * (4 * kCUs - 1);
-        auto run = [&](auto mt) {
-            constexpr int MT = decltype(mt)::value;
-            for (uint64_t r = 0; r < n; r += kMostRows) {
-                a.n = (uint32_t)std::min(kMostRows, n - r);
-                const uint32_t blocks = (a.n + 15) / 16;
-                if (many) product_thin_kernel<MT, 4><<<blocks, 256, 0, stream>>>(a);
-                else product_thin_kernel<MT, 16><<<blocks, 1024, 0, stream>>>(a);
-                a.b_codes += kMostRows * sh.code_pitch;
-                a.b_scales += kMostRows * sh.scale_pitch;
-                a.c = (uint8_t*)a.c + kMostRows * es;
-            }
-        };
-        if (m <= 16) run(std::integral_constant<int, 1>{});
-        else if (m <= 32) run(std::integral_constant<int, 2>{});
-        else run(std::integral_constant<int, 4>{});
-        return hipGetLastError();
+    if (m <= 64 && n64 <= kGrid && thin <= std::min(c64, c128)) {
+        // enough waves for the chip: more of them share K where there are few rows of b (from 13
+        // rows of a on, 64 x 64 tiles take over before b has that many)
+        if (m > 16) return m <= 32 ? kMxStream2x16 : kMxStream4x16;
+        return n > 16 * (4 * kCUs - 1) ? kMxStream1x4 : kMxStream1x16;
     }
-    if (c64 < c128 && c64 < c256) product_even_kernel<Mx64><<<(uint32_t)n64, Mx64::NT, 0, stream>>>(a);
-    else if (c256 < c128) product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
-    else product_even_kernel<Mx128><<<(uint32_t)n128, Mx128::NT, 0, stream>>>(a);
+    if (c64 < c128 && c64 < c256) return kMxTiles64;
+    return c256 < c128 ? kMxTiles256 : kMxTiles128;
+}
+
+hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
+                             const void* b_scales, uint64_t n, uint64_t k, void* c, int dtype,
+                             uint64_t ldc, hipStream_t stream) {
+    const MxShape sh = mx_shape(k);
+    const uint64_t es = dtype == NEOX_F32 ? 4 : 2;
+    const ProductArgs a{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
+                        (const uint8_t*)b_scales, c, ldc, (uint32_t)m, (uint32_t)n, (uint32_t)sh.code_pitch,
+                        (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
+    const uint32_t stripes = (uint32_t)((n + 15) / 16);
+    switch (mx_product_kernel(m, n)) {
+    case kMxStream1x4: product_thin_kernel<1, 4><<<stripes, 256, 0, stream>>>(a); break;
+    case kMxStream1x16: product_thin_kernel<1, 16><<<stripes, 1024, 0, stream>>>(a); break;
+    case kMxStream2x16: product_thin_kernel<2, 16><<<stripes, 1024, 0, stream>>>(a); break;
+    case kMxStream4x16: product_thin_kernel<4, 16><<<stripes, 1024, 0, stream>>>(a); break;
+    case kMxTiles64: product_even_kernel<Mx64><<<(uint32_t)tiles(m, n, 64), Mx64::NT, 0, stream>>>(a); break;
+    case kMxTiles128: product_even_kernel<Mx128><<<(uint32_t)tiles(m, n, 128), Mx128::NT, 0, stream>>>(a); break;
+    case kMxTiles256: {
+        double cost = 0.0;
+        uint64_t blocks = 0;
+        const TileMap map = mx_tiles256(m, n, &cost, &blocks);
+        product_mixed_kernel<<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
+    }
+    }
     return hipGetLastError();
 }
 

@@ -11,6 +11,7 @@ import pytest
 import mixed_precision_zero_amd as Z
 from mixed_precision_zero_amd import build
 from mixed_precision_zero_amd import matrix as M
+from matrix_cases import PRODUCTS_BY_KERNEL
 from test_kernel_asm_cpu import PACKED_FP32, SCALAR_OK, _device_asm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -272,3 +273,28 @@ def test_muon_matrix_is_on_one_device(other):
         return
     with pytest.raises(ValueError, match="device"):
         M.muon_matrix(**parts, decay=True)
+
+
+def product_kernel(m, n):
+    """The host's own choice of a product's kernel (csrc/matrix_internal.h)."""
+    f = getattr(M.lib(), "_ZN3nz117mx_product_kernelEmm")
+    f.argtypes, f.restype = [C.c_uint64, C.c_uint64], C.c_int32
+    return f(m, n)
+
+
+def test_every_product_kernel_has_its_shapes():
+    """The list that the GPU tests run meets each kernel twice or more, and a sweep of sizes takes no
+    kernel that the list leaves out."""
+    got = [product_kernel(m, n) for _, m, n, _ in PRODUCTS_BY_KERNEL]
+    assert got == [kernel for kernel, *_ in PRODUCTS_BY_KERNEL]
+    swept = {product_kernel(m, n) for m in list(range(1, 70)) + [100, 128, 333, 700, 2048, 8192, 60000]
+             for n in [1 << s for s in range(22)] + [3 * 1001 ** 2 >> s for s in range(20)]}
+    assert swept == set(got) and all(got.count(k) > 1 for k in swept)
+
+
+@pytest.mark.parametrize("m", [1, 7, 16, 31, 64])
+def test_streaming_products_fit_one_grid(m):
+    """Blocks of 16 rows of b, up to 1,024 threads each, in fewer than 2^32 threads."""
+    for n in [1 << s for s in range(31)] + [(1 << 29) + 1, 197149, 204800]:
+        if product_kernel(m, n) >= 3:
+            assert (n + 15) // 16 * 1024 < 1 << 32
