@@ -39,11 +39,20 @@ extern "C" {
  *
  * Arithmetic: products of FP16 operands summed in FP32.  The iterate is carried as a pair
  * of FP16 numbers (22 bits) of which only the product terms see the first alone, and the
- * diagonals of A and of b A + c A A are kept in FP32.  The result differs from the
- * polynomial in exact arithmetic by 2e-4 to 2e-3 of its norm, besides the rounding to the
- * output type, whether G's singular values are alike, decay or mostly vanish; by up to 5e-3
- * where a matrix of 64 rows or less has rank 1.  The order of all sums depends on the shape
- * and the coefficients only, not on the batch: each matrix gets the same bits as alone.
+ * diagonals of A and of b A + c A A are kept in FP32.  With the default steps the result
+ * differs from the polynomial in exact arithmetic, besides the rounding to the output type, by
+ *   1e-3 of its norm as a rule, where G's elements vary freely; up to 3e-3, with a smaller side
+ *       below 16 up to 8e-3, whether the singular values are alike or decay;
+ *   more in small matrices of low rank, up to 0.2 / sqrt(smaller side) of the norm (at rank 1;
+ *       half of it at rank 4) with a smaller side of up to 256, above that 3e-3 again;
+ *   2e-3 as a rule and up to 3e-2 where many elements are equal (a constant matrix, blocks of
+ *       ones).  With a smaller side above 512 and a larger one of at least twice that, where
+ *       two steps are taken at a time, 4e-3 as a rule and up to 5e-2.
+ * (In the last two roundings of one sign add up instead of averaging out.)  Where the norm of
+ * G is below about 1e-7 eps, X0 falls below FP16's range and the error grows tenfold with each
+ * tenth of the norm.
+ * The order of all sums depends on the shape and the coefficients only, not on the batch nor
+ * on where and how its matrices lie: each matrix gets the same bits as alone.
  * ------------------------------------------------------------------------------------ */
 #define NEOX_NS_MAX_STEPS 16
 typedef struct neox_ns_config {

@@ -20,9 +20,16 @@
 // see the first alone: their error is filtered through P or X once more and stays at the
 // FP16 level.  A and P have diagonals far larger than the rest (of similar size along the
 // diagonal too, so that their roundings would add up in one direction): the diagonals are
-// kept in FP32, apart, and FP16 holds the rest.  Simulated against 64 bits on Gaussian,
-// decaying and low-rank spectra, 256 rows and more: 2e-4 .. 2e-3 of the result's norm, the
-// larger ones with two steps at a time or rank 1 (64 rows: up to 5e-3 at rank 1).
+// kept in FP32, apart, and FP16 holds the rest.  Simulated against 64 bits: matrices of 128
+// rows and more with Gaussian, decaying and low-rank (Gaussian factors) spectra 2e-4 .. 2e-3 of
+// the result's norm, 4e-3 at rank 1 below 256 rows.  That counts on roundings of either sign in
+// many elements.  Fewer rows leave fewer to average over: at rank 1 up to 0.15 / sqrt(rows) (1e-2
+// at 128 rows, 8e-2 at 4), half of it at rank 4, 1e-3 at full rank.  And equal elements of A are
+// rounded alike: of 16 million matrices of 1 to 64 diagonal blocks of ones half were off by 2e-3,
+// one in a thousand by 1.5e-2, the worst by 2.6e-2; with two steps at a time, of 8 million, 4e-3,
+// 2.7e-2 and 4.4e-2.  (All roundings at their largest and of one sign give 8e-2 and 1.3e-1 to
+// first order.)  A second half for A and P, as X has one, would take that away, for twice the
+// products and more.
 #include "matrix_internal.h"
 #include "tile_core.h"
 

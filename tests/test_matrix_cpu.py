@@ -11,7 +11,7 @@ import pytest
 import mixed_precision_zero_amd as Z
 from mixed_precision_zero_amd import build
 from mixed_precision_zero_amd import matrix as M
-from matrix_cases import PRODUCTS_BY_KERNEL
+from matrix_cases import ACCURACY, PRODUCTS_BY_KERNEL, source, stated_error
 from test_kernel_asm_cpu import PACKED_FP32, SCALAR_OK, _device_asm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -298,3 +298,23 @@ def test_streaming_products_fit_one_grid(m):
     for n in [1 << s for s in range(31)] + [(1 << 29) + 1, 197149, 204800]:
         if product_kernel(m, n) >= 3:
             assert (n + 15) // 16 * 1024 < 1 << 32
+
+
+@pytest.mark.parametrize("kind,rows,cols", ACCURACY)
+def test_roundings_stay_within_the_stated_accuracy(kind, rows, cols):
+    """The kernels' roundings alone, simulated, against the header's figures: what the GPU tests'
+    tolerances are made of is itself held to a limit."""
+    pytest.importorskip("torch")
+    import matrix_reference as R
+    x = source(kind, rows, cols)
+    want = R.newton_schulz(x)
+    err = R.newton_schulz_rounded(x) - want
+    assert float(err.norm() / want.norm()) <= stated_error(kind, rows, cols)
+
+
+def test_stated_accuracy_is_the_headers():
+    text = " ".join(open(os.path.join(ROOT, "include", "neox_matrix.h")).read().split()).replace(" * ", " ")
+    for words in ("as a rule, where G's elements vary freely; up to 3e-3, with a smaller side below 16 up to 8e-3",
+                  "up to 0.2 / sqrt(smaller side) of the norm", "with a smaller side of up to 256, above that 3e-3 again",
+                  "up to 3e-2 where many elements are equal", "4e-3 as a rule and up to 5e-2"):
+        assert words in text, words
