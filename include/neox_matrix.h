@@ -69,7 +69,9 @@ int neox_ns_default_config(neox_ns_config* cfg);
  * any coefficients: 8 per element and 4 per element of a smaller-side square (6 where the
  * larger side is at least twice the smaller one and that is above 512), each side rounded
  * up to a multiple of 64 or 128, and the partial sums: 2 KB a matrix, with a smaller side of
- * up to 512 and a larger one of 2,048 or more up to 3 MB.  Host only. */
+ * up to 512 and a larger one of 2,048 or more up to 3 MB.  A matrix of up to 128 x 128, or 64 x 256 or 256 x 64,
+ * is one block's work: the size for those goes by the same formula, but nothing is written to
+ * that memory.  Host only. */
 int neox_orthogonalize_workspace(uint64_t count, uint64_t rows, uint64_t cols, uint64_t* bytes);
 
 /* Orthogonalise `count` rows x cols matrices.  Matrix i starts at element i * src_stride
@@ -115,7 +117,8 @@ typedef struct neox_muon_config {
     uint64_t workspace_bytes;      /* most device memory for the products, 0 = 4 GiB.  A
                                       matrix that needs more by itself gets what it needs;
                                       matrices of one shape share a launch as far as this
-                                      lets them.  Results do not depend on it.          */
+                                      lets them.  Matrices of up to 128 x 128, 64 x 256 or
+                                      256 x 64 need none.  Results do not depend on it. */
 } neox_muon_config;
 
 /* One rows x cols weight: dense row-major arrays of rows * cols elements, types and

@@ -323,8 +323,10 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
         for (const auto& kv : by) {
             const NsShape s = ns_shape(kv.first.first, kv.first.second, pairs);
             uint64_t most = std::min<uint64_t>(kv.second.size(), launch_count(s));
-            most = std::max<uint64_t>(1, std::min<uint64_t>(most, cap / ns_bytes(s, 1)));
-            while (most > 1 && ns_bytes(s, most) > cap) --most;
+            if (!s.small) {
+                most = std::max<uint64_t>(1, std::min<uint64_t>(most, cap / ns_bytes(s, 1)));
+                while (most > 1 && ns_bytes(s, most) > cap) --most;
+            }
             const double rows = (double)s.rows, cols = (double)s.cols;
             const double f = mcfg->scale_mode == NEOX_MUON_SCALE_RMS ? 0.2 * std::sqrt(std::max(rows, cols))
                                                                      : std::sqrt(std::max(1.0, rows / cols));
@@ -348,7 +350,7 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
                     h->mats.push_back(m);
                 }
                 h->groups.push_back(g);
-                work = std::max(work, ns_bytes(s, g.count));
+                if (!s.small) work = std::max(work, ns_bytes(s, g.count));
             }
         }
     } catch (const std::exception&) {
@@ -365,7 +367,7 @@ extern "C" int neox_muon_create(const neox_zero1_config* cfg, const neox_muon_co
     if (e == hipSuccess) e = hipMalloc(&h->d_partial, nnorm * sizeof(double));
     if (e == hipSuccess) e = hipMalloc(&h->d_state, sizeof(DevState));
     if (e == hipSuccess) e = hipMalloc(&h->d_mats, table.size() * sizeof(MuonMat));
-    if (e == hipSuccess) e = hipMalloc(&h->d_work, work);
+    if (e == hipSuccess && work) e = hipMalloc(&h->d_work, work);
     if (e != hipSuccess)
         return e == hipErrorOutOfMemory ? set_error(NEOX_ENOMEM, "hipMalloc of library scratch (%llu bytes)",
                                                     (unsigned long long)work)
@@ -412,7 +414,7 @@ static hipError_t muon_apply(neox_muon* h, const double* sumsq, uint32_t nparts,
     hipError_t e = launch_finalize(sumsq, nparts, h->sl.st, h->sl.fin, stream);
     for (const Group& g : h->groups) {
         if (e != hipSuccess) return e;
-        const NsBuf w = ns_place(g.shape, g.count, h->d_work);
+        const NsBuf w = g.shape.small ? NsBuf{} : ns_place(g.shape, g.count, h->d_work);
         const MuonIO io{h->d_mats + g.first, h->sl.st, h->sl.dtype, h->nesterov, h->sl.upd.b1, lr,
                         h->sl.upd.wd, g.scale, h->ns_eps};
         e = enqueue_muon(g.shape, w, g.count, io, h->coef, h->steps, stream);
