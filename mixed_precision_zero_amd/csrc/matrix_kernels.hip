@@ -965,7 +965,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ns_small_kernel(IO io, NsShape s
                 *quad_at<TB>(la, j, i) = o[u][v];
             }
         __syncthreads();
-        // B = b A + c A A (see Poly)
+        // B = b A + c A A (see Sym)
         lds_product<TP, SQ, TB>(a, la, pi, la, qs);
 #pragma unroll
         for (int u = 0; u < TP; ++u)

@@ -44,12 +44,19 @@ struct TileRows {
 };
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
-// A raw buffer of n bytes: offsets at or behind n read 0.  Flags: the 32-bit data format word
-// of gfx9's untyped buffers.
+// A raw buffer of n bytes: what lies at or behind n reads 0.  Flags: the 32-bit data format word
+// of gfx9's untyped buffers.  The loads below rely on two things that the hardware's range check
+// does with a lane's offset v and the scalar offset s (measured on gfx950 for loads of 4 and 16
+// bytes to LDS): it is made on v + s, not on v alone, and it holds where s by itself lies behind n
+// (n = 64, v = 0, s = 2^20 reads 0, n = 2^23 with s = 3 * 2^29 too) and where v = 2^31 (s up to 3 *
+// 2^29 + 2^23, n up to 2^31).  Edge tiles of MXFP4 operands need that: whole rows are in s, also
+// rows that the operand does not have; of 256 rows of 2^23 bytes, the longest ones, s reaches 3 *
+// 2^29 + 2^23 + 384.
 __device__ __forceinline__ rsrc_t raw_buffer(const void* p, uint32_t n) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, n, 0x00027000);
 }
-constexpr uint32_t kNowhere = 0x80000000u;      // an offset behind every operand (at most 2^31 bytes)
+constexpr uint32_t kNowhere = 0x80000000u;      // an offset behind every operand (at most 2^31 bytes);
+                                                // with the largest s it stays below 2^32
 
 // BP x BQ output tile by WP x WQ waves, FP16 or MXFP4, NS slabs of K in LDS.
 //
