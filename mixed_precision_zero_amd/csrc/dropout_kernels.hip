@@ -1,0 +1,219 @@
+// dropout_kernels.hip -- the element-wise passes of the linear layer on gfx950: dropout with
+// bias and residual, and the way back through dropout and activation with the columns' sums.
+#include "epilogue.h"
+#include "spread.h"
+
+#include <algorithm>
+
+namespace nz1 {
+
+namespace {
+
+struct DropoutArgs {
+    const void *x, *bias, *residual;
+    void* y;
+    uint64_t x_ld, r_ld, y_ld, rows, row0;
+    uint32_t cols;
+    Drop drop;
+};
+
+constexpr uint32_t kDeep = 2;              // rows a thread has in flight
+
+template <int DT>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp) {
+    const Unit u(sp, kDeep);
+    const uint32_t c = u.unit * 8;
+    if (c >= a.cols) return;
+    const uint32_t n = a.cols - c;
+    const uint64_t off = drop_offset(a.drop);
+    float x[kDeep][8], r[kDeep][8], b[8] = {};
+    if (a.bias) load8<DT>(a.bias, c, n, b);
+#pragma unroll
+    for (uint32_t k = 0; k < kDeep; ++k) {
+        const uint64_t row = u.row + k * u.step;
+        if (row >= a.rows) break;
+        load8<DT>(a.x, row * a.x_ld + c, n, x[k]);
+        if (a.residual) load8<DT>(a.residual, row * a.r_ld + c, n, r[k]);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kDeep; ++k) {
+        const uint64_t row = u.row + k * u.step;
+        if (row >= a.rows) break;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] += b[e];
+        if (a.drop.limit) drop8(a.drop, off, (uint32_t)(a.row0 + row), u.unit, x[k]);
+        if (a.residual) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[k][e] += r[k][e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] = opaque(x[k][e]);
+        store8<DT>(a.y, row * a.y_ld + c, n, x[k]);
+    }
+}
+
+// The way back.  A block takes `across` columns of a run of rows and adds up what it makes of
+// them, column by column: eight sums a thread, joined in order over the threads of one column,
+// then over the runs by join_kernel.  So the sums' order goes by the sizes alone.
+struct BackArgs {
+    Backward b;
+    float* part;               // [runs][cols], or null: no sums, or one run that writes dbias
+    uint64_t run;              // rows of a run
+    uint32_t across, shift;    // as in Spread
+};
+constexpr uint32_t kDeepBack = 4;
+
+template <int DT>
+__device__ __forceinline__ void put_bias(const Backward& b, uint32_t c, float v) {
+    if (b.accumulate) v += load_elem(b.dbias, DT, c);
+    store_elem(b.dbias, DT, c, opaque(v));
+}
+
+template <int DT, int ACT>
+__global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
+    __shared__ float sums[256 * 8];
+    const Backward& b = a.b;
+    const uint32_t wide = 1u << a.shift, step = 256u >> a.shift;
+    const uint32_t down = blockIdx.x / a.across;
+    const uint32_t unit = ((blockIdx.x - down * a.across) << a.shift) + (threadIdx.x & (wide - 1));
+    const uint32_t c = unit * 8;
+    const uint32_t cols = (uint32_t)b.cols, n = c < cols ? cols - c : 0;
+    const uint64_t first = down * a.run, last = min(b.rows, first + a.run);
+    const uint64_t off = drop_offset(b.drop);
+    float s[8] = {};
+    if (n) {
+        for (uint64_t row0 = first + (threadIdx.x >> a.shift); row0 < last; row0 += kDeepBack * step) {
+            float d[kDeepBack][8], p[kDeepBack][8];
+#pragma unroll
+            for (uint32_t k = 0; k < kDeepBack; ++k) {
+                const uint64_t row = row0 + k * step;
+                if (row >= last) break;
+                load8<DT>(b.dy, row * b.dy_ld + c, n, d[k]);
+                if constexpr (ACT != NEOX_ACT_NONE) load8<DT>(b.pre, row * b.pre_ld + c, n, p[k]);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < kDeepBack; ++k) {
+                const uint64_t row = row0 + k * step;
+                if (row >= last) break;
+                if constexpr (ACT != NEOX_ACT_NONE) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[k][e] *= slope<ACT>(p[k][e]);
+                }
+                if (b.drop.limit) drop8(b.drop, off, (uint32_t)row, unit, d[k]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d[k][e] = opaque(d[k][e]);
+                    s[e] += d[k][e];
+                }
+                if (b.d) store8<DT>(b.d, row * b.d_ld + c, n, d[k]);
+            }
+        }
+    }
+    if (!b.dbias) return;
+    if (step > 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[e * 256 + threadIdx.x] = s[e];
+        __syncthreads();
+        if (threadIdx.x >= wide) return;
+        for (uint32_t k = 1; k < step; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += sums[e * 256 + k * wide + threadIdx.x];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < (int)n) {
+            if (a.part) a.part[(uint64_t)down * cols + c + e] = s[e];
+            else put_bias<DT>(b, c + e, s[e]);
+        }
+}
+
+// Sums the runs' sums: 64 columns and 16 shares of the runs a block.
+template <int DT>
+__global__ __launch_bounds__(1024) void join_kernel(Backward b, const float* part, uint32_t runs) {
+    __shared__ float sums[16][64];
+    const uint32_t c = blockIdx.x * 64 + (threadIdx.x & 63), share = threadIdx.x >> 6;
+    float s = 0.0f;
+    if (c < b.cols)
+        for (uint32_t r = share; r < runs; r += 16) s += part[(uint64_t)r * b.cols + c];
+    sums[share][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (share || c >= b.cols) return;
+    for (int k = 1; k < 16; ++k) s += sums[k][threadIdx.x];
+    put_bias<DT>(b, c, s);
+}
+
+// dbias of no rows
+template <int DT>
+__global__ __launch_bounds__(256) void no_rows_kernel(Backward b) {
+    const uint64_t c = blockIdx.x * 256ull + threadIdx.x;
+    if (c < b.cols) put_bias<DT>(b, (uint32_t)c, 0.0f);
+}
+
+// Runs of rows for the sums: enough blocks for the chip, but not so many that their sums weigh
+// against the rows.
+struct Runs {
+    uint32_t shift, across, count;
+    uint64_t rows;             // of a run
+};
+Runs runs_of(uint64_t rows, uint64_t cols) {
+    const Spread s = spread(1, (cols + 7) / 8, 1);
+    Runs r{s.shift, s.across, 0, 0};
+    const uint64_t least = (256u >> r.shift) * kDeepBack;       // rows a block has in flight
+    const uint64_t most = std::max<uint64_t>(1, 1024 / r.across);
+    const uint64_t want = std::min((rows + least - 1) / least, most);
+    r.rows = ((rows + want - 1) / std::max<uint64_t>(want, 1) + least - 1) / least * least;
+    r.count = r.rows ? (uint32_t)((rows + r.rows - 1) / r.rows) : 0;
+    return r;
+}
+
+template <class F>
+void with_dtype(int32_t dtype, F f) {
+    if (dtype == NEOX_F32) f(std::integral_constant<int, NEOX_F32>{});
+    else if (dtype == NEOX_F16) f(std::integral_constant<int, NEOX_F16>{});
+    else f(std::integral_constant<int, NEOX_BF16>{});
+}
+
+}  // namespace
+
+hipError_t launch_dropout(const void* x, uint64_t x_ld, const void* bias, const void* residual, uint64_t residual_ld,
+                          void* y, uint64_t y_ld, uint64_t rows, uint64_t cols, int32_t dtype, const Drop& drop,
+                          hipStream_t stream) {
+    const uint64_t size = dtype == NEOX_F32 ? 4 : 2;
+    rows_in_grids(rows, (cols + 7) / 8, kDeep, [&](uint64_t r, uint64_t n, const Spread& sp) {
+        const DropoutArgs a{(const uint8_t*)x + r * x_ld * size, bias,
+                            residual ? (const uint8_t*)residual + r * residual_ld * size : nullptr,
+                            (uint8_t*)y + r * y_ld * size, x_ld, residual_ld, y_ld, n, r, (uint32_t)cols, drop};
+        with_dtype(dtype, [&](auto dt) {
+            dropout_kernel<decltype(dt)::value><<<(uint32_t)sp.blocks, 256, 0, stream>>>(a, sp);
+        });
+    });
+    return hipGetLastError();
+}
+
+uint64_t backward_workspace(uint64_t rows, uint64_t cols) {
+    const Runs r = runs_of(rows, cols);
+    return r.count > 1 ? (r.count * cols * 4 + 255) / 256 * 256 : 0;
+}
+
+hipError_t launch_backward(const Backward& b, void* workspace, hipStream_t stream) {
+    const Runs r = runs_of(b.rows, b.cols);
+    with_dtype(b.dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (b.rows == 0) {
+            no_rows_kernel<DT><<<(uint32_t)((b.cols + 255) / 256), 256, 0, stream>>>(b);
+            return;
+        }
+        const bool join = b.dbias && r.count > 1;
+        const BackArgs a{b, join ? (float*)workspace : nullptr, r.rows, r.across, r.shift};
+        const uint32_t blocks = r.across * r.count;
+        auto run = [&](auto act) { backward_kernel<DT, decltype(act)::value><<<blocks, 256, 0, stream>>>(a); };
+        // (only half types have an act)
+        if constexpr (DT == NEOX_F32) run(std::integral_constant<int, NEOX_ACT_NONE>{});
+        else with_act(b.act, run);
+        if (join)
+            join_kernel<DT><<<(uint32_t)((b.cols + 63) / 64), 1024, 0, stream>>>(b, (const float*)workspace, r.count);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace nz1

@@ -1,0 +1,299 @@
+// epilogue.h -- device code that the linear layer's kernels and the MXFP4 product share: the
+// random bits of dropout, activations and their slopes (include/neox_linear.h).
+#pragma once
+
+#include "linear_internal.h"
+#include "tile_core.h"
+
+#include <type_traits>
+
+namespace nz1 {
+
+// ------------------------------------------------------------------------------------
+// dropout
+// ------------------------------------------------------------------------------------
+// The bits of elements (row, 8 unit) to (row, 8 unit + 7): Philox-4x32, ten rounds, written from
+// its publication (Salmon et al., SC 2011): a round multiplies two words by constants and mixes
+// the products' halves with the other two words and the round's key.  16 bits an element instead
+// of 32: the 20 wide multiplications of a call, at a quarter of the rate of other instructions,
+// are most of what dropout computes, and probabilities in steps of 2^-16 are fine enough.
+struct Bits {
+    uint32_t w[4];
+};
+__device__ __forceinline__ Bits philox(const uint32_t (&seed)[2], uint64_t offset, uint32_t row, uint32_t unit) {
+    uint32_t a = unit, b = row, c = (uint32_t)offset, d = (uint32_t)(offset >> 32);
+    uint32_t k0 = seed[0], k1 = seed[1];
+    // (the keys of all rounds would be kept, and crowd out a product's results)
+    asm volatile("" : "+s"(k0), "+s"(k1));
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t x = (uint64_t)0xD2511F53u * a, y = (uint64_t)0xCD9E8D57u * c;
+        a = (uint32_t)(y >> 32) ^ b ^ k0;
+        b = (uint32_t)y;
+        c = (uint32_t)(x >> 32) ^ d ^ k1;
+        d = (uint32_t)x;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return Bits{{a, b, c, d}};
+}
+// o of the header: read once, when the work runs
+__device__ __forceinline__ uint64_t drop_offset(const Drop& d) {
+    return d.offset + (d.limit && d.counter ? *d.counter : 0ull);
+}
+// A dropped element is zero whatever v is.
+__device__ __forceinline__ float dropped(const Drop& d, uint32_t word, int odd, float v) {
+    const uint32_t bits = odd ? word >> 16 : word & 0xFFFFu;
+    return bits >= d.limit ? v * d.scale : 0.0f;
+}
+
+// ------------------------------------------------------------------------------------
+// activations, by the hardware's exp2 and reciprocal (1 ulp each)
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// The normal distribution's tail behind |x|, times exp(x^2 / 2): with t = 1 / (1 + 0.3 |x|) a
+// polynomial of t, fitted on [0, 15] to 6e-8 relative (and FP32's roundings on top).
+__device__ __forceinline__ float tail_scaled(float ax) {
+    const float t = rcp_fast(__builtin_fmaf(0.3f, ax, 1.0f));
+    float r = 0.03842540085315704f;
+    r = __builtin_fmaf(r, t, -0.16939479112625122f);
+    r = __builtin_fmaf(r, t, 0.22913166880607605f);
+    r = __builtin_fmaf(r, t, -0.07704470306634903f);
+    r = __builtin_fmaf(r, t, 0.1429063081741333f);
+    r = __builtin_fmaf(r, t, 0.09452608972787857f);
+    r = __builtin_fmaf(r, t, 0.12196046113967896f);
+    r = __builtin_fmaf(r, t, 0.11948209255933762f);
+    return __builtin_fmaf(r, t, 7.495441877836129e-06f);
+}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanhC = 0.7978845608028654f;          // sqrt(2 / pi)
+
+// Below -kFar an act or slope is less than 1e-36 and taken as zero: near there the formulas'
+// exponentials overflow, and at -inf they would give inf * 0.  Above kFar a slope is 1.  A NaN
+// passes the comparisons.
+template <int ACT>
+constexpr float kFar = ACT == NEOX_ACT_GELU ? 15.0f : ACT == NEOX_ACT_GELU_TANH ? 10.0f : 88.0f;
+
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+    if constexpr (ACT == NEOX_ACT_NONE) return x;
+    if constexpr (ACT == NEOX_ACT_RELU) return x <= 0.0f ? 0.0f : x;
+    if constexpr (ACT == NEOX_ACT_GELU) {
+        const float q = tail_scaled(__builtin_fabsf(x)) * exp2_fast(x * x * (-0.5f * kLog2e));
+        // (1 - q) from the tail itself: x (1 - q) for x > 0
+        const float y = x > 0.0f ? __builtin_fmaf(-x, q, x) : x * q;
+        return x < -kFar<ACT> ? 0.0f : x > kFar<ACT> ? x : y;
+    }
+    if constexpr (ACT == NEOX_ACT_GELU_TANH) {
+        // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+        const float u = x * __builtin_fmaf(x * x, -2.0f * kLog2e * kTanhC * 0.044715f, -2.0f * kLog2e * kTanhC);
+        const float y = x * rcp_fast(1.0f + exp2_fast(u));
+        return x < -kFar<ACT> ? 0.0f : y;
+    }
+    if constexpr (ACT == NEOX_ACT_SILU) {
+        const float y = x * rcp_fast(1.0f + exp2_fast(x * -kLog2e));
+        return x < -kFar<ACT> ? 0.0f : y;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ float slope(float x) {
+    if constexpr (ACT == NEOX_ACT_NONE) return 1.0f;
+    if constexpr (ACT == NEOX_ACT_RELU) return x <= 0.0f ? 0.0f : x > 0.0f ? 1.0f : x;
+    if constexpr (ACT == NEOX_ACT_GELU) {
+        const float e = exp2_fast(x * x * (-0.5f * kLog2e));
+        const float q = tail_scaled(__builtin_fabsf(x)) * e;
+        const float y = __builtin_fmaf(x * 0.3989422804014327f, e, x > 0.0f ? 1.0f - q : q);
+        return x < -kFar<ACT> ? 0.0f : x > kFar<ACT> ? 1.0f : y;
+    }
+    if constexpr (ACT == NEOX_ACT_GELU_TANH) {
+        const float xx = x * x;
+        const float e = exp2_fast(x * __builtin_fmaf(xx, -2.0f * kLog2e * kTanhC * 0.044715f, -2.0f * kLog2e * kTanhC));
+        const float s = rcp_fast(1.0f + e);
+        // s + x s (1 - s) 2 u', 1 - s = e s
+        const float du = __builtin_fmaf(xx, 6.0f * kTanhC * 0.044715f, 2.0f * kTanhC);
+        const float y = __builtin_fmaf(x * s * (e * s), du, s);
+        return x < -kFar<ACT> ? 0.0f : x > kFar<ACT> ? 1.0f : y;
+    }
+    if constexpr (ACT == NEOX_ACT_SILU) {
+        const float e = exp2_fast(x * -kLog2e), s = rcp_fast(1.0f + e);
+        const float y = __builtin_fmaf(x * s, e * s, s);
+        return x < -kFar<ACT> ? 0.0f : x > kFar<ACT> ? 1.0f : y;
+    }
+}
+template <class F>
+__host__ __device__ __forceinline__ void with_act(int32_t act, F f) {
+    switch (act) {
+    case NEOX_ACT_RELU: f(std::integral_constant<int, NEOX_ACT_RELU>{}); break;
+    case NEOX_ACT_GELU: f(std::integral_constant<int, NEOX_ACT_GELU>{}); break;
+    case NEOX_ACT_GELU_TANH: f(std::integral_constant<int, NEOX_ACT_GELU_TANH>{}); break;
+    case NEOX_ACT_SILU: f(std::integral_constant<int, NEOX_ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, NEOX_ACT_NONE>{});
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// eight neighbouring elements of a row
+// ------------------------------------------------------------------------------------
+// Vectors at any element's address: gfx950 serves unaligned vector accesses of global memory, at
+// full rate within a cache line, so rows that begin anywhere take one access each.
+typedef tu32x4 __attribute__((aligned(2))) loose_u32x4;
+typedef tf32x4 __attribute__((aligned(4))) loose_f32x4;
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, uint64_t at, uint32_t n, float (&v)[8]) {
+    if (n >= 8) {
+        if constexpr (DT == NEOX_F32) {
+            const tf32x4 a = *(const loose_f32x4*)((const float*)p + at), b = *(const loose_f32x4*)((const float*)p + at + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = a[e];
+                v[4 + e] = b[e];
+            }
+        } else {
+            const tu32x4 a = *(const loose_u32x4*)((const uint16_t*)p + at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = half_to_float(DT, (uint16_t)(a[e / 2] >> (16 * (e & 1))));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < (int)n ? load_elem(p, DT, at + e) : 0.0f;
+    }
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* p, uint64_t at, uint32_t n, const float (&v)[8]) {
+    if (n >= 8) {
+        if constexpr (DT == NEOX_F32) {
+            *(loose_f32x4*)((float*)p + at) = tf32x4{v[0], v[1], v[2], v[3]};
+            *(loose_f32x4*)((float*)p + at + 4) = tf32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            tu32x4 q;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q[e] = float_to_half(DT, v[2 * e]) | (uint32_t)float_to_half(DT, v[2 * e + 1]) << 16;
+            *(loose_u32x4*)((uint16_t*)p + at) = q;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < (int)n) store_elem(p, DT, at + e, v[e]);
+    }
+}
+__device__ __forceinline__ void drop8(const Drop& d, uint64_t off, uint32_t row, uint32_t unit, float (&v)[8]) {
+    const Bits b = philox(d.seed, off, row, unit);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = dropped(d, b.w[e / 2], e & 1, v[e]);
+}
+
+// ------------------------------------------------------------------------------------
+// results of a product
+// ------------------------------------------------------------------------------------
+struct Result {
+    void* out;
+    uint64_t ld;
+    uint32_t I, J;             // columns, rows
+    int32_t dtype;             // of out
+    bool accumulate, epilogue;
+    Epilogue e;
+};
+// Takes the sums of elements (row, col) to (row, col + 7), col a multiple of 8, to memory.
+template <int DT, int HT>
+__device__ __forceinline__ void emit8(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8]) {
+    const uint32_t n = r.I - col;
+    float t[8];
+    if (r.epilogue) {
+        if (r.e.bias) {
+            load8<HT>(r.e.bias, col, n, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += t[e];
+        }
+        if (r.e.pre) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);
+            store8<HT>(r.e.pre, row * r.e.pre_ld + col, n, v);
+        }
+        with_act(r.e.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = activate<decltype(act)::value>(v[e]);
+        });
+        if (r.e.drop.limit) drop8(r.e.drop, off, row, col / 8, v);
+        if (r.e.residual) {
+            load8<DT>(r.e.residual, row * r.e.residual_ld + col, n, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += t[e];
+        }
+    }
+    if (r.accumulate) {
+        load8<DT>(r.out, row * r.ld + col, n, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);
+    store8<DT>(r.out, row * r.ld + col, n, v);
+}
+
+// ... with out's type looked at: HT's own or FP32.
+template <int HT>
+__device__ __forceinline__ void emit8_any(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8]) {
+    if (r.dtype == NEOX_F32) emit8<NEOX_F32, HT>(r, off, row, col, v);
+    else emit8<HT, HT>(r, off, row, col, v);
+}
+
+// The results of a wave's part of a block tile, through the wave's own part of LDS in FP32: there
+// a lane's four elements of 16 rows become eight neighbouring ones of a row, so that what the
+// epilogue reads and writes moves 16 bytes a lane, dropout takes all 128 bits of a call, and the
+// epilogue's code is one loop and not one copy for each register.  Rows are padded by 16 bytes
+// (they fall on different banks).  at.i, at.j: the block tile's first column and row.
+template <class Core>
+struct Rows {
+    static constexpr int kU = Core::TP < 4 ? Core::TP : 4, kV = Core::TQ < 2 ? Core::TQ : 2;
+    static constexpr int kCols = 16 * kU, kRows = 16 * kV, kPitch = kCols * 4 + 16;
+    static constexpr int kBytes = kRows * kPitch, kWaves = Core::NT / 64;
+    static_assert(kBytes * kWaves <= Core::kLds, "");
+    static_assert(Core::TP % kU == 0 && Core::TQ % kV == 0, "");
+};
+template <int HT, class Core>
+__device__ __forceinline__ void emit_tile(const Result& r, const Core& t, uint32_t i0, uint32_t j0, uint8_t* lds) {
+    using R = Rows<Core>;
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint8_t* l = lds + wave * R::kBytes;
+    const uint32_t wi = __builtin_amdgcn_readfirstlane(i0 + Core::wave_p()), wj = __builtin_amdgcn_readfirstlane(j0 + Core::wave_q());
+    const uint64_t off = drop_offset(r.e.drop);
+    constexpr uint32_t kLanes = R::kCols / 8, kStep = 64 / kLanes;      // lanes a row, rows a pass
+    constexpr int kAcross = Core::TP / R::kU, kPieces = kAcross * (Core::TQ / R::kV);
+    auto pass = [&](auto dt) {
+        // (a loop over pieces that picks their registers by comparison made the compiler keep the
+        // results in scratch memory)
+#pragma unroll
+        for (int piece = 0; piece < kPieces; ++piece) {
+            const uint32_t bi = wi + piece % kAcross * R::kCols, bj = wj + piece / kAcross * R::kRows;
+            if (bi >= r.I || bj >= r.J) continue;
+#pragma unroll
+            for (int u = 0; u < R::kU; ++u)
+#pragma unroll
+                for (int v = 0; v < R::kV; ++v)
+                    *(tf32x4*)(l + (16 * v + l16) * R::kPitch + (16 * u + 4 * g) * 4) =
+                        t.acc[piece % kAcross * R::kU + u][piece / kAcross * R::kV + v];
+            // A wave's LDS operations execute in order; the compiler must keep them so too.
+            asm volatile("" ::: "memory");
+            const uint32_t c = bi + lane % kLanes * 8;
+#pragma unroll 1
+            for (uint32_t k = lane / kLanes; k < R::kRows; k += kStep) {
+                if (bj + k >= r.J || c >= r.I) break;
+                const tf32x4* s = (const tf32x4*)(l + k * R::kPitch + lane % kLanes * 32);
+                const tf32x4 a = s[0], b = s[1];
+                float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                emit8<decltype(dt)::value, HT>(r, off, bj + k, c, x);
+            }
+            asm volatile("" ::: "memory");
+        }
+    };
+    if (r.dtype == NEOX_F32) pass(std::integral_constant<int, NEOX_F32>{});
+    else pass(std::integral_constant<int, HT>{});
+}
+
+}  // namespace nz1

@@ -1,0 +1,74 @@
+// linear_internal.h -- types shared by the host side and the gfx950 kernels of the linear
+// layer's operators (include/neox_linear.h).  Not part of the public ABI.
+#pragma once
+
+#include "matrix_internal.h"
+#include "neox_linear.h"
+
+namespace nz1 {
+
+// neox_drop as the kernels take it.
+struct Drop {
+    uint32_t limit;            // T: draws below it are dropped (0: no dropout)
+    float scale;               // 65536 / (65536 - T); 0 for T = 65536
+    uint32_t seed[2];
+    uint64_t offset;
+    const uint64_t* counter;
+};
+struct Epilogue {
+    const uint16_t* bias;      // of the half type
+    const void* residual;      // of the result's type
+    uint16_t* pre;             // of the half type
+    uint64_t residual_ld, pre_ld;
+    int32_t act;
+    Drop drop;
+};
+
+// One operand of a product: `side` rows or columns of the result, over K.  Rows of K
+// consecutive elements, or (strided) K rows of `side` consecutive elements.
+struct Operand {
+    const uint16_t* at;
+    uint64_t ld;
+    bool strided;
+};
+// out[j][i] = sum over k of p(i, k) q(j, k): I columns, J rows.
+struct Product {
+    Operand p, q;
+    uint32_t I, J;
+    uint64_t K;
+    int32_t dtype;             // of the operands
+    int32_t out_dtype;
+    void* out;
+    uint64_t out_ld;
+    bool accumulate;           // out += (then no epilogue)
+    bool epilogue;             // whether epi holds anything
+    Epilogue epi;
+};
+uint64_t product_workspace(const Product& p);
+hipError_t launch_product(const Product& p, void* workspace, hipStream_t stream);
+
+// d = D(dy) act'(pre), and the sums of its columns.
+struct Backward {
+    const void* dy;
+    const uint16_t* pre;       // null: no act
+    void* d;                   // or null
+    void* dbias;               // or null
+    uint64_t dy_ld, pre_ld, d_ld;
+    uint64_t rows, cols;
+    int32_t dtype, act;
+    bool accumulate;
+    Drop drop;
+};
+uint64_t backward_workspace(uint64_t rows, uint64_t cols);     // for dbias
+hipError_t launch_backward(const Backward& b, void* workspace, hipStream_t stream);
+
+hipError_t launch_dropout(const void* x, uint64_t x_ld, const void* bias, const void* residual, uint64_t residual_ld,
+                          void* y, uint64_t y_ld, uint64_t rows, uint64_t cols, int32_t dtype, const Drop& drop,
+                          hipStream_t stream);
+
+// the MXFP4 product with an epilogue (mxfp4_kernels.hip)
+hipError_t launch_mx_linear(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
+                            const void* b_scales, uint64_t n, uint64_t k, void* c, int32_t dtype, uint64_t ldc,
+                            int32_t half, const Epilogue& epi, hipStream_t stream);
+
+}  // namespace nz1

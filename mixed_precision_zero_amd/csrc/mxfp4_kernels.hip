@@ -1,6 +1,8 @@
 // mxfp4_kernels.hip -- MXFP4 quantise, dequantise and product on gfx950 (layout and
 // rounding as include/neox_matrix.h states them).
+#include "epilogue.h"
 #include "matrix_internal.h"
+#include "spread.h"
 #include "tile_core.h"
 
 #include <algorithm>
@@ -29,34 +31,6 @@ __device__ __forceinline__ uint32_t codes8(const float* v, uint32_t s) {
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], f, 3);
     return s == 255u ? 0u : w;
 }
-
-// How the rows of an array are spread over blocks of 256 threads, a thread taking eight
-// elements of each of `deep` rows: `wide` threads side by side (a power of two) on 256 / wide
-// rows, `deep` times.
-struct Spread {
-    uint32_t shift;        // log2(wide)
-    uint32_t across;       // blocks across a row
-    uint64_t blocks;
-};
-Spread spread(uint64_t rows, uint64_t units, uint32_t deep) {
-    Spread s{};
-    while (s.shift < 8 && (1ull << s.shift) < units) ++s.shift;
-    s.across = (uint32_t)((units + (1ull << s.shift) - 1) >> s.shift);
-    const uint64_t per = (256u >> s.shift) * deep;
-    s.blocks = (rows + per - 1) / per * s.across;
-    return s;
-}
-struct Unit {
-    uint64_t row;          // the first; the others `step` further each
-    uint32_t unit;         // eight elements each
-    uint32_t step;
-    __device__ Unit(const Spread& s, uint32_t deep) {
-        const uint32_t down = blockIdx.x / s.across;
-        step = 256u >> s.shift;
-        row = (uint64_t)down * (step * deep) + (threadIdx.x >> s.shift);
-        unit = ((blockIdx.x - down * s.across) << s.shift) + (threadIdx.x & ((1u << s.shift) - 1));
-    }
-};
 
 __device__ __forceinline__ float decode(int dtype, uint32_t w, int k) {
     return half_to_float(dtype, (uint16_t)(w >> (16 * k)));
@@ -240,6 +214,14 @@ struct ProductArgs {
     int32_t dtype;
     bool vec;                  // rows of c can be written 16 bytes at a time
 };
+// The product of a layer: what happens to its sums is the epilogue's (r.out is c).
+template <int HT>
+struct LinearArgs : ProductArgs {
+    static constexpr int kHalf = HT;
+    Result r;
+};
+template <class Args>
+constexpr bool kLayer = !std::is_same_v<Args, ProductArgs>;
 
 __device__ __forceinline__ void store_four(const ProductArgs& a, uint32_t i, uint32_t j, tf32x4 x) {
     if (i >= a.m) return;
@@ -256,14 +238,18 @@ __device__ __forceinline__ void store_four(const ProductArgs& a, uint32_t i, uin
 }
 
 // One tile of c: rows at.j .., columns at.i ..
-template <class Core>
-__device__ __forceinline__ void product_tile(const ProductArgs& a, const TileAt& at, uint8_t* lds) {
+template <class Core, class Args>
+__device__ __forceinline__ void product_tile(const Args& a, const TileAt& at, uint8_t* lds) {
     const TileRows p{a.b_codes + (uint64_t)at.i * a.pitch, a.b_scales + (uint64_t)at.i * a.spitch,
                      min((uint32_t)Core::BP, a.n - at.i), a.pitch, a.spitch};
     const TileRows q{a.a_codes + (uint64_t)at.j * a.pitch, a.a_scales + (uint64_t)at.j * a.spitch,
                      min((uint32_t)Core::BQ, a.m - at.j), a.pitch, a.spitch};
     Core t;
     t.run(p, q, a.pitch, lds);
+    if constexpr (kLayer<Args>) {
+        emit_tile<Args::kHalf>(a.r, t, at.i, at.j, lds);
+        return;
+    }
     using P = Piece<Core>;
 #pragma unroll
     for (int u0 = 0; u0 < Core::TP; u0 += P::kU) {
@@ -295,7 +281,8 @@ using Mx256 = TileCore<256, 256, 2, 4, true>;
 using Mx128 = TileCore<128, 128, 2, 4, true>;        // by the same 512 threads: its quarters too
 using Mx64 = TileCore<64, 64, 2, 2, true>;
 
-__global__ __launch_bounds__(512, 2) void product_mixed_kernel(ProductArgs a, TileMap m) {
+template <class Args>
+__global__ __launch_bounds__(512, 2) void product_mixed_kernel(Args a, TileMap m) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Mx256::kLds];
     const TileAt at = place<false>(m);
     if (at.full) product_tile<Mx256>(a, at, lds);
@@ -303,8 +290,8 @@ __global__ __launch_bounds__(512, 2) void product_mixed_kernel(ProductArgs a, Ti
 }
 // Two blocks share a CU, and so a SIMD's registers four waves.  Eight waves a tile instead of
 // four: 700 x 5000 x 4096 18.6 -> 14.5 us, 512 x 6144 x 6144 23.1 -> 19.4.
-template <class Core>
-__global__ __launch_bounds__(Core::NT, 4) void product_even_kernel(ProductArgs a) {
+template <class Core, class Args>
+__global__ __launch_bounds__(Core::NT, 4) void product_even_kernel(Args a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
     const uint32_t p = (a.n + Core::BP - 1) / Core::BP;
     TileAt at{};
@@ -319,8 +306,8 @@ __global__ __launch_bounds__(Core::NT, 4) void product_even_kernel(ProductArgs a
 // group of lanes each 32 of them) and their four scale bytes as one dword, so each of the four
 // products of a step picks its scale by byte.  Measured: one row by 24576 x 6144 (80 MB) 16.0
 // us, 5.0 TB/s.
-template <int MT, int WK>
-__global__ __launch_bounds__(WK * 64) void product_thin_kernel(ProductArgs a) {
+template <int MT, int WK, class Args>
+__global__ __launch_bounds__(WK * 64) void product_thin_kernel(Args a) {
     static_assert(WK >= MT, "");
     __shared__ tf32x4 part[WK][MT][64];
     const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
@@ -373,27 +360,26 @@ __global__ __launch_bounds__(WK * 64) void product_thin_kernel(ProductArgs a) {
         tf32x4 x = part[0][wave][lane];
 #pragma unroll
         for (int w = 1; w < WK; ++w) x = x + part[w][wave][lane];
-        store_four(a, 16 * wave + l16, n0 + 4 * g, x);
+        if constexpr (kLayer<Args>) {
+            // a lane's four elements and its neighbour's: eight of one row, finished by the first
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = x[e];
+                v[4 + e] = __shfl_xor(x[e], 16, 64);
+            }
+            const uint32_t row = 16 * wave + l16, col = n0 + 4 * g;
+            if ((g & 1) == 0 && row < a.m && col < a.n) emit8_any<Args::kHalf>(a.r, drop_offset(a.r.e.drop), row, col, v);
+        } else {
+            store_four(a, 16 * wave + l16, n0 + 4 * g, x);
+        }
     }
 }
 
 }  // namespace
 
-// Blocks of one launch: a grid has fewer than 2^32 threads.
-constexpr uint64_t kGrid = 1ull << 23;
 // Rows of a transposed copy that a launch takes.
 constexpr uint64_t kMostRows = 1ull << 22;
-
-// Launches f(first row, rows, their spread) for as many rows at a time as a grid takes.
-template <class F>
-static void rows_in_grids(uint64_t rows, uint64_t units, uint32_t deep, F f) {
-    const Spread one = spread(1, units, deep);          // (at most 2^20 blocks across)
-    const uint64_t most = kGrid / one.across * ((256u >> one.shift) * deep);
-    for (uint64_t r = 0; r < rows; r += most) {
-        const uint64_t n = std::min(most, rows - r);
-        f(r, n, spread(n, units, deep));
-    }
-}
 
 // whether rows of eight elements can be moved 16 bytes at a time
 static bool eights(const void* p, int dtype, uint64_t ld) {
@@ -489,14 +475,18 @@ MxKernel mx_product_kernel(uint64_t m, uint64_t n) {
     return c256 < c128 ? kMxTiles256 : kMxTiles128;
 }
 
-hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
-                             const void* b_scales, uint64_t n, uint64_t k, void* c, int dtype,
-                             uint64_t ldc, hipStream_t stream) {
+static ProductArgs product_args(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
+                                const void* b_scales, uint64_t n, uint64_t k, void* c, int dtype, uint64_t ldc) {
     const MxShape sh = mx_shape(k);
     const uint64_t es = dtype == NEOX_F32 ? 4 : 2;
-    const ProductArgs a{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
-                        (const uint8_t*)b_scales, c, ldc, (uint32_t)m, (uint32_t)n, (uint32_t)sh.code_pitch,
-                        (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
+    return ProductArgs{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
+                       (const uint8_t*)b_scales, c, ldc, (uint32_t)m, (uint32_t)n, (uint32_t)sh.code_pitch,
+                       (uint32_t)sh.scale_pitch, dtype, (uintptr_t)c % 16 == 0 && ldc * es % 16 == 0};
+}
+
+template <class Args>
+static hipError_t launch_mx(const Args& a, hipStream_t stream) {
+    const uint64_t m = a.m, n = a.n;
     const uint32_t stripes = (uint32_t)((n + 15) / 16);
     switch (mx_product_kernel(m, n)) {
     case kMxStream1x4: product_thin_kernel<1, 4><<<stripes, 256, 0, stream>>>(a); break;
@@ -513,6 +503,24 @@ hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t
     }
     }
     return hipGetLastError();
+}
+
+hipError_t launch_mx_product(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
+                             const void* b_scales, uint64_t n, uint64_t k, void* c, int dtype,
+                             uint64_t ldc, hipStream_t stream) {
+    return launch_mx(product_args(a_codes, a_scales, m, b_codes, b_scales, n, k, c, dtype, ldc), stream);
+}
+
+hipError_t launch_mx_linear(const void* a_codes, const void* a_scales, uint64_t m, const void* b_codes,
+                            const void* b_scales, uint64_t n, uint64_t k, void* c, int32_t dtype, uint64_t ldc,
+                            int32_t half, const Epilogue& epi, hipStream_t stream) {
+    auto run = [&](auto ht) {
+        LinearArgs<decltype(ht)::value> a{};
+        static_cast<ProductArgs&>(a) = product_args(a_codes, a_scales, m, b_codes, b_scales, n, k, c, dtype, ldc);
+        a.r = Result{c, ldc, (uint32_t)n, (uint32_t)m, dtype, false, true, epi};
+        return launch_mx(a, stream);
+    };
+    return half == NEOX_F16 ? run(std::integral_constant<int, NEOX_F16>{}) : run(std::integral_constant<int, NEOX_BF16>{});
 }
 
 }  // namespace nz1
