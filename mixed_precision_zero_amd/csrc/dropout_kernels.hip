@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
                     d[k][e] = opaque(d[k][e]);
                     s[e] += d[k][e];
                 }
-                if (b.d) store8<DT>(b.d, row * b.d_ld + c, n, d[k]);
+                if (b.d) store8<DT>(b.d, row * b.d_ld + c, b.padded ? 8 : n, d[k]);
             }
         }
     }

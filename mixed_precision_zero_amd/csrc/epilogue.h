@@ -249,9 +249,10 @@ __device__ __forceinline__ void emit8_any(const Result& r, uint64_t off, uint32_
 // (they fall on different banks).  at.i, at.j: the block tile's first column and row.
 template <class Core>
 struct Rows {
-    static constexpr int kU = Core::TP < 4 ? Core::TP : 4, kV = Core::TQ < 2 ? Core::TQ : 2;
-    static constexpr int kCols = 16 * kU, kRows = 16 * kV, kPitch = kCols * 4 + 16;
-    static constexpr int kBytes = kRows * kPitch, kWaves = Core::NT / 64;
+    static constexpr int kWaves = Core::NT / 64;
+    static constexpr int kU = Core::TP < 4 ? Core::TP : 4, kCols = 16 * kU, kPitch = kCols * 4 + 16;
+    static constexpr int kV = Core::TQ >= 2 && 32 * kPitch * kWaves <= Core::kLds ? 2 : 1;
+    static constexpr int kRows = 16 * kV, kBytes = kRows * kPitch;
     static_assert(kBytes * kWaves <= Core::kLds, "");
     static_assert(Core::TP % kU == 0 && Core::TQ % kV == 0, "");
 };

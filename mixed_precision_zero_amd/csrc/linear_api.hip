@@ -173,8 +173,8 @@ int take_linear(const neox_linear_args* a, Arrays& arr, Product& p) {
     arr.reads("w", a->w, a->n, a->k, a->w_ld, 2);
     if (arr.check()) return arr.rc;
     const Epilogue& e = p.epi;
-    p.p = Operand{(const uint16_t*)a->w, a->n > 1 ? a->w_ld : a->k, false};
-    p.q = Operand{(const uint16_t*)a->x, a->m > 1 ? a->x_ld : a->k, false};
+    p.p = Operand{(const uint16_t*)a->w, a->n > 1 ? a->w_ld : a->k, false, false};
+    p.q = Operand{(const uint16_t*)a->x, a->m > 1 ? a->x_ld : a->k, false, false};
     p.I = (uint32_t)a->n;
     p.J = (uint32_t)a->m;
     p.K = a->k;
@@ -240,6 +240,7 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
     b.dtype = a->dtype;
     b.act = a->act;
     b.accumulate = a->accumulate != 0;
+    b.padded = made;
 
     auto product = [&](Operand p, Operand q, uint64_t I, uint64_t J, uint64_t K, void* out, uint64_t out_ld) {
         Product r{};
@@ -254,12 +255,12 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
         return r;
     };
     // (d's place is filled in when the workspace is known; its alignment is the workspace's)
-    const Operand dy{made ? nullptr : (const uint16_t*)a->dy, made ? d_ld : b.dy_ld, false};
+    const Operand dy{made ? nullptr : (const uint16_t*)a->dy, made ? d_ld : b.dy_ld, false, made};
     if (g.has_dx)
-        g.dx = product(Operand{(const uint16_t*)a->w, n > 1 ? a->w_ld : k, true}, dy, k, m, n, a->dx,
+        g.dx = product(Operand{(const uint16_t*)a->w, n > 1 ? a->w_ld : k, true, false}, dy, k, m, n, a->dx,
                        m > 1 ? a->dx_ld : k);
     if (g.has_dw) {
-        g.dw = product(Operand{(const uint16_t*)a->x, m > 1 ? a->x_ld : k, true}, Operand{dy.at, dy.ld, true}, k, n, m,
+        g.dw = product(Operand{(const uint16_t*)a->x, m > 1 ? a->x_ld : k, true, false}, Operand{dy.at, dy.ld, true, made}, k, n, m,
                        a->dw, n > 1 ? a->dw_ld : k);
         g.dw.accumulate = a->accumulate != 0;
     }

@@ -30,6 +30,7 @@ struct Operand {
     const uint16_t* at;
     uint64_t ld;
     bool strided;
+    bool padded;               // its rows may be read up to a multiple of 8 elements: zeros
 };
 // out[j][i] = sum over k of p(i, k) q(j, k): I columns, J rows.
 struct Product {
@@ -44,6 +45,16 @@ struct Product {
     bool epilogue;             // whether epi holds anything
     Epilogue epi;
 };
+// Which kernel a product takes, and into how many shares of how many slabs (64 elements) its sums
+// over K are split: by the sizes alone.  Deep: four slabs of K in LDS instead of two, for launches
+// that leave a CU one block, whose loads are then all that is under way.
+enum ProductKernel : int32_t { kTiles64, kTiles128, kTiles128Deep, kTiles256 };
+struct ProductPlan {
+    ProductKernel kernel;
+    uint32_t shares;
+    uint64_t slabs;
+};
+ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K);
 uint64_t product_workspace(const Product& p);
 hipError_t launch_product(const Product& p, void* workspace, hipStream_t stream);
 
@@ -57,6 +68,7 @@ struct Backward {
     uint64_t rows, cols;
     int32_t dtype, act;
     bool accumulate;
+    bool padded;               // rows of d are filled with zeros up to a multiple of 8 elements
     Drop drop;
 };
 uint64_t backward_workspace(uint64_t rows, uint64_t cols);     // for dbias

@@ -30,6 +30,7 @@ namespace nz1 {
 
 typedef float tf32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 tf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 tbf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t tu32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t ti32x8 __attribute__((ext_vector_type(8)));
 
@@ -41,6 +42,19 @@ struct TileRows {
     const uint8_t* base;
     const uint8_t* scales;            // MXFP4: row r's at r * spitch
     uint32_t rows, pitch, spitch;
+};
+// What a core's operands are: rows of K whose slabs are whole (but for MXFP4's last half slab)...
+struct WholeRows {
+    static constexpr bool kBf16 = false, kStridedP = false, kStridedQ = false, kAnyK = false;
+};
+// ... or 16-bit elements, FP16 or BF16, over any multiple of eight of K, each operand as rows of K
+// or strided: spitch (at most K, the rest reads as zeros) rows of `rows` consecutive elements,
+// pitch bytes apart.  A strided operand's slab lies in LDS as it does in memory, 64 rows of K;
+// fragments are read with the transposing LDS load (ds_read_b64_tr_b16: of 16 lanes' 8 bytes, as
+// 4 rows of 16 elements, lane l gets column l), two of them for eight elements of K.
+template <bool BF16, bool PS, bool QS>
+struct HalfOperands {
+    static constexpr bool kBf16 = BF16, kStridedP = PS, kStridedQ = QS, kAnyK = true;
 };
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
@@ -72,8 +86,9 @@ constexpr uint32_t kNowhere = 0x80000000u;      // an offset behind every operan
 // and copy them at each product (10 times slower).  Tried as well, of no use: slabs of 64 bytes
 // in four stages (equal, 128 x 128 tiles 20% slower), more stages, the Q fragments a row
 // earlier, waves 4 x 2, a higher wave priority in the products.
-template <int BP_, int BQ_, int WP_, int WQ_, bool FP4_, int NS_ = 2>
+template <int BP_, int BQ_, int WP_, int WQ_, bool FP4_, int NS_ = 2, class Form_ = WholeRows>
 struct TileCore {
+    using Form = Form_;
     static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NS = NS_;
     static constexpr bool FP4 = FP4_;
     static constexpr int NT = WP * WQ * 64;
@@ -111,18 +126,65 @@ struct TileCore {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    // lds: kLds bytes.  kbytes: bytes of K, a multiple of 128 (FP16) or 64 (MXFP4).
+    // A strided slab's rows: the 32-byte units (16 elements) of row r are at position u ^ turn(r),
+    // so that the eight rows which 32 lanes read at a time, 4 of two lane groups, fall on different
+    // banks.  Rows 16 further turn alike, as the loads of one thread need.
+    template <int B>
+    static __device__ __forceinline__ uint32_t turn(uint32_t r) {
+        return B >= 128 ? (r & 3) | (r >> 1 & 4) : (r >> 1 & 1) | (r >> 2 & 2);
+    }
+    // This thread's first 16 bytes of a strided slab: its offset in the operand.
+    template <int B>
+    static __device__ __forceinline__ uint32_t strided_lane(uint32_t pitch) {
+        constexpr uint32_t kChunks = B / 8;
+        const uint32_t r = threadIdx.x / kChunks, c = threadIdx.x % kChunks;
+        return r * pitch + ((c >> 1 ^ turn<B>(r)) << 1 | (c & 1)) * 16;
+    }
+    // Slab s of a strided operand; behind the last row of K it reads as zeros.  (Loads are 16 bytes,
+    // so a last row whose elements do not fill them must be readable up to a multiple of 8.)
+    static __device__ __forceinline__ rsrc_t strided_slab(const TileRows& t, uint32_t s) {
+        const uint32_t first = s * 64, left = t.spitch > first ? min(64u, t.spitch - first) : 0u;
+        // (a scalar: the compiler took a vector subtraction for its borrow, and with the length in a
+        // vector register every load is a loop over the lanes, 2.5 times slower)
+        const uint32_t n = left ? (left - 1) * t.pitch + (t.rows + 7) / 8 * 16 : 0u;
+        return raw_buffer(t.base + (uint64_t)first * t.pitch, __builtin_amdgcn_readfirstlane(n));
+    }
+    // A restricted pointer, which says nothing here (nothing else is accessed), gives the read an
+    // alias scope of its own.  Without one the compiler takes it for a possible store and makes it
+    // wait for every load to LDS under way (4096^3: 260 us against 110); that the slab has landed
+    // is for wait_barrier to see to, as with the other fragments.
+    static __device__ __forceinline__ uint2 transposed(const uint8_t* __restrict__ at) {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* tptr;
+        return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tptr)at));
+    }
+    // Elements 32 h + 8 g .. + 7 of K of column `unit` * 16 + l16 of a strided slab.
+    template <int B>
+    static __device__ __forceinline__ tu32x4 strided_frag(const uint8_t* slab, uint32_t unit, int h) {
+        const uint32_t l16 = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, r = 8 * g + (l16 >> 2);
+        const uint8_t* at = slab + (32 * h + r) * (2 * B) + ((unit ^ turn<B>(r)) << 5) + (l16 & 3) * 8;
+        const uint2 x = transposed(at), y = transposed(at + 4 * (2 * B));
+        return tu32x4{x.x, x.y, y.x, y.y};
+    }
+
+    // lds: kLds bytes.  kbytes: bytes of K, a multiple of 128 (FP16) or 64 (MXFP4), or with kAnyK of
+    // 16.
     __device__ __forceinline__ void run(const TileRows& p, const TileRows& q, uint32_t kbytes,
                                         uint8_t* lds) {
         const uint32_t tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
         const uint32_t slabs = (kbytes + kSlab - 1) / kSlab;
-        const rsrc_t pb = raw_buffer(p.base, p.rows * p.pitch), qb = raw_buffer(q.base, q.rows * q.pitch);
+        constexpr bool kPS = Form::kStridedP, kQS = Form::kStridedQ;
+        rsrc_t pb = raw_buffer(p.base, p.rows * p.pitch), qb = raw_buffer(q.base, q.rows * q.pitch);
         // this thread's chunk of its first row; the others are NT / 8 rows further each
         const uint32_t chunk = (tid & 7) ^ ((tid >> 3) & 7);
-        const uint32_t pv = (tid >> 3) * p.pitch + chunk * 16, qv = (tid >> 3) * q.pitch + chunk * 16;
-        const uint32_t pstep = NT / 8 * p.pitch, qstep = NT / 8 * q.pitch;
+        const uint32_t pv = kPS ? strided_lane<BP>(p.pitch) : (tid >> 3) * p.pitch + chunk * 16;
+        const uint32_t qv = kQS ? strided_lane<BQ>(q.pitch) : (tid >> 3) * q.pitch + chunk * 16;
+        const uint32_t pstep = (kPS ? NT * 8 / BP : NT / 8) * p.pitch, qstep = (kQS ? NT * 8 / BQ : NT / 8) * q.pitch;
         // MXFP4: the last slab may be half a slab; its second half is read as zeros
+        // (with kAnyK, end somewhere; a thread's chunk lies behind the end or not)
+        const uint32_t end = Form::kAnyK ? kbytes % kSlab : 0u;
         const bool half_tail = FP4 && (kbytes & 64u);
+        const bool cut = Form::kAnyK ? end && chunk * 16 >= end : half_tail && chunk >= 4;
         const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int rp = wave_p() + (int)l16, rq = wave_q() + (int)l16;
         uint8_t* sl = lds + NS * kStage;
@@ -131,14 +193,20 @@ struct TileCore {
         // Load n (of LP + LQ) of slab s.  Slabs behind the last one are loaded from nowhere: the
         // loop has no branches, and the number of loads under way at each wait is known.
         auto stage = [&](int n, uint32_t s, uint8_t* buf) {
-            const bool live = s < slabs - (half_tail && chunk >= 4 ? 1 : 0);
+            const bool live = s < slabs - (cut ? 1 : 0);
             if (n < LP)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(pb, (lptr)(buf + wave * 1024 + n * NT * 16), 16,
-                                                         live ? pv : kNowhere, s * kSlab + n * pstep, 0, 0);
+                                                         kPS || live ? pv : kNowhere, (kPS ? 0u : s * kSlab) + n * pstep,
+                                                         0, 0);
             else
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    qb, (lptr)(buf + BP * kSlab + wave * 1024 + (n - LP) * NT * 16), 16, live ? qv : kNowhere,
-                    s * kSlab + (n - LP) * qstep, 0, 0);
+                    qb, (lptr)(buf + BP * kSlab + wave * 1024 + (n - LP) * NT * 16), 16, kQS || live ? qv : kNowhere,
+                    (kQS ? 0u : s * kSlab) + (n - LP) * qstep, 0, 0);
+        };
+        // Strided operands' buffers move on with the slab to load.
+        auto point = [&](uint32_t s) {
+            if constexpr (kPS) pb = strided_slab(p, s);
+            if constexpr (kQS) qb = strided_slab(q, s);
         };
         // Quarter k of the scales of slabs 4u .. 4u + 3: a group is loaded over the four slabs
         // before it, so that these loads need no branch either.
@@ -181,6 +249,10 @@ struct TileCore {
                                                                            0, (int)sq[set][j])
                         : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[i][j], 4, 4, 1, (int)sp[i],
                                                                            1, (int)sq[set][j]);
+                } else if constexpr (Form::kBf16) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(tbf16x8, fp[i]),
+                                                                        __builtin_bit_cast(tbf16x8, fq[h][j]),
+                                                                        acc[i][j], 0, 0, 0);
                 } else {
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(tf16x8, fp[i]),
                                                                        __builtin_bit_cast(tf16x8, fq[h][j]),
@@ -188,9 +260,15 @@ struct TileCore {
                 }
             }
         };
-        auto read_p = [&](int i, const uint8_t* c, int h) { fp[i] = frag(c, rp + 16 * i, 2 * (int)g + h); };
+        // (a strided fragment is 32 consecutive elements of K, so the other operand's is too)
+        auto kchunk = [&](int h) { return Form::kAnyK ? (int)g + 4 * h : 2 * (int)g + h; };
+        auto read_p = [&](int i, const uint8_t* c, int h) {
+            if constexpr (kPS) fp[i] = strided_frag<BP>(c, wave_p() / 16 + i, h);
+            else fp[i] = frag(c, rp + 16 * i, kchunk(h));
+        };
         auto read_q = [&](int j, const uint8_t* c, int h) {
-            fq[h][j] = frag(c + BP * kSlab, rq + 16 * j, 2 * (int)g + h);
+            if constexpr (kQS) fq[h][j] = strided_frag<BQ>(c + BP * kSlab, wave_q() / 16 + j, h);
+            else fq[h][j] = frag(c + BP * kSlab, rq + 16 * j, kchunk(h));
         };
         const uint32_t sswap = (l16 & 8) << 1;
         auto scale_p = [&](int i, uint32_t s) {
@@ -211,6 +289,7 @@ struct TileCore {
         group(1, 0);
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
+            point(k);
 #pragma unroll
             for (int n = 0; n < LP + LQ; ++n) stage(n, k, lds + k * kStage);
         }
@@ -230,6 +309,7 @@ struct TileCore {
             uint8_t* cur = lds + at * kStage;
             at = at + 1 == NS ? 0 : at + 1;
             const uint8_t* nxt = lds + at * kStage;
+            point(s + NS);
             // first half: products of (s, 0), reads of (s, 1)
 #pragma unroll
             for (int i = 0; i < TP; ++i) {

@@ -8,6 +8,7 @@ torch = pytest.importorskip("torch")
 import linear_reference as R  # noqa: E402
 import mixed_precision_zero_amd as Z  # noqa: E402
 from mixed_precision_zero_amd import linear as L  # noqa: E402
+from linear_cases import PRODUCTS  # noqa: E402
 from mixed_precision_zero_amd import matrix as M  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -82,6 +83,24 @@ def test_backward_sizes(m, n, k, half):
     assert same_bits(dx.cpu(), (d @ w.double().cpu() + 0.0).to(half))
     assert same_bits(dw.cpu(), (d.t() @ x.double().cpu() + 0.0).to(half))
     assert same_bits(db.cpu(), (d.sum(0) + 0.0).to(half))
+
+
+@HALVES
+@pytest.mark.parametrize("kernel,shared,I,J,K", PRODUCTS)
+def test_every_product_kernel(kernel, shared, I, J, K, half):
+    """Each kernel, with and without shares of K, in the three products that take it: whole numbers,
+    exact sums, the epilogue's bias and residual among them."""
+    a, b = ints((J, K), 1, half, 2), ints((I, K), 2, half, 2)
+    bias, res = ints((I,), 3, half, 9), ints((J, I), 4, half, 9)
+    want = a.double() @ b.double().t() + 0.0
+    y, pre = L.linear(a, b, bias, residual=res, act="relu", pre=True)
+    v = want + bias.double()
+    assert same_bits(pre, v.to(half)) and same_bits(y, (v.clamp(min=0) + res.double()).to(half))
+    dx, _, _ = L.linear_backward(a, None, b.t().contiguous(), dw=False)
+    assert same_bits(dx, want.to(half))
+    dw = res.clone()
+    L.linear_backward(a.t().contiguous(), b.t().contiguous(), None, dx=False, dw=dw, accumulate=True)
+    assert same_bits(dw, (want + res.double()).to(half))
 
 
 @HALVES

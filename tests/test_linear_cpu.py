@@ -15,6 +15,7 @@ import linear_reference as R
 import mixed_precision_zero_amd as Z
 from mixed_precision_zero_amd import build
 from mixed_precision_zero_amd import linear as L
+from linear_cases import PRODUCTS
 from test_kernel_asm_cpu import PACKED_FP32, SCALAR_OK, _device_asm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -290,3 +291,50 @@ def test_mask_follows_the_probability():
         n, q = k.numel(), 1 - R.limit_of(p) / 65536
         assert abs(int(k.sum()) - n * q) < 5 * math.sqrt(n * q * (1 - q))
         assert abs(scale * q - 1) < 1e-7
+
+
+# ----------------------------------------------------------------------------------------
+# which kernel a product takes
+# ----------------------------------------------------------------------------------------
+
+class _Plan(C.Structure):
+    _fields_ = [("kernel", C.c_int32), ("shares", C.c_uint32), ("slabs", C.c_uint64)]
+
+
+def plan(I, J, K):
+    """The host's own choice (csrc/linear_internal.h)."""
+    f = getattr(L.lib(), "_ZN3nz112product_planEmmm")
+    f.argtypes, f.restype = [C.c_uint64] * 3, _Plan
+    return f(I, J, K)
+
+
+def test_every_product_kernel_has_its_shapes():
+    """The list that the GPU tests run meets each kernel, with and without shares of K, twice or
+    more, and a sweep of sizes takes none that the list leaves out."""
+    got = [(plan(*s).kernel, plan(*s).shares > 1) for *_, I, J, K in PRODUCTS for s in [(I, J, K)]]
+    assert got == [(kernel, shared) for kernel, shared, *_ in PRODUCTS]
+    swept = set()
+    for I in [1 << s for s in range(23)] + [1001, 3001, 24576]:
+        for J in (0, 1, 7, 64, 100, 333, 1000, 2048, 3001, 8192, 65536):
+            for K in (0, 1, 64, 1000, 6144, 16384, 1 << 22):
+                if ((I + 63) // 64) * ((J + 63) // 64) <= 1 << 23:
+                    p = plan(I, J, K)
+                    swept.add((p.kernel, p.shares > 1))
+                    # the shares cover K, none is empty, and the blocks fit a grid
+                    slabs = max(1, -(-K // 64))
+                    assert (p.shares - 1) * p.slabs < slabs <= p.shares * p.slabs
+                    unit, threads = {0: (64, 256), 1: (128, 512), 2: (128, 512), 3: (128, 512)}[p.kernel]
+                    assert -(-I // unit) * -(-J // unit) * p.shares * threads < 1 << 32
+    assert swept == set(got) and all(got.count(k) > 1 for k in swept)
+
+
+def test_workspaces_go_by_sizes_and_alignment():
+    """Aligned operands need none but for shares; others room for their copies."""
+    aligned = dict(x_ld=64, k=64, n=40)
+    assert L.neox_linear_workspace(forward(**aligned)[0]) == 0
+    one = L.neox_linear_workspace(forward(**dict(aligned, x=X + 2))[0])
+    both = L.neox_linear_workspace(forward(**dict(aligned, x=X + 2, w=W + 2))[0])
+    assert one == 30 * 64 * 2 // 256 * 256 + (256 if 30 * 64 * 2 % 256 else 0) and both == one + 40 * 64 * 2
+    shared = dict(m=128, n=128, k=16384, x_ld=16384, w_ld=16384, y_ld=128, residual_ld=128, pre_ld=128)
+    p = plan(128, 128, 16384)
+    assert L.neox_linear_workspace(forward(**shared)[0]) == p.shares * 128 * 128 * 4
