@@ -18,8 +18,9 @@ struct DropoutArgs {
 };
 
 constexpr uint32_t kDeep = 2;              // rows a thread has in flight
+constexpr uint64_t kStreaming = 1ull << 26; // bytes of a pass from which on its accesses are non-temporal
 
-template <int DT>
+template <int DT, bool NT>
 __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp) {
     const Unit u(sp, kDeep);
     const uint32_t c = u.unit * 8;
@@ -32,8 +33,8 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp) 
     for (uint32_t k = 0; k < kDeep; ++k) {
         const uint64_t row = u.row + k * u.step;
         if (row >= a.rows) break;
-        load8<DT>(a.x, row * a.x_ld + c, n, x[k]);
-        if (a.residual) load8<DT>(a.residual, row * a.r_ld + c, n, r[k]);
+        load8<DT, NT>(a.x, row * a.x_ld + c, n, x[k]);
+        if (a.residual) load8<DT, NT>(a.residual, row * a.r_ld + c, n, r[k]);
     }
 #pragma unroll
     for (uint32_t k = 0; k < kDeep; ++k) {
@@ -48,20 +49,23 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp) 
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[k][e] = opaque(x[k][e]);
-        store8<DT>(a.y, row * a.y_ld + c, n, x[k]);
+        store8<DT, NT>(a.y, row * a.y_ld + c, n, x[k]);
     }
 }
 
-// The way back.  A block takes `across` columns of a run of rows and adds up what it makes of
-// them, column by column: eight sums a thread, joined in order over the threads of one column,
-// then over the runs by join_kernel.  So the sums' order goes by the sizes alone.
+// The way back.  A block takes a stripe of columns and every count-th row (of groups of 256 / wide
+// of them), so that the blocks under way sweep over neighbouring rows together, and adds up what
+// it makes of them column by column: eight sums a thread, joined in order over the threads of one
+// column, then over the blocks by join_kernel.  The sums' order goes by the sizes alone.
 struct BackArgs {
     Backward b;
-    float* part;               // [runs][cols], or null: no sums, or one run that writes dbias
-    uint64_t run;              // rows of a run
+    float* part;               // [count][cols], or null: no sums, or one block that writes dbias
     uint32_t across, shift;    // as in Spread
+    uint32_t count;            // blocks that share the rows
 };
 constexpr uint32_t kDeepBack = 4;
+
+constexpr uint32_t kMostBlocks = 1024;
 
 template <int DT>
 __device__ __forceinline__ void put_bias(const Backward& b, uint32_t c, float v) {
@@ -69,7 +73,7 @@ __device__ __forceinline__ void put_bias(const Backward& b, uint32_t c, float v)
     store_elem(b.dbias, DT, c, opaque(v));
 }
 
-template <int DT, int ACT>
+template <int DT, int ACT, bool NT>
 __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
     __shared__ float sums[256 * 8];
     const Backward& b = a.b;
@@ -78,23 +82,23 @@ __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
     const uint32_t unit = ((blockIdx.x - down * a.across) << a.shift) + (threadIdx.x & (wide - 1));
     const uint32_t c = unit * 8;
     const uint32_t cols = (uint32_t)b.cols, n = c < cols ? cols - c : 0;
-    const uint64_t first = down * a.run, last = min(b.rows, first + a.run);
     const uint64_t off = drop_offset(b.drop);
     float s[8] = {};
     if (n) {
-        for (uint64_t row0 = first + (threadIdx.x >> a.shift); row0 < last; row0 += kDeepBack * step) {
+        const uint64_t apart = (uint64_t)a.count * step;
+        for (uint64_t row0 = down * step + (threadIdx.x >> a.shift); row0 < b.rows; row0 += kDeepBack * apart) {
             float d[kDeepBack][8], p[kDeepBack][8];
 #pragma unroll
             for (uint32_t k = 0; k < kDeepBack; ++k) {
-                const uint64_t row = row0 + k * step;
-                if (row >= last) break;
-                load8<DT>(b.dy, row * b.dy_ld + c, n, d[k]);
-                if constexpr (ACT != NEOX_ACT_NONE) load8<DT>(b.pre, row * b.pre_ld + c, n, p[k]);
+                const uint64_t row = row0 + k * apart;
+                if (row >= b.rows) break;
+                load8<DT, NT>(b.dy, row * b.dy_ld + c, n, d[k]);
+                if constexpr (ACT != NEOX_ACT_NONE) load8<DT, NT>(b.pre, row * b.pre_ld + c, n, p[k]);
             }
 #pragma unroll
             for (uint32_t k = 0; k < kDeepBack; ++k) {
-                const uint64_t row = row0 + k * step;
-                if (row >= last) break;
+                const uint64_t row = row0 + k * apart;
+                if (row >= b.rows) break;
                 if constexpr (ACT != NEOX_ACT_NONE) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) d[k][e] *= slope<ACT>(p[k][e]);
@@ -105,7 +109,7 @@ __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
                     d[k][e] = opaque(d[k][e]);
                     s[e] += d[k][e];
                 }
-                if (b.d) store8<DT>(b.d, row * b.d_ld + c, b.padded ? 8 : n, d[k]);
+                if (b.d) store8<DT, NT>(b.d, row * b.d_ld + c, b.padded ? 8 : n, d[k]);
             }
         }
     }
@@ -127,14 +131,20 @@ __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
         }
 }
 
-// Sums the runs' sums: 64 columns and 16 shares of the runs a block.
+// Sums the blocks' sums: 64 columns and 16 shares of them a block, eight loads a thread under way.
 template <int DT>
-__global__ __launch_bounds__(1024) void join_kernel(Backward b, const float* part, uint32_t runs) {
+__global__ __launch_bounds__(1024) void join_kernel(Backward b, const float* part, uint32_t count) {
     __shared__ float sums[16][64];
     const uint32_t c = blockIdx.x * 64 + (threadIdx.x & 63), share = threadIdx.x >> 6;
     float s = 0.0f;
     if (c < b.cols)
-        for (uint32_t r = share; r < runs; r += 16) s += part[(uint64_t)r * b.cols + c];
+        for (uint32_t r = share; r < count; r += 16 * 8) {
+            float t[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) t[k] = r + 16 * k < count ? part[(uint64_t)(r + 16 * k) * b.cols + c] : 0.0f;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) s += t[k];
+        }
     sums[share][threadIdx.x & 63] = s;
     __syncthreads();
     if (share || c >= b.cols) return;
@@ -149,21 +159,16 @@ __global__ __launch_bounds__(256) void no_rows_kernel(Backward b) {
     if (c < b.cols) put_bias<DT>(b, (uint32_t)c, 0.0f);
 }
 
-// Runs of rows for the sums: enough blocks for the chip, but not so many that their sums weigh
-// against the rows.
-struct Runs {
+// Blocks of the way back: enough for the chip, but not so many that their sums weigh against the
+// rows.
+struct Blocks {
     uint32_t shift, across, count;
-    uint64_t rows;             // of a run
 };
-Runs runs_of(uint64_t rows, uint64_t cols) {
-    const Spread s = spread(1, (cols + 7) / 8, 1);
-    Runs r{s.shift, s.across, 0, 0};
-    const uint64_t least = (256u >> r.shift) * kDeepBack;       // rows a block has in flight
-    const uint64_t most = std::max<uint64_t>(1, 1024 / r.across);
-    const uint64_t want = std::min((rows + least - 1) / least, most);
-    r.rows = ((rows + want - 1) / std::max<uint64_t>(want, 1) + least - 1) / least * least;
-    r.count = r.rows ? (uint32_t)((rows + r.rows - 1) / r.rows) : 0;
-    return r;
+Blocks blocks_of(uint64_t rows, uint64_t cols) {
+    const Spread s = spread_close(1, (cols + 7) / 8, 1);
+    const uint64_t least = (256u >> s.shift) * kDeepBack;       // rows a block has in flight
+    const uint64_t most = std::max<uint64_t>(1, kMostBlocks / s.across);
+    return Blocks{s.shift, s.across, (uint32_t)std::min((rows + least - 1) / least, most)};
 }
 
 template <class F>
@@ -179,24 +184,32 @@ hipError_t launch_dropout(const void* x, uint64_t x_ld, const void* bias, const 
                           void* y, uint64_t y_ld, uint64_t rows, uint64_t cols, int32_t dtype, const Drop& drop,
                           hipStream_t stream) {
     const uint64_t size = dtype == NEOX_F32 ? 4 : 2;
+    const bool nt = rows * cols * size * (residual ? 3 : 2) >= kStreaming;
     rows_in_grids(rows, (cols + 7) / 8, kDeep, [&](uint64_t r, uint64_t n, const Spread& sp) {
         const DropoutArgs a{(const uint8_t*)x + r * x_ld * size, bias,
                             residual ? (const uint8_t*)residual + r * residual_ld * size : nullptr,
                             (uint8_t*)y + r * y_ld * size, x_ld, residual_ld, y_ld, n, r, (uint32_t)cols, drop};
         with_dtype(dtype, [&](auto dt) {
-            dropout_kernel<decltype(dt)::value><<<(uint32_t)sp.blocks, 256, 0, stream>>>(a, sp);
+            constexpr int DT = decltype(dt)::value;
+            if (nt) dropout_kernel<DT, true><<<(uint32_t)sp.blocks, 256, 0, stream>>>(a, sp);
+            else dropout_kernel<DT, false><<<(uint32_t)sp.blocks, 256, 0, stream>>>(a, sp);
         });
-    });
+    }, spread_close);
     return hipGetLastError();
 }
 
 uint64_t backward_workspace(uint64_t rows, uint64_t cols) {
-    const Runs r = runs_of(rows, cols);
+    const Blocks r = blocks_of(rows, cols);
     return r.count > 1 ? (r.count * cols * 4 + 255) / 256 * 256 : 0;
 }
 
 hipError_t launch_backward(const Backward& b, void* workspace, hipStream_t stream) {
-    const Runs r = runs_of(b.rows, b.cols);
+    // without an act and sums it is dropout of dy
+    if (!b.dbias && !b.pre && !b.padded)
+        return launch_dropout(b.dy, b.dy_ld, nullptr, nullptr, 0, b.d, b.d_ld, b.rows, b.cols, b.dtype, b.drop, stream);
+    const Blocks r = blocks_of(b.rows, b.cols);
+    const uint64_t arrays = 1 + (b.pre ? 1 : 0) + (b.d ? 1 : 0);
+    const bool nt = b.rows * b.cols * (b.dtype == NEOX_F32 ? 4 : 2) * arrays >= kStreaming;
     with_dtype(b.dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         if (b.rows == 0) {
@@ -204,9 +217,13 @@ hipError_t launch_backward(const Backward& b, void* workspace, hipStream_t strea
             return;
         }
         const bool join = b.dbias && r.count > 1;
-        const BackArgs a{b, join ? (float*)workspace : nullptr, r.rows, r.across, r.shift};
+        const BackArgs a{b, join ? (float*)workspace : nullptr, r.across, r.shift, r.count};
         const uint32_t blocks = r.across * r.count;
-        auto run = [&](auto act) { backward_kernel<DT, decltype(act)::value><<<blocks, 256, 0, stream>>>(a); };
+        auto run = [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
+            if (nt) backward_kernel<DT, ACT, true><<<blocks, 256, 0, stream>>>(a);
+            else backward_kernel<DT, ACT, false><<<blocks, 256, 0, stream>>>(a);
+        };
         // (only half types have an act)
         if constexpr (DT == NEOX_F32) run(std::integral_constant<int, NEOX_ACT_NONE>{});
         else with_act(b.act, run);

@@ -142,18 +142,30 @@ __host__ __device__ __forceinline__ void with_act(int32_t act, F f) {
 typedef tu32x4 __attribute__((aligned(2))) loose_u32x4;
 typedef tf32x4 __attribute__((aligned(4))) loose_f32x4;
 
-template <int DT>
+// NT: non-temporal, for what passes through once and is larger than the caches.
+template <bool NT, class T>
+__device__ __forceinline__ T get(const T* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool NT, class T>
+__device__ __forceinline__ void put(T* p, T v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+template <int DT, bool NT = false>
 __device__ __forceinline__ void load8(const void* p, uint64_t at, uint32_t n, float (&v)[8]) {
     if (n >= 8) {
         if constexpr (DT == NEOX_F32) {
-            const tf32x4 a = *(const loose_f32x4*)((const float*)p + at), b = *(const loose_f32x4*)((const float*)p + at + 4);
+            const tf32x4 a = get<NT>((const loose_f32x4*)((const float*)p + at));
+            const tf32x4 b = get<NT>((const loose_f32x4*)((const float*)p + at + 4));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[e] = a[e];
                 v[4 + e] = b[e];
             }
         } else {
-            const tu32x4 a = *(const loose_u32x4*)((const uint16_t*)p + at);
+            const tu32x4 a = get<NT>((const loose_u32x4*)((const uint16_t*)p + at));
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = half_to_float(DT, (uint16_t)(a[e / 2] >> (16 * (e & 1))));
         }
@@ -162,18 +174,18 @@ __device__ __forceinline__ void load8(const void* p, uint64_t at, uint32_t n, fl
         for (int e = 0; e < 8; ++e) v[e] = e < (int)n ? load_elem(p, DT, at + e) : 0.0f;
     }
 }
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void store8(void* p, uint64_t at, uint32_t n, const float (&v)[8]) {
     if (n >= 8) {
         if constexpr (DT == NEOX_F32) {
-            *(loose_f32x4*)((float*)p + at) = tf32x4{v[0], v[1], v[2], v[3]};
-            *(loose_f32x4*)((float*)p + at + 4) = tf32x4{v[4], v[5], v[6], v[7]};
+            put<NT>((loose_f32x4*)((float*)p + at), (loose_f32x4)tf32x4{v[0], v[1], v[2], v[3]});
+            put<NT>((loose_f32x4*)((float*)p + at + 4), (loose_f32x4)tf32x4{v[4], v[5], v[6], v[7]});
         } else {
             tu32x4 q;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 q[e] = float_to_half(DT, v[2 * e]) | (uint32_t)float_to_half(DT, v[2 * e + 1]) << 16;
-            *(loose_u32x4*)((uint16_t*)p + at) = q;
+            put<NT>((loose_u32x4*)((uint16_t*)p + at), (loose_u32x4)q);
         }
     } else {
 #pragma unroll

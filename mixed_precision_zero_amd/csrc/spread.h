@@ -23,6 +23,27 @@ inline Spread spread(uint64_t rows, uint64_t units, uint32_t deep) {
     s.blocks = (rows + per - 1) / per * s.across;
     return s;
 }
+// The same with as few idle threads as rows of 16 threads or more allow: the widest one that wastes
+// less than a tenth, or else the one that wastes least.
+inline Spread spread_close(uint64_t rows, uint64_t units, uint32_t deep) {
+    uint32_t best = 8;
+    double most = 0.0;
+    for (uint32_t shift = 8; shift >= 4; --shift) {
+        const double used = (double)units / (double)((units + (1ull << shift) - 1) >> shift << shift);
+        if (used > most) {
+            most = used;
+            best = shift;
+        }
+        if (used > 0.9) break;
+    }
+    while (best > 0 && units <= (1ull << best) / 2) --best;
+    Spread s{};
+    s.shift = best;
+    s.across = (uint32_t)((units + (1ull << best) - 1) >> best);
+    const uint64_t per = (256u >> best) * deep;
+    s.blocks = (rows + per - 1) / per * s.across;
+    return s;
+}
 struct Unit {
     uint64_t row;          // the first; the others `step` further each
     uint32_t unit;         // eight elements each
@@ -40,12 +61,12 @@ constexpr uint64_t kGrid = 1ull << 23;
 
 // Launches f(first row, rows, their spread) for as many rows at a time as a grid takes.
 template <class F>
-void rows_in_grids(uint64_t rows, uint64_t units, uint32_t deep, F f) {
-    const Spread one = spread(1, units, deep);          // (at most 2^20 blocks across)
+void rows_in_grids(uint64_t rows, uint64_t units, uint32_t deep, F f, Spread lay(uint64_t, uint64_t, uint32_t) = spread) {
+    const Spread one = lay(1, units, deep);             // (at most 2^20 blocks across)
     const uint64_t most = kGrid / one.across * ((256u >> one.shift) * deep);
     for (uint64_t r = 0; r < rows; r += most) {
         const uint64_t n = std::min(most, rows - r);
-        f(r, n, spread(n, units, deep));
+        f(r, n, lay(n, units, deep));
     }
 }
 
