@@ -153,26 +153,44 @@ __device__ __forceinline__ void put(T* p, T v) {
     if constexpr (NT) __builtin_nontemporal_store(v, p);
     else *p = v;
 }
+// Eight elements as they lie in memory, n of them (zeros for the others).
+template <int DT>
+struct Raw8 {
+    tu32x4 q[DT == NEOX_F32 ? 2 : 1];
+};
 template <int DT, bool NT = false>
-__device__ __forceinline__ void load8(const void* p, uint64_t at, uint32_t n, float (&v)[8]) {
+__device__ __forceinline__ Raw8<DT> raw8(const void* p, uint64_t at, uint32_t n) {
+    Raw8<DT> r;
     if (n >= 8) {
         if constexpr (DT == NEOX_F32) {
-            const tf32x4 a = get<NT>((const loose_f32x4*)((const float*)p + at));
-            const tf32x4 b = get<NT>((const loose_f32x4*)((const float*)p + at + 4));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = a[e];
-                v[4 + e] = b[e];
-            }
+            r.q[0] = __builtin_bit_cast(tu32x4, get<NT>((const loose_f32x4*)((const float*)p + at)));
+            r.q[1] = __builtin_bit_cast(tu32x4, get<NT>((const loose_f32x4*)((const float*)p + at + 4)));
         } else {
-            const tu32x4 a = get<NT>((const loose_u32x4*)((const uint16_t*)p + at));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = half_to_float(DT, (uint16_t)(a[e / 2] >> (16 * (e & 1))));
+            r.q[0] = get<NT>((const loose_u32x4*)((const uint16_t*)p + at));
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < (int)n ? load_elem(p, DT, at + e) : 0.0f;
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (DT == NEOX_F32) {
+                r.q[e / 4][e % 4] = e < (int)n ? ((const uint32_t*)p)[at + e] : 0u;
+            } else {
+                const uint32_t h = e < (int)n ? ((const uint16_t*)p)[at + e] : 0u;
+                r.q[0][e / 2] = e & 1 ? r.q[0][e / 2] | h << 16 : h;
+            }
+        }
     }
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ float element(const Raw8<DT>& r, int e) {
+    if constexpr (DT == NEOX_F32) return __uint_as_float(r.q[e / 4][e % 4]);
+    else return half_to_float(DT, (uint16_t)(r.q[0][e / 2] >> (16 * (e & 1))));
+}
+template <int DT, bool NT = false>
+__device__ __forceinline__ void load8(const void* p, uint64_t at, uint32_t n, float (&v)[8]) {
+    const Raw8<DT> r = raw8<DT, NT>(p, at, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = element(r, e);
 }
 template <int DT, bool NT = false>
 __device__ __forceinline__ void store8(void* p, uint64_t at, uint32_t n, const float (&v)[8]) {
@@ -207,51 +225,50 @@ struct Result {
     uint64_t ld;
     uint32_t I, J;             // columns, rows
     int32_t dtype;             // of out
-    bool accumulate, epilogue;
-    Epilogue e;
+    Epilogue e;                // (of nothing: all zero)
 };
-// Takes the sums of elements (row, col) to (row, col + 7), col a multiple of 8, to memory.
+// Takes the sums of elements (row, col) to (row, col + 7), col a multiple of 8, to memory; bias and
+// residual: what lies there (looked at where there are such).
 template <int DT, int HT>
-__device__ __forceinline__ void emit8(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8]) {
+__device__ __forceinline__ void emit8(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8],
+                                      const Raw8<HT>& bias, const Raw8<DT>& residual) {
     const uint32_t n = r.I - col;
-    float t[8];
-    if (r.epilogue) {
-        if (r.e.bias) {
-            load8<HT>(r.e.bias, col, n, t);
+    if (r.e.bias) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += t[e];
-        }
-        if (r.e.pre) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);
-            store8<HT>(r.e.pre, row * r.e.pre_ld + col, n, v);
-        }
-        with_act(r.e.act, [&](auto act) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = activate<decltype(act)::value>(v[e]);
-        });
-        if (r.e.drop.limit) drop8(r.e.drop, off, row, col / 8, v);
-        if (r.e.residual) {
-            load8<DT>(r.e.residual, row * r.e.residual_ld + col, n, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += t[e];
-        }
+        for (int e = 0; e < 8; ++e) v[e] += element(bias, e);
     }
-    if (r.accumulate) {
-        load8<DT>(r.out, row * r.ld + col, n, t);
+    if (r.e.pre) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += t[e];
+        for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);
+        store8<HT>(r.e.pre, row * r.e.pre_ld + col, n, v);
+    }
+    with_act(r.e.act, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = activate<decltype(act)::value>(v[e]);
+    });
+    if (r.e.drop.limit) drop8(r.e.drop, off, row, col / 8, v);
+    if (r.e.residual) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += element(residual, e);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);
     store8<DT>(r.out, row * r.ld + col, n, v);
 }
-
-// ... with out's type looked at: HT's own or FP32.
+template <int HT>
+__device__ __forceinline__ Raw8<HT> bias8(const Result& r, uint32_t col) {
+    return r.e.bias ? raw8<HT>(r.e.bias, col, r.I - col) : Raw8<HT>{};
+}
+template <int DT>
+__device__ __forceinline__ Raw8<DT> residual8(const Result& r, uint32_t row, uint32_t col) {
+    return r.e.residual ? raw8<DT>(r.e.residual, row * r.e.residual_ld + col, r.I - col) : Raw8<DT>{};
+}
+// The same of elements that come one by one; out of type HT or FP32.
 template <int HT>
 __device__ __forceinline__ void emit8_any(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8]) {
-    if (r.dtype == NEOX_F32) emit8<NEOX_F32, HT>(r, off, row, col, v);
-    else emit8<HT, HT>(r, off, row, col, v);
+    const Raw8<HT> bias = bias8<HT>(r, col);
+    if (r.dtype == NEOX_F32) emit8<NEOX_F32, HT>(r, off, row, col, v, bias, residual8<NEOX_F32>(r, row, col));
+    else emit8<HT, HT>(r, off, row, col, v, bias, residual8<HT>(r, row, col));
 }
 
 // The results of a wave's part of a block tile, through the wave's own part of LDS in FP32: there
@@ -293,14 +310,23 @@ __device__ __forceinline__ void emit_tile(const Result& r, const Core& t, uint32
                         t.acc[piece % kAcross * R::kU + u][piece / kAcross * R::kV + v];
             // A wave's LDS operations execute in order; the compiler must keep them so too.
             asm volatile("" ::: "memory");
+            constexpr int DT = decltype(dt)::value;
             const uint32_t c = bi + lane % kLanes * 8;
+            uint32_t k = lane / kLanes;
+            const uint32_t rows = c < r.I ? min((uint32_t)R::kRows, r.J - bj) : 0u;
+            if (k < rows) {
+                // the next row's residual is under way while this one is worked on
+                const Raw8<HT> bias = bias8<HT>(r, c);
+                Raw8<DT> residual = residual8<DT>(r, bj + k, c);
 #pragma unroll 1
-            for (uint32_t k = lane / kLanes; k < R::kRows; k += kStep) {
-                if (bj + k >= r.J || c >= r.I) break;
-                const tf32x4* s = (const tf32x4*)(l + k * R::kPitch + lane % kLanes * 32);
-                const tf32x4 a = s[0], b = s[1];
-                float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-                emit8<decltype(dt)::value, HT>(r, off, bj + k, c, x);
+                for (; k < rows; k += kStep) {
+                    const tf32x4* s = (const tf32x4*)(l + k * R::kPitch + lane % kLanes * 32);
+                    const tf32x4 a = s[0], b = s[1];
+                    float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                    const Raw8<DT> now = residual;
+                    if (k + kStep < rows) residual = residual8<DT>(r, bj + k + kStep, c);
+                    emit8<DT, HT>(r, off, bj + k, c, x, bias, now);
+                }
             }
             asm volatile("" ::: "memory");
         }

@@ -172,7 +172,6 @@ int take_linear(const neox_linear_args* a, Arrays& arr, Product& p) {
     arr.reads("x", a->x, a->m, a->k, a->x_ld, 2);
     arr.reads("w", a->w, a->n, a->k, a->w_ld, 2);
     if (arr.check()) return arr.rc;
-    const Epilogue& e = p.epi;
     p.p = Operand{(const uint16_t*)a->w, a->n > 1 ? a->w_ld : a->k, false, false};
     p.q = Operand{(const uint16_t*)a->x, a->m > 1 ? a->x_ld : a->k, false, false};
     p.I = (uint32_t)a->n;
@@ -182,7 +181,6 @@ int take_linear(const neox_linear_args* a, Arrays& arr, Product& p) {
     p.out_dtype = a->y_dtype;
     p.out = a->y;
     p.out_ld = a->y_ld;
-    p.epilogue = e.bias || e.residual || e.pre || e.act || e.drop.limit;
     return NEOX_OK;
 }
 
@@ -226,8 +224,8 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
     g.has_dw = a->dw != nullptr;
     const bool made = (act || b.drop.limit) && (g.has_dx || g.has_dw) && m;
     g.pass = made || a->dbias;
-    // rows of d begin at multiples of 16 bytes
-    const uint64_t d_ld = round_up(n, 8);
+    // rows of d are whole lines of 128 bytes
+    const uint64_t d_ld = round_up(n, 64);
     g.d_bytes = made ? round_up(m * d_ld * 2, 256) : 0;
     b.dy = a->dy;
     b.pre = act ? (const uint16_t*)a->pre : nullptr;
@@ -262,7 +260,10 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
     if (g.has_dw) {
         g.dw = product(Operand{(const uint16_t*)a->x, m > 1 ? a->x_ld : k, true, false}, Operand{dy.at, dy.ld, true, made}, k, n, m,
                        a->dw, n > 1 ? a->dw_ld : k);
-        g.dw.accumulate = a->accumulate != 0;
+        if (a->accumulate) {
+            g.dw.epi.residual = a->dw;
+            g.dw.epi.residual_ld = g.dw.out_ld;
+        }
     }
     // the passes run one after the other, so what follows d serves each in turn
     uint64_t rest = a->dbias ? backward_workspace(m, n) : 0;

@@ -41,9 +41,7 @@ struct Product {
     int32_t out_dtype;
     void* out;
     uint64_t out_ld;
-    bool accumulate;           // out += (then no epilogue)
-    bool epilogue;             // whether epi holds anything
-    Epilogue epi;
+    Epilogue epi;              // (of nothing: all zero)
 };
 // Which kernel a product takes, and into how many shares of how many slabs (64 elements) its sums
 // over K are split: by the sizes alone.  Deep: four slabs of K in LDS instead of two, for launches
