@@ -246,11 +246,12 @@ hipError_t launch_product(const Product& p, void* workspace, hipStream_t stream)
     uint8_t* work = (uint8_t*)workspace;
     Operand P = p.p, Q = p.q;
     pack(P, p.I, Q, p.J, p.K, work, stream);
-    const Result r{p.out, p.out_ld, p.I, p.J, p.out_dtype, p.epi};
+    const bool beyond = (uint64_t)p.I * p.J * (p.out_dtype == NEOX_F32 ? 4 : 2) >= kBeyond;
+    const Result r{p.out, p.out_ld, p.I, p.J, p.out_dtype, beyond, p.epi};
     TileArgs a{(const uint8_t*)P.at, (const uint8_t*)Q.at, (uint32_t)(P.ld * 2), (uint32_t)(Q.ld * 2), p.K, c.slabs,
                c.shares, r};
     if (c.shares > 1) {
-        a.r = Result{work, part_ld(p.I), p.I, p.J, NEOX_F32, Epilogue{}};
+        a.r = Result{work, part_ld(p.I), p.I, p.J, NEOX_F32, false, Epilogue{}};
     }
     auto run = [&](auto ht) {
         constexpr int HT = decltype(ht)::value;
