@@ -1,5 +1,6 @@
 // dropout_kernels.hip -- the element-wise passes of the linear layer on gfx950: dropout with
 // bias and residual, and the way back through dropout and activation with the columns' sums.
+#include "column_sums.h"
 #include "epilogue.h"
 #include "spread.h"
 
@@ -65,13 +66,7 @@ struct BackArgs {
 };
 constexpr uint32_t kDeepBack = 4;
 
-constexpr uint32_t kMostBlocks = 1024;
-
-template <int DT>
-__device__ __forceinline__ void put_bias(const Backward& b, uint32_t c, float v) {
-    if (b.accumulate) v += load_elem(b.dbias, DT, c);
-    store_elem(b.dbias, DT, c, opaque(v));
-}
+constexpr uint32_t kMostBlocks = 768;
 
 template <int DT, int ACT, bool NT>
 __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
@@ -131,25 +126,10 @@ __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
         }
 }
 
-// Sums the blocks' sums: 64 columns and 16 shares of them a block, eight loads a thread under way.
 template <int DT>
 __global__ __launch_bounds__(1024) void join_kernel(Backward b, const float* part, uint32_t count) {
-    __shared__ float sums[16][64];
-    const uint32_t c = blockIdx.x * 64 + (threadIdx.x & 63), share = threadIdx.x >> 6;
-    float s = 0.0f;
-    if (c < b.cols)
-        for (uint32_t r = share; r < count; r += 16 * 8) {
-            float t[8];
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) t[k] = r + 16 * k < count ? part[(uint64_t)(r + 16 * k) * b.cols + c] : 0.0f;
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) s += t[k];
-        }
-    sums[share][threadIdx.x & 63] = s;
-    __syncthreads();
-    if (share || c >= b.cols) return;
-    for (int k = 1; k < 16; ++k) s += sums[k][threadIdx.x];
-    put_bias<DT>(b, c, s);
+    __shared__ float sums[16 * 64];
+    join_columns<DT>(b, part, count, blockIdx.x, sums);
 }
 
 // dbias of no rows
@@ -198,12 +178,17 @@ hipError_t launch_dropout(const void* x, uint64_t x_ld, const void* bias, const 
     return hipGetLastError();
 }
 
+uint32_t backward_parts(uint64_t rows, uint64_t cols) {
+    const uint32_t n = blocks_of(rows, cols).count;
+    return n > 1 ? n : 0;
+}
+
 uint64_t backward_workspace(uint64_t rows, uint64_t cols) {
     const Blocks r = blocks_of(rows, cols);
     return r.count > 1 ? (r.count * cols * 4 + 255) / 256 * 256 : 0;
 }
 
-hipError_t launch_backward(const Backward& b, void* workspace, hipStream_t stream) {
+hipError_t launch_backward(const Backward& b, void* workspace, bool join_here, hipStream_t stream) {
     // without an act and sums it is dropout of dy
     if (!b.dbias && !b.pre && !b.padded)
         return launch_dropout(b.dy, b.dy_ld, nullptr, nullptr, 0, b.d, b.d_ld, b.rows, b.cols, b.dtype, b.drop, stream);
@@ -227,9 +212,17 @@ hipError_t launch_backward(const Backward& b, void* workspace, hipStream_t strea
         // (only half types have an act)
         if constexpr (DT == NEOX_F32) run(std::integral_constant<int, NEOX_ACT_NONE>{});
         else with_act(b.act, run);
-        if (join)
-            join_kernel<DT><<<(uint32_t)((b.cols + 63) / 64), 1024, 0, stream>>>(b, (const float*)workspace, r.count);
     });
+    if (join_here) return launch_join(b, workspace, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(const Backward& b, const void* workspace, hipStream_t stream) {
+    const uint32_t parts = backward_parts(b.rows, b.cols);
+    if (b.dbias && parts)
+        with_dtype(b.dtype, [&](auto dt) {
+            join_kernel<decltype(dt)::value><<<(uint32_t)((b.cols + 63) / 64), 1024, 0, stream>>>(b, (const float*)workspace, parts);
+        });
     return hipGetLastError();
 }
 

@@ -234,25 +234,28 @@ constexpr uint64_t kBeyond = 1ull << 28;
 // residual is read, and FP32 written, past them only where they could not hold it: 1968 -> 1914
 // and 2044 -> 1925 us there, but 20.0 -> 24.3 and 23.6 -> 29.4 at 2048 x 4096 x 1024.
 // Takes the sums of elements (row, col) to (row, col + 7), col a multiple of 8, to memory; bias and
-// residual: what lies there (looked at where there are such).
-template <int DT, int HT>
+// residual: what lies there (looked at where there are such).  LAYER: whether there may be anything
+// but a residual.
+template <int DT, int HT, bool LAYER>
 __device__ __forceinline__ void emit8(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8],
                                       const Raw8<HT>& bias, const Raw8<DT>& residual) {
     const uint32_t n = r.I - col;
-    if (r.e.bias) {
+    if constexpr (LAYER) {
+        if (r.e.bias) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += element(bias, e);
+            for (int e = 0; e < 8; ++e) v[e] += element(bias, e);
+        }
+        if (r.e.pre) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);
+            store8<HT, true>(r.e.pre, row * r.e.pre_ld + col, n, v);
+        }
+        with_act(r.e.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = activate<decltype(act)::value>(v[e]);
+        });
+        if (r.e.drop.limit) drop8(r.e.drop, off, row, col / 8, v);
     }
-    if (r.e.pre) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);
-        store8<HT, true>(r.e.pre, row * r.e.pre_ld + col, n, v);
-    }
-    with_act(r.e.act, [&](auto act) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = activate<decltype(act)::value>(v[e]);
-    });
-    if (r.e.drop.limit) drop8(r.e.drop, off, row, col / 8, v);
     if (r.e.residual) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += element(residual, e);
@@ -276,8 +279,8 @@ __device__ __forceinline__ Raw8<DT> residual8(const Result& r, uint32_t row, uin
 template <int HT>
 __device__ __forceinline__ void emit8_any(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8]) {
     const Raw8<HT> bias = bias8<HT>(r, col);
-    if (r.dtype == NEOX_F32) emit8<NEOX_F32, HT>(r, off, row, col, v, bias, residual8<NEOX_F32>(r, row, col));
-    else emit8<HT, HT>(r, off, row, col, v, bias, residual8<HT>(r, row, col));
+    if (r.dtype == NEOX_F32) emit8<NEOX_F32, HT, true>(r, off, row, col, v, bias, residual8<NEOX_F32>(r, row, col));
+    else emit8<HT, HT, true>(r, off, row, col, v, bias, residual8<HT>(r, row, col));
 }
 
 // The results of a wave's part of a block tile, through the wave's own part of LDS in FP32: there
@@ -294,7 +297,7 @@ struct Rows {
     static_assert(kBytes * kWaves <= Core::kLds, "");
     static_assert(Core::TP % kU == 0 && Core::TQ % kV == 0, "");
 };
-template <int HT, class Core>
+template <int HT, bool LAYER = true, class Core>
 __device__ __forceinline__ void emit_tile(const Result& r, const Core& t, uint32_t i0, uint32_t j0, uint8_t* lds) {
     using R = Rows<Core>;
     const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
@@ -325,7 +328,7 @@ __device__ __forceinline__ void emit_tile(const Result& r, const Core& t, uint32
             const uint32_t rows = c < r.I ? min((uint32_t)R::kRows, r.J - bj) : 0u;
             if (k < rows) {
                 // the next row's residual is under way while this one is worked on
-                const Raw8<HT> bias = bias8<HT>(r, c);
+                const Raw8<HT> bias = LAYER ? bias8<HT>(r, c) : Raw8<HT>{};
                 Raw8<DT> residual = residual8<DT>(r, bj + k, c);
 #pragma unroll 1
                 for (; k < rows; k += kStep) {
@@ -334,7 +337,7 @@ __device__ __forceinline__ void emit_tile(const Result& r, const Core& t, uint32
                     float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
                     const Raw8<DT> now = residual;
                     if (k + kStep < rows) residual = residual8<DT>(r, bj + k + kStep, c);
-                    emit8<DT, HT>(r, off, bj + k, c, x, bias, now);
+                    emit8<DT, HT, LAYER>(r, off, bj + k, c, x, bias, now);
                 }
             }
             asm volatile("" ::: "memory");

@@ -191,6 +191,7 @@ struct Gradients {
     Product dx{}, dw{};
     bool has_dx = false, has_dw = false;
     uint64_t d_bytes = 0;      // d itself, if it is not dy
+    uint64_t sums_bytes = 0;   // the parts of dbias
     uint64_t bytes = 0;        // in all
 };
 
@@ -265,11 +266,8 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
             g.dw.epi.residual_ld = g.dw.out_ld;
         }
     }
-    // the passes run one after the other, so what follows d serves each in turn
-    uint64_t rest = a->dbias ? backward_workspace(m, n) : 0;
-    if (g.has_dx) rest = std::max(rest, product_workspace(g.dx));
-    if (g.has_dw) rest = std::max(rest, product_workspace(g.dw));
-    g.bytes = g.d_bytes + rest;
+    g.sums_bytes = a->dbias ? backward_workspace(m, n) : 0;
+    g.bytes = g.d_bytes + g.sums_bytes + products_workspace(g.has_dx ? &g.dx : nullptr, g.has_dw ? &g.dw : nullptr);
     return NEOX_OK;
 }
 
@@ -281,7 +279,7 @@ extern "C" int neox_linear_workspace(const neox_linear_args* a, uint64_t* bytes)
     Product p;
     const int rc = take_linear(a, arr, p);
     if (rc) return rc;
-    *bytes = p.J ? product_workspace(p) : 0;
+    *bytes = p.J ? products_workspace(&p, nullptr) : 0;
     return NEOX_OK;
 }
 
@@ -291,9 +289,9 @@ extern "C" int neox_linear(const neox_linear_args* a, void* workspace, uint64_t 
     int rc = take_linear(a, arr, p);
     if (rc) return rc;
     if (p.J == 0) return NEOX_OK;
-    rc = arr.check_workspace(workspace, workspace_bytes, product_workspace(p));
+    rc = arr.check_workspace(workspace, workspace_bytes, products_workspace(&p, nullptr));
     if (rc) return rc;
-    const hipError_t e = launch_product(p, workspace, static_cast<hipStream_t>(hip_stream));
+    const hipError_t e = launch_products(&p, nullptr, nullptr, nullptr, workspace, static_cast<hipStream_t>(hip_stream));
     return e == hipSuccess ? NEOX_OK : set_hip_error(e, "linear launch");
 }
 
@@ -316,15 +314,17 @@ extern "C" int neox_linear_backward(const neox_linear_grads* a, void* workspace,
     rc = arr.check_workspace(workspace, workspace_bytes, g.bytes);
     if (rc) return rc;
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    uint8_t* rest = (uint8_t*)workspace + g.d_bytes;
+    uint8_t* sums = (uint8_t*)workspace + g.d_bytes;
     if (g.d_bytes) {
         g.d.d = workspace;
         g.dx.q.at = g.dw.q.at = (const uint16_t*)workspace;
     }
+    const bool products = g.has_dx || g.has_dw;
     hipError_t e = hipSuccess;
-    if (g.pass) e = launch_backward(g.d, rest, s);
-    if (e == hipSuccess && g.has_dx) e = launch_product(g.dx, rest, s);
-    if (e == hipSuccess && g.has_dw) e = launch_product(g.dw, rest, s);
+    if (g.pass) e = launch_backward(g.d, sums, !products, s);
+    if (e == hipSuccess && products)
+        e = launch_products(g.has_dx ? &g.dx : nullptr, g.has_dw ? &g.dw : nullptr, g.sums_bytes ? &g.d : nullptr, sums,
+                            sums + g.sums_bytes, s);
     return e == hipSuccess ? NEOX_OK : set_hip_error(e, "linear_backward launch");
 }
 
@@ -429,6 +429,6 @@ extern "C" int neox_dropout_backward(const void* dy, uint64_t dy_ld, void* dx, u
     b.cols = cols;
     b.dtype = dtype;
     b.accumulate = accumulate != 0;
-    const hipError_t e = launch_backward(b, workspace, static_cast<hipStream_t>(hip_stream));
+    const hipError_t e = launch_backward(b, workspace, true, static_cast<hipStream_t>(hip_stream));
     return e == hipSuccess ? NEOX_OK : set_hip_error(e, "dropout_backward launch");
 }

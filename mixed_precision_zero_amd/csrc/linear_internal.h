@@ -51,11 +51,9 @@ struct ProductPlan {
     ProductKernel kernel;
     uint32_t shares;
     uint64_t slabs;
+    double cost;               // us
 };
 ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K);
-uint64_t product_workspace(const Product& p);
-hipError_t launch_product(const Product& p, void* workspace, hipStream_t stream);
-
 // d = D(dy) act'(pre), and the sums of its columns.
 struct Backward {
     const void* dy;
@@ -69,8 +67,18 @@ struct Backward {
     bool padded;               // rows of d are filled with zeros up to a multiple of 8 elements
     Drop drop;
 };
-uint64_t backward_workspace(uint64_t rows, uint64_t cols);     // for dbias
-hipError_t launch_backward(const Backward& b, void* workspace, hipStream_t stream);
+// The sums of blocks that share the rows, [parts][cols] in FP32 in the workspace, are joined by
+// launch_join, or by a kernel that follows anyway; 0 parts: dbias is written at once.
+uint32_t backward_parts(uint64_t rows, uint64_t cols);
+uint64_t backward_workspace(uint64_t rows, uint64_t cols);
+hipError_t launch_backward(const Backward& b, void* workspace, bool join_here, hipStream_t stream);
+hipError_t launch_join(const Backward& b, const void* workspace, hipStream_t stream);
+
+// One product, or two (dx and dw) that may run side by side; either may be null.  join: null, or
+// sums of a launch_backward, in `sums`, that are joined too.
+uint64_t products_workspace(const Product* x, const Product* w);
+hipError_t launch_products(const Product* x, const Product* w, const Backward* join, const void* sums, void* workspace,
+                           hipStream_t stream);
 
 hipError_t launch_dropout(const void* x, uint64_t x_ld, const void* bias, const void* residual, uint64_t residual_ld,
                           void* y, uint64_t y_ld, uint64_t rows, uint64_t cols, int32_t dtype, const Drop& drop,

@@ -1,4 +1,5 @@
 // linear_kernels.hip -- products of half-precision matrices with an epilogue on gfx950.
+#include "column_sums.h"
 #include "epilogue.h"
 #include "spread.h"
 
@@ -30,7 +31,8 @@ __device__ __forceinline__ TileRows rows_of(const uint8_t* base, uint32_t pitch,
     else return TileRows{base + (uint64_t)first * pitch + k0 * 2, nullptr, side, pitch, 0};
 }
 
-template <class Core, int HT>
+// (only the layer's own product has more of an epilogue than a residual)
+template <class Core, int HT, bool LAYER = !Core::Form::kStridedP>
 __device__ __forceinline__ void linear_tile(const TileArgs& a, const TileAt& at, uint32_t share, uint8_t* lds) {
     const uint64_t k0 = share * a.slabs * 64;
     const uint32_t left = (uint32_t)min(a.K - k0, a.slabs * 64);
@@ -39,13 +41,9 @@ __device__ __forceinline__ void linear_tile(const TileArgs& a, const TileAt& at,
     Core t;
     // rows of K are zeros up to a multiple of 8
     t.run(p, q, (left + 7) / 8 * 16, lds);
-    if (a.shares > 1) {
-        Result r = a.r;
-        r.out = (float*)a.r.out + share * (uint64_t)a.r.J * a.r.ld;
-        emit_tile<HT>(r, t, at.i, at.j, lds);
-    } else {
-        emit_tile<HT>(a.r, t, at.i, at.j, lds);
-    }
+    Result r = a.r;
+    if (a.shares > 1) r.out = (float*)a.r.out + share * (uint64_t)a.r.J * a.r.ld;
+    emit_tile<HT, LAYER>(r, t, at.i, at.j, lds);
 }
 
 template <class Form>
@@ -69,17 +67,46 @@ __global__ __launch_bounds__(512, 2) void linear_mixed_kernel(TileArgs a, TileMa
 struct EvenMap {
     uint32_t across, down, per, blocks;     // per: tiles of a share
 };
-template <class Core, int HT>
-__global__ __launch_bounds__(Core::NT, Core::NT == 512 ? 4 : 2) void linear_even_kernel(TileArgs a, EvenMap m) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
-    const uint32_t x = blockIdx.x % 8, run = m.blocks / 8, more = m.blocks % 8;
-    const uint32_t b = x * run + min(x, more) + blockIdx.x / 8;
-    const uint32_t share = b / m.per, t = b - share * m.per;
+template <class Core>
+__device__ __forceinline__ TileAt even_tile(const EvenMap& m, uint32_t block, uint32_t& share) {
+    const uint32_t x = block % 8, run = m.blocks / 8, more = m.blocks % 8;
+    const uint32_t b = x * run + min(x, more) + block / 8;
+    share = b / m.per;
+    const uint32_t t = b - share * m.per;
     const uint32_t group = t / (8 * m.across), rows = min(8u, m.down - 8 * group), in = t - group * 8 * m.across;
     TileAt at{};
     at.i = in / rows * Core::BP;
     at.j = (8 * group + in % rows) * Core::BQ;
+    return at;
+}
+template <class Core, int HT>
+__global__ __launch_bounds__(Core::NT, Core::NT == 512 ? 4 : 2) void linear_even_kernel(TileArgs a, EvenMap m) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Core::kLds];
+    uint32_t share;
+    const TileAt at = even_tile<Core>(m, blockIdx.x, share);
     linear_tile<Core, HT>(a, at, share, lds);
+}
+// The joins of the bias's gradient (first: they wait for memory mostly), dx's tiles and dw's, side by
+// side: neither product of a few thousand tokens fills the chip alone.
+template <class CoreX, class CoreW, int HT>
+__global__ __launch_bounds__(CoreX::NT, CoreX::NT == 512 ? 4 : 2) void linear_pair_kernel(TileArgs x, EvenMap mx, TileArgs w,
+                                                                                          EvenMap mw, Backward b, const float* sums,
+                                                                                          uint32_t parts, uint32_t joins) {
+    static_assert(CoreX::kLds == CoreW::kLds && CoreX::NT == CoreW::NT, "");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[CoreX::kLds];
+    uint32_t share;
+    if (blockIdx.x < joins) {
+        join_columns<HT>(b, sums, parts, blockIdx.x, (float*)lds);
+        return;
+    }
+    const uint32_t block = blockIdx.x - joins;
+    if (block < mx.blocks) {
+        const TileAt at = even_tile<CoreX>(mx, block, share);
+        linear_tile<CoreX, HT>(x, at, share, lds);
+    } else {
+        const TileAt at = even_tile<CoreW>(mw, block - mx.blocks, share);
+        linear_tile<CoreW, HT>(w, at, share, lds);
+    }
 }
 
 // Adds up the shares in order and takes the sums through the epilogue.
@@ -98,8 +125,8 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, uint64_t l
     emit8_any<HT>(r, drop_offset(r.e.drop), (uint32_t)u.row, c, v);
 }
 
-// Copies rows of `cols` 16-bit elements into rows of `pitch` elements, zeros behind them; two
-// operands in one launch, the first by the first `blocks` blocks.
+// Copies rows of `cols` 16-bit elements into rows of `pitch` elements, zeros behind them; up to three
+// operands in one launch.
 struct Pack {
     const uint16_t* src;
     uint16_t* dst;
@@ -107,24 +134,32 @@ struct Pack {
     uint32_t cols, pitch;
     uint32_t blocks;
 };
-__global__ __launch_bounds__(256) void pack_kernel(Pack p, Pack q) {
-    const bool first = blockIdx.x < p.blocks;
-    const Pack& a = first ? p : q;
-    const uint32_t units = a.pitch / 8, block = first ? blockIdx.x : blockIdx.x - p.blocks;
-    const uint64_t all = a.rows * units, step = a.blocks * 256ull;
+__global__ __launch_bounds__(256) void pack_kernel(Pack p, Pack q, Pack r) {
+    uint32_t block = blockIdx.x;
+    const Pack* a = &p;
+    if (block >= p.blocks) {
+        block -= p.blocks;
+        a = &q;
+        if (block >= q.blocks) {
+            block -= q.blocks;
+            a = &r;
+        }
+    }
+    const uint32_t units = a->pitch / 8;
+    const uint64_t all = a->rows * units, step = a->blocks * 256ull;
     for (uint64_t u = block * 256ull + threadIdx.x; u < all; u += step) {
         const uint64_t row = u / units;
         const uint32_t c = (uint32_t)(u - row * units) * 8;
-        const uint16_t* s = a.src + row * a.ld + c;
+        const uint16_t* s = a->src + row * a->ld + c;
         tu32x4 v = {0, 0, 0, 0};
-        if (c + 8 <= a.cols) {
+        if (c + 8 <= a->cols) {
             v = *(const loose_u32x4*)s;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (c + e < a.cols) v[e / 2] |= (uint32_t)s[e] << (16 * (e & 1));
+                if (c + e < a->cols) v[e / 2] |= (uint32_t)s[e] << (16 * (e & 1));
         }
-        *(tu32x4*)(a.dst + u * 8) = v;
+        *(tu32x4*)(a->dst + u * 8) = v;
     }
 }
 
@@ -141,26 +176,7 @@ bool direct(const Operand& o, uint64_t side, uint64_t K) {
 // (whole 128-byte lines: 8192 x 24576 x 6144 takes 1780 us with rows of K + 64 elements, 2260 with
 // K + 8)
 uint64_t packed_pitch(const Operand& o, uint64_t side, uint64_t K) { return ((o.strided ? side : K) + 63) / 64 * 64; }
-uint64_t packed_bytes(const Operand& o, uint64_t side, uint64_t K) {
-    return direct(o, side, K) ? 0 : ((o.strided ? K : side) * packed_pitch(o, side, K) * 2 + 255) / 256 * 256;
-}
 uint64_t part_ld(uint64_t I) { return (I + 7) / 8 * 8; }
-
-// Copies what tiles cannot be loaded from; moves `work` behind the copies.
-void pack(Operand& p, uint64_t I, Operand& q, uint64_t J, uint64_t K, uint8_t*& work, hipStream_t stream) {
-    auto one = [&](Operand& o, uint64_t side) {
-        if (direct(o, side, K)) return Pack{};
-        const uint64_t rows = o.strided ? K : side, pitch = packed_pitch(o, side, K);
-        const Pack r{o.at, (uint16_t*)work, o.ld, rows, (uint32_t)(o.strided ? side : K), (uint32_t)pitch,
-                     (uint32_t)std::min<uint64_t>((rows * pitch / 8 + 255) / 256, 1u << 13)};
-        work += packed_bytes(o, side, K);
-        o.at = r.dst;
-        o.ld = pitch;
-        return r;
-    };
-    const Pack a = one(p, I), b = one(q, J);
-    if (a.blocks + b.blocks) pack_kernel<<<a.blocks + b.blocks, 256, 0, stream>>>(a, b);
-}
 
 // The launch of 256 x 256 tiles, and its cost (see product_plan).
 TileMap tiles256(uint32_t I, uint32_t J, uint64_t slabs, double* cost, uint64_t* blocks) {
@@ -171,16 +187,20 @@ template <class T>
 struct Type {
     using type = T;
 };
+EvenMap even_map(const TileArgs& a, uint32_t unit) {
+    EvenMap m{};
+    m.across = (a.r.I + unit - 1) / unit;
+    m.down = (a.r.J + unit - 1) / unit;
+    m.per = m.across * m.down;
+    m.blocks = m.per * a.shares;
+    return m;
+}
 template <class Form, int HT>
-void launch_tiles(TileArgs a, const ProductPlan& c, hipStream_t stream) {
+void launch_tiles(const TileArgs& a, const ProductPlan& c, hipStream_t stream) {
     const uint32_t I = a.r.I, J = a.r.J;
     auto even = [&](auto core) {
         using Core = typename decltype(core)::type;
-        EvenMap m{};
-        m.across = (I + Core::BP - 1) / Core::BP;
-        m.down = (J + Core::BQ - 1) / Core::BQ;
-        m.per = m.across * m.down;
-        m.blocks = m.per * c.shares;
+        const EvenMap m = even_map(a, Core::BP);
         linear_even_kernel<Core, HT><<<m.blocks, Core::NT, 0, stream>>>(a, m);
     };
     switch (c.kernel) {
@@ -194,6 +214,22 @@ void launch_tiles(TileArgs a, const ProductPlan& c, hipStream_t stream) {
         linear_mixed_kernel<Form, HT><<<(uint32_t)blocks, 512, 0, stream>>>(a, map);
     }
     }
+}
+
+// Costs of a launch of even tiles, in us (see product_plan): of one block, and of them all.
+struct EvenCost {
+    uint64_t fit, few;
+    double c_few, c, round;
+};
+constexpr EvenCost kCost[3] = {{512, 256, 0.27, 0.53, 0.9}, {512, 256, 0.66, 0.91, 3.5}, {256, 128, 0.42, 0.50, 3.2}};
+double block_cost(const EvenCost& k, uint64_t blocks, uint64_t slabs) {
+    return (double)slabs * (blocks <= k.few ? k.c_few : k.c) + k.round;
+}
+double even_cost(const EvenCost& k, uint64_t blocks, uint64_t slabs) {
+    return (blocks <= k.fit ? 1.0 : (double)blocks / (double)k.fit + 0.42) * block_cost(k, blocks, slabs);
+}
+double join_cost(uint64_t shares, uint64_t I, uint64_t J) {
+    return shares == 1 ? 0.0 : 3.7 + (double)(shares * I * J) * 8e-6 / 5.7;
 }
 
 }  // namespace
@@ -210,64 +246,150 @@ void launch_tiles(TileArgs a, const ProductPlan& c, hipStream_t stream) {
 // mostly.  Blocks beyond a round start as others end: a part of a round more.
 ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K) {
     const uint64_t slabs = std::max<uint64_t>(1, (K + 63) / 64), n64 = tiles(I, J, 64), n128 = tiles(I, J, 128);
-    ProductPlan best{kTiles256, 1, slabs};
+    ProductPlan best{kTiles256, 1, slabs, 0.0};
     uint64_t blocks = 0;
-    double least = 0.0;
-    tiles256((uint32_t)I, (uint32_t)J, slabs, &least, &blocks);
-    auto consider = [&](ProductKernel kernel, uint64_t shares, uint64_t per, uint64_t blocks, uint64_t fit, uint64_t few,
-                        double c_few, double c, double round) {
-        const double join = shares == 1 ? 0.0 : 3.7 + (double)(shares * I * J) * 8e-6 / 5.7;
-        const double rounds = blocks <= fit ? 1.0 : (double)blocks / (double)fit + 0.42;
-        const double cost = join + rounds * ((double)per * (blocks <= few ? c_few : c) + round);
-        if (cost < least) {
-            least = cost;
-            best = ProductPlan{kernel, (uint32_t)shares, per};
-        }
-    };
+    tiles256((uint32_t)I, (uint32_t)J, slabs, &best.cost, &blocks);
     for (uint64_t want = 1; want <= 16 && want <= slabs; want *= 2) {
         const uint64_t per = (slabs + want - 1) / want, shares = (slabs + per - 1) / per;
-        consider(kTiles64, shares, per, n64 * shares, 512, 256, 0.27, 0.53, 0.9);
-        consider(kTiles128, shares, per, n128 * shares, 512, 256, 0.66, 0.91, 3.5);
-        consider(kTiles128Deep, shares, per, n128 * shares, 256, 128, 0.42, 0.50, 3.2);
+        for (int k = kTiles64; k <= kTiles128Deep; ++k) {
+            const double cost = join_cost(shares, I, J) + even_cost(kCost[k], (k == kTiles64 ? n64 : n128) * shares, per);
+            if (cost < best.cost) best = ProductPlan{(ProductKernel)k, (uint32_t)shares, per, cost};
+        }
         if (n64 > 1024) break;                          // enough blocks without shares
     }
     return best;
 }
 
-uint64_t product_workspace(const Product& p) {
-    const ProductPlan c = product_plan(p.I, p.J, p.K);
-    uint64_t n = packed_bytes(p.p, p.I, p.K) + packed_bytes(p.q, p.J, p.K);
-    if (c.shares > 1) n += (c.shares * (uint64_t)p.J * part_ld(p.I) * 4 + 255) / 256 * 256;
-    return n;
+// Whether two products are worth one launch, and on which tiles; each keeps its shares, so neither's
+// results depend on the other.  A block of one lasts as long as its sums; together they fill rounds.
+bool pair_plan(uint64_t Ix, uint64_t Jx, const ProductPlan& x, uint64_t Iw, uint64_t Jw, const ProductPlan& w,
+               ProductKernel* kernel) {
+    double least = x.cost + w.cost + 2.0;               // a launch more
+    bool pair = false;
+    for (int k = kTiles64; k <= kTiles128Deep; ++k) {
+        const uint64_t unit = k == kTiles64 ? 64 : 128;
+        const uint64_t bx = tiles(Ix, Jx, unit) * x.shares, bw = tiles(Iw, Jw, unit) * w.shares, all = bx + bw;
+        const double cx = block_cost(kCost[k], all, x.slabs), cw = block_cost(kCost[k], all, w.slabs);
+        const double longest = std::max(cx, cw), work = ((double)bx * cx + (double)bw * cw) / (double)kCost[k].fit;
+        const double cost = join_cost(x.shares, Ix, Jx) + join_cost(w.shares, Iw, Jw) +
+                            (all <= kCost[k].fit ? longest : std::max(longest, work + 0.42 * longest));
+        if (all < 1ull << 22 && cost < least) {
+            least = cost;
+            *kernel = (ProductKernel)k;
+            pair = true;
+        }
+    }
+    return pair;
 }
 
-hipError_t launch_product(const Product& p, void* workspace, hipStream_t stream) {
-    const ProductPlan c = product_plan(p.I, p.J, p.K);
-    uint8_t* work = (uint8_t*)workspace;
-    Operand P = p.p, Q = p.q;
-    pack(P, p.I, Q, p.J, p.K, work, stream);
-    const bool beyond = (uint64_t)p.I * p.J * (p.out_dtype == NEOX_F32 ? 4 : 2) >= kBeyond;
-    const Result r{p.out, p.out_ld, p.I, p.J, p.out_dtype, beyond, p.epi};
-    TileArgs a{(const uint8_t*)P.at, (const uint8_t*)Q.at, (uint32_t)(P.ld * 2), (uint32_t)(Q.ld * 2), p.K, c.slabs,
-               c.shares, r};
-    if (c.shares > 1) {
-        a.r = Result{work, part_ld(p.I), p.I, p.J, NEOX_F32, false, Epilogue{}};
-    }
-    auto run = [&](auto ht) {
-        constexpr int HT = decltype(ht)::value;
-        constexpr bool BF = HT == NEOX_BF16;
-        if (p.q.strided) launch_tiles<HalfOperands<BF, true, true>, HT>(a, c, stream);
-        else if (p.p.strided) launch_tiles<HalfOperands<BF, true, false>, HT>(a, c, stream);
-        else launch_tiles<HalfOperands<BF, false, false>, HT>(a, c, stream);
-        if (c.shares > 1) {
-            // (few results: one grid)
-            const Spread sp = spread(p.J, (p.I + 7) / 8, 1);
-            join_kernel<HT><<<(uint32_t)sp.blocks, 256, 0, stream>>>((const float*)work, part_ld(p.I), c.shares, r, sp);
+namespace {
+
+// The products of one call, with their packed operands and shares in the workspace.
+struct Placed {
+    const Product* p = nullptr;
+    ProductPlan c{};
+    TileArgs a{};
+    Result r{};
+    const float* part = nullptr;
+};
+struct Work {
+    Pack packs[3] = {};
+    Placed at[2];
+    int n = 0, npacks = 0;
+    uint64_t bytes = 0;
+
+    Work(const Product* x, const Product* w, uint8_t* base) {
+        for (const Product* p : {x, w})
+            if (p) at[n++].p = p;
+        for (int i = 0; i < n; ++i) {
+            Placed& t = at[i];
+            const Product& p = *t.p;
+            t.c = product_plan(p.I, p.J, p.K);
+            const Operand P = operand(p.p, p.I, p.K, base), Q = operand(p.q, p.J, p.K, base);
+            t.r = Result{p.out, p.out_ld, p.I, p.J, p.out_dtype, (uint64_t)p.I * p.J * (p.out_dtype == NEOX_F32 ? 4 : 2) >= kBeyond,
+                         p.epi};
+            t.a = TileArgs{(const uint8_t*)P.at, (const uint8_t*)Q.at, (uint32_t)(P.ld * 2), (uint32_t)(Q.ld * 2), p.K, t.c.slabs,
+                           t.c.shares, t.r};
+            if (t.c.shares > 1) {
+                t.part = (const float*)(base + bytes);
+                t.a.r = Result{base + bytes, part_ld(p.I), p.I, p.J, NEOX_F32, false, Epilogue{}};
+                bytes += (t.c.shares * (uint64_t)p.J * part_ld(p.I) * 4 + 255) / 256 * 256;
+            }
         }
-    };
-    if (p.dtype == NEOX_F16) run(std::integral_constant<int, NEOX_F16>{});
-    else run(std::integral_constant<int, NEOX_BF16>{});
+    }
+    // The operand itself where tiles can be loaded from it, or its copy.  (d is an operand of both
+    // products, and is copied once: its rows are the same, whichever way it is read.)
+    Operand operand(Operand o, uint64_t side, uint64_t K, uint8_t* base) {
+        if (direct(o, side, K)) return o;
+        const uint64_t rows = o.strided ? K : side, cols = o.strided ? side : K, pitch = packed_pitch(o, side, K);
+        for (int i = 0; i < npacks; ++i)
+            if (packs[i].src == o.at && packs[i].ld == o.ld && packs[i].rows == rows && packs[i].cols == cols) {
+                o.at = packs[i].dst;
+                o.ld = pitch;
+                return o;
+            }
+        packs[npacks++] = Pack{o.at, (uint16_t*)(base + bytes), o.ld, rows, (uint32_t)cols, (uint32_t)pitch,
+                               (uint32_t)std::min<uint64_t>((rows * pitch / 8 + 255) / 256, 1u << 13)};
+        o.at = (const uint16_t*)(base + bytes);
+        o.ld = pitch;
+        bytes += (rows * pitch * 2 + 255) / 256 * 256;
+        return o;
+    }
+};
+
+template <int HT>
+hipError_t launch_work(const Work& w, const Backward* join, const void* sums, hipStream_t stream) {
+    constexpr bool BF = HT == NEOX_BF16;
+    const uint32_t blocks = w.packs[0].blocks + w.packs[1].blocks + w.packs[2].blocks;
+    if (blocks) pack_kernel<<<blocks, 256, 0, stream>>>(w.packs[0], w.packs[1], w.packs[2]);
+    ProductKernel kernel;
+    if (w.n == 2 && pair_plan(w.at[0].p->I, w.at[0].p->J, w.at[0].c, w.at[1].p->I, w.at[1].p->J, w.at[1].c, &kernel)) {
+        const TileArgs &x = w.at[0].a, &d = w.at[1].a;
+        const uint32_t parts = join ? backward_parts(join->rows, join->cols) : 0;
+        const uint32_t joins = parts ? (uint32_t)((join->cols + 63) / 64) : 0;
+        auto pair = [&](auto cx, auto cw) {
+            using X = typename decltype(cx)::type;
+            using W = typename decltype(cw)::type;
+            const EvenMap mx = even_map(x, X::BP), mw = even_map(d, X::BP);
+            linear_pair_kernel<X, W, HT><<<mx.blocks + mw.blocks + joins, X::NT, 0, stream>>>(
+                x, mx, d, mw, join ? *join : Backward{}, (const float*)sums, parts, joins);
+        };
+        using FX = HalfOperands<BF, true, false>;
+        using FW = HalfOperands<BF, true, true>;
+        if (kernel == kTiles64) pair(Type<Lin64<FX>>{}, Type<Lin64<FW>>{});
+        else if (kernel == kTiles128) pair(Type<Lin128<FX>>{}, Type<Lin128<FW>>{});
+        else pair(Type<Lin128d<FX>>{}, Type<Lin128d<FW>>{});
+    } else {
+        if (join) {
+            const hipError_t e = launch_join(*join, sums, stream);
+            if (e != hipSuccess) return e;
+        }
+        for (int i = 0; i < w.n; ++i) {
+            const Placed& t = w.at[i];
+            if (t.p->q.strided) launch_tiles<HalfOperands<BF, true, true>, HT>(t.a, t.c, stream);
+            else if (t.p->p.strided) launch_tiles<HalfOperands<BF, true, false>, HT>(t.a, t.c, stream);
+            else launch_tiles<HalfOperands<BF, false, false>, HT>(t.a, t.c, stream);
+        }
+    }
+    for (int i = 0; i < w.n; ++i) {
+        const Placed& t = w.at[i];
+        if (t.c.shares == 1) continue;
+        // (few results: one grid)
+        const Spread sp = spread(t.r.J, (t.r.I + 7) / 8, 1);
+        join_kernel<HT><<<(uint32_t)sp.blocks, 256, 0, stream>>>(t.part, part_ld(t.r.I), t.c.shares, t.r, sp);
+    }
     return hipGetLastError();
+}
+
+}  // namespace
+
+uint64_t products_workspace(const Product* x, const Product* w) { return Work(x, w, nullptr).bytes; }
+
+hipError_t launch_products(const Product* x, const Product* w, const Backward* join, const void* sums, void* workspace,
+                           hipStream_t stream) {
+    const Work work(x, w, (uint8_t*)workspace);
+    return (x ? x : w)->dtype == NEOX_F16 ? launch_work<NEOX_F16>(work, join, sums, stream)
+                                          : launch_work<NEOX_BF16>(work, join, sums, stream);
 }
 
 }  // namespace nz1

@@ -51,6 +51,7 @@ EXPORTS = ("neox_linear_workspace", "neox_linear", "neox_linear_backward_workspa
            "neox_dropout_backward_workspace", "neox_dropout_backward")
 
 _lib = None
+_byref = C.byref
 
 
 def lib():
@@ -79,7 +80,7 @@ def lib():
 
 def neox_linear_workspace(args: neox_linear_args) -> int:
     n = _U()
-    _check(lib().neox_linear_workspace(C.byref(args), C.byref(n)))
+    _check(lib().neox_linear_workspace(_byref(args), _byref(n)))
     return n.value
 
 
@@ -164,17 +165,16 @@ def _half(t, name) -> int:
 
 
 def _vector(t, name, n, dtype, device):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or \
-            (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must hold {n} adjacent elements of {dtype} on {device}")
     return t.data_ptr()
 
 
 def _matrix(t, name, m, n, dtype, device):
-    """(address, row stride) of an m x n matrix of that type and device."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != (m, n):
+    """(address, row stride) of an m x n matrix of that type and (CUDA) device."""
+    if t.dtype != dtype or t.device != device or t.shape != (m, n):
         raise ValueError(f"{name} must be {m} x {n} of {dtype} on {device}")
-    return t.data_ptr(), _rows_of(t, name)
+    return t.data_ptr(), n if t.is_contiguous() else _rows_of(t, name)
 
 
 def _drop_of(drop, device):
@@ -209,7 +209,7 @@ def _result(out, m, n, dtype, device):
     import torch
     if out is None:
         return torch.empty((m, n), dtype=dtype, device=device), n
-    if tuple(out.shape) != (m, n) or out.device != device or (dtype is not None and out.dtype != dtype):
+    if out.shape != (m, n) or out.device != device or (dtype is not None and out.dtype != dtype):
         raise ValueError("out must have the result's shape and device, and the type asked for")
     return out, _rows_of(out, "out")
 

@@ -298,7 +298,7 @@ def test_mask_follows_the_probability():
 # ----------------------------------------------------------------------------------------
 
 class _Plan(C.Structure):
-    _fields_ = [("kernel", C.c_int32), ("shares", C.c_uint32), ("slabs", C.c_uint64)]
+    _fields_ = [("kernel", C.c_int32), ("shares", C.c_uint32), ("slabs", C.c_uint64), ("cost", C.c_double)]
 
 
 def plan(I, J, K):
