@@ -21,36 +21,65 @@ struct DropoutArgs {
 constexpr uint32_t kDeep = 2;              // rows a thread has in flight
 constexpr uint64_t kStreaming = 1ull << 26; // bytes of a pass from which on its accesses are non-temporal
 
-template <int DT, bool NT>
-__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp) {
+// Rows of `units` threads in a row of all threads, for lengths that blocks of whole rows or stripes
+// would leave threads idle in: n / units as a multiplication (n < 2^31; none for a single unit).
+struct Flat {
+    uint32_t units, mul, shift;
+    uint64_t all;              // units in all
+};
+Flat flat(uint64_t rows, uint32_t units) {
+    Flat f{units, 0, 0, rows * units};
+    while ((1ull << f.shift) < units) ++f.shift;
+    // 2^(31 + shift) / units, rounded up: off by less than units / 2^(31 + shift) of itself, too
+    // little to show in a quotient of n < 2^31
+    if (units > 1) f.mul = (uint32_t)(((1ull << (31 + f.shift)) + units - 1) / units);
+    return f;
+}
+__device__ __forceinline__ uint32_t row_of(const Flat& f, uint32_t n) { return f.mul ? __umulhi(n, f.mul) >> (f.shift - 1) : n; }
+
+// Memory-bound.  MEASURED_FWD
+template <int DT, bool NT, bool FLAT>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp, Flat f) {
     const Unit u(sp, kDeep);
-    const uint32_t c = u.unit * 8;
-    if (c >= a.cols) return;
-    const uint32_t n = a.cols - c;
     const uint64_t off = drop_offset(a.drop);
-    float x[kDeep][8], r[kDeep][8], b[8] = {};
-    if (a.bias) load8<DT>(a.bias, c, n, b);
+    uint64_t row[kDeep];
+    uint32_t unit[kDeep];
+    bool in[kDeep];
+    float x[kDeep][8], r[kDeep][8], b[kDeep][8] = {};
 #pragma unroll
     for (uint32_t k = 0; k < kDeep; ++k) {
-        const uint64_t row = u.row + k * u.step;
-        if (row >= a.rows) break;
-        load8<DT, NT>(a.x, row * a.x_ld + c, n, x[k]);
-        if (a.residual) load8<DT, NT>(a.residual, row * a.r_ld + c, n, r[k]);
+        if constexpr (FLAT) {
+            const uint32_t n = (blockIdx.x * kDeep + k) * 256 + threadIdx.x, q = row_of(f, n);
+            row[k] = q;
+            unit[k] = n - q * f.units;
+            in[k] = n < f.all;
+        } else {
+            row[k] = u.row + k * u.step;
+            unit[k] = u.unit;
+            in[k] = row[k] < a.rows && u.unit * 8u < a.cols;
+        }
+        const uint32_t c = unit[k] * 8, left = a.cols - c;
+        if (!in[k]) break;
+        if (a.bias && (FLAT || k == 0)) load8<DT>(a.bias, c, left, b[k]);
+        load8<DT, NT>(a.x, row[k] * a.x_ld + c, left, x[k]);
+        if (a.residual) load8<DT, NT>(a.residual, row[k] * a.r_ld + c, left, r[k]);
     }
 #pragma unroll
     for (uint32_t k = 0; k < kDeep; ++k) {
-        const uint64_t row = u.row + k * u.step;
-        if (row >= a.rows) break;
+        if (!in[k]) break;
+        const uint32_t c = unit[k] * 8, left = a.cols - c;
+        if (a.bias) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] += b[e];
-        if (a.drop.limit) drop8(a.drop, off, (uint32_t)(a.row0 + row), u.unit, x[k]);
+            for (int e = 0; e < 8; ++e) x[k][e] += b[FLAT ? k : 0][e];
+        }
+        if (a.drop.limit) drop8(a.drop, off, (uint32_t)(a.row0 + row[k]), unit[k], x[k]);
         if (a.residual) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] += r[k][e];
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[k][e] = opaque(x[k][e]);
-        store8<DT, NT>(a.y, row * a.y_ld + c, n, x[k]);
+        store8<DT, NT>(a.y, row[k] * a.y_ld + c, left, x[k]);
     }
 }
 
@@ -165,16 +194,27 @@ hipError_t launch_dropout(const void* x, uint64_t x_ld, const void* bias, const 
                           hipStream_t stream) {
     const uint64_t size = dtype == NEOX_F32 ? 4 : 2;
     const bool nt = rows * cols * size * (residual ? 3 : 2) >= kStreaming;
-    rows_in_grids(rows, (cols + 7) / 8, kDeep, [&](uint64_t r, uint64_t n, const Spread& sp) {
-        const DropoutArgs a{(const uint8_t*)x + r * x_ld * size, bias,
-                            residual ? (const uint8_t*)residual + r * residual_ld * size : nullptr,
-                            (uint8_t*)y + r * y_ld * size, x_ld, residual_ld, y_ld, n, r, (uint32_t)cols, drop};
+    const uint64_t units = (cols + 7) / 8;
+    const Spread one = spread_close(1, units, kDeep);
+    const bool even = units % (1ull << one.shift) == 0;
+    // rows of a launch: of whole rows or stripes as many as a grid takes, in a row 2^31 units
+    const uint64_t most = even ? kGrid / one.across * ((256u >> one.shift) * kDeep) : std::max<uint64_t>(1, ((1ull << 31) - 1024) / units);
+    for (uint64_t row = 0; row < rows; row += most) {
+        const uint64_t n = std::min(most, rows - row);
+        const DropoutArgs a{(const uint8_t*)x + row * x_ld * size, bias,
+                            residual ? (const uint8_t*)residual + row * residual_ld * size : nullptr,
+                            (uint8_t*)y + row * y_ld * size, x_ld, residual_ld, y_ld, n, row, (uint32_t)cols, drop};
+        const Spread sp = spread_close(n, units, kDeep);
+        const Flat f = flat(n, (uint32_t)units);
+        const uint32_t blocks = even ? (uint32_t)sp.blocks : (uint32_t)((f.all + 256 * kDeep - 1) / (256 * kDeep));
         with_dtype(dtype, [&](auto dt) {
             constexpr int DT = decltype(dt)::value;
-            if (nt) dropout_kernel<DT, true><<<(uint32_t)sp.blocks, 256, 0, stream>>>(a, sp);
-            else dropout_kernel<DT, false><<<(uint32_t)sp.blocks, 256, 0, stream>>>(a, sp);
+            if (even && nt) dropout_kernel<DT, true, false><<<blocks, 256, 0, stream>>>(a, sp, f);
+            else if (even) dropout_kernel<DT, false, false><<<blocks, 256, 0, stream>>>(a, sp, f);
+            else if (nt) dropout_kernel<DT, true, true><<<blocks, 256, 0, stream>>>(a, sp, f);
+            else dropout_kernel<DT, false, true><<<blocks, 256, 0, stream>>>(a, sp, f);
         });
-    }, spread_close);
+    }
     return hipGetLastError();
 }
 

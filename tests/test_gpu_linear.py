@@ -481,6 +481,73 @@ def test_another_stream():
     assert same_bits(got, want)
 
 
+@HALVES
+def test_two_streams_at_once(half):
+    """Calls that overlap take workspaces of their own."""
+    cases = []
+    for i, (m, n, k) in enumerate([(387, 1001, 999), (128, 128, 16384)]):
+        dy, x, w, pre = rand((m, n), 10 + i, half), rand((m, k), 20 + i, half), rand((n, k), 30 + i, half), rand((m, n), 40 + i, half)
+        drop = L.Dropout(0.1, i)
+
+        def run(dy=dy, x=x, w=w, pre=pre, drop=drop):
+            return [L.linear(x, w, act="gelu", dropout=drop, residual=dy)[0],
+                    *L.linear_backward(dy, x, w, pre, "gelu", drop, dbias=True)]
+        cases.append((run, run(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (run, _, stream) in enumerate(cases):
+            with torch.cuda.stream(stream):
+                got[i].append(run())
+    torch.cuda.synchronize()
+    for i, (_, want, _) in enumerate(cases):
+        assert all(same_bits(a, b) for g in got[i] for a, b in zip(g, want))
+
+
+def test_offsets_beyond_32_bits():
+    """Results, gradients and masks of more than 2^32 elements: their last rows as well as their
+    first; and sums over a million tokens."""
+    m, n, k = (1 << 20) + 3, 4100, 24
+    x, w = ints((m, k), 1, BF16, 1), ints((n, k), 2, BF16, 1)
+    res = torch.ones(m, n, dtype=BF16, device=DEV)
+    drop = L.Dropout(0.5, 5, 6)
+    y, pre = L.linear(x, w, dropout=drop, residual=res, out=res, pre=True)
+    for first in (0, (1 << 31) // n - 1, (1 << 32) // n - 1, m - 2):
+        v = x[first:first + 2].double().cpu() @ w.double().cpu().t() + 0.0
+        keep = R.draws(5, 6, 2, n, first) >= 32768
+        assert same_bits(pre[first:first + 2].cpu(), v.to(BF16))
+        assert same_bits(y[first:first + 2].cpu(), (torch.where(keep, v * 2, 0.0) + 1).to(BF16))
+    dy = pre                                            # whole numbers of up to 24, few of them large
+    dx, dw, db = L.linear_backward(dy, x, w, dbias=True)
+    want = torch.zeros(n, k, dtype=torch.float64, device=DEV)
+    bias = torch.zeros(n, dtype=torch.float64, device=DEV)
+    for a in range(0, m, 1 << 16):
+        d = dy[a:a + (1 << 16)].double()
+        want += d.t().contiguous() @ x[a:a + (1 << 16)].double()
+        bias += d.sum(0)
+        if a == 0 or a + (1 << 16) >= m:
+            assert same_bits(dx[a:a + (1 << 16)], (d @ w.double() + 0.0).to(BF16))
+    assert float(want.abs().max()) < 2 ** 24            # so FP32's sums are exact
+    assert same_bits(dw, want.to(BF16)) and same_bits(db, bias.to(BF16))
+    del dy, pre, y, res
+    x = torch.ones(70001, 70001, dtype=F16, device=DEV)
+    y = L.dropout(x, drop, out=x)
+    for first in (0, 30677, 30678, 61356, 70000):
+        keep = R.draws(5, 6, 1, 70001, first) >= 32768
+        assert bool(((y[first:first + 1] != 0).cpu() == keep).all())
+    dx, db = L.dropout_backward(y, L.Dropout(0.0, 0), dx=False, dbias=True)
+    kept = (y != 0).sum(0)
+    assert same_bits(db, (2.0 * kept).to(F16))
+
+
+def test_long_sums():
+    """A million elements of K: exact, whole numbers of -1 to 1."""
+    k = (1 << 20) + 8
+    x, w = ints((5, k), 1, BF16, 1), ints((70, k), 2, BF16, 1)
+    y, _ = L.linear(x, w, dtype=F32)
+    assert same_bits(y, (x.double() @ w.double().t() + 0.0).float())
+
+
 def test_captured_and_replayed():
     """A layer and its gradients in one graph: replays draw new masks from a counter that the graph
     itself moves on, and give the eager calls' bits, whatever else ran between."""
