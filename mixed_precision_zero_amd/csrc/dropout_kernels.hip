@@ -37,7 +37,10 @@ Flat flat(uint64_t rows, uint32_t units) {
 }
 __device__ __forceinline__ uint32_t row_of(const Flat& f, uint32_t n) { return f.mul ? __umulhi(n, f.mul) >> (f.shift - 1) : n; }
 
-// Memory-bound.  MEASURED_FWD
+// Memory-bound: BF16 16384 x 6144 with bias and residual 92 us, 6.5 TB/s; the random bits hide behind
+// the memory (90 us without).  Two rows a thread, non-temporal both ways, measured (us): one row 103,
+// four 105; ordinary loads 103, ordinary stores as well 111.  Below kStreaming bytes, where the caches
+// keep what is read, ordinary accesses are as fast (2048 x 1024 4.9) and leave the result there.
 template <int DT, bool NT, bool FLAT>
 __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp, Flat f) {
     const Unit u(sp, kDeep);
@@ -87,6 +90,11 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp, 
 // of them), so that the blocks under way sweep over neighbouring rows together, and adds up what
 // it makes of them column by column: eight sums a thread, joined in order over the threads of one
 // column, then over the blocks by join_kernel.  The sums' order goes by the sizes alone.
+//
+// Memory-bound without an act: BF16 16384 x 6144 77 us with the join, 5.3 TB/s (64 without sums, by
+// dropout_kernel).  Blocks that take runs of rows instead 97 (their rows lie far apart), 512 of them
+// 119, 1024 80, two rows in flight 81.  With an act and dropout bound by their arithmetic, some 60
+// instructions an element: 8192 x 24576 GELU 205 us to read 805 MB, 160 without dropout.
 struct BackArgs {
     Backward b;
     float* part;               // [count][cols], or null: no sums, or one block that writes dbias

@@ -20,6 +20,8 @@ namespace nz1 {
 struct Bits {
     uint32_t w[4];
 };
+// one instruction (0x96: the truth table of a ^ b ^ c)
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
 __device__ __forceinline__ Bits philox(const uint32_t (&seed)[2], uint64_t offset, uint32_t row, uint32_t unit) {
     uint32_t a = unit, b = row, c = (uint32_t)offset, d = (uint32_t)(offset >> 32);
     uint32_t k0 = seed[0], k1 = seed[1];
@@ -28,9 +30,9 @@ __device__ __forceinline__ Bits philox(const uint32_t (&seed)[2], uint64_t offse
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
         const uint64_t x = (uint64_t)0xD2511F53u * a, y = (uint64_t)0xCD9E8D57u * c;
-        a = (uint32_t)(y >> 32) ^ b ^ k0;
+        a = xor3((uint32_t)(y >> 32), b, k0);
         b = (uint32_t)y;
-        c = (uint32_t)(x >> 32) ^ d ^ k1;
+        c = xor3((uint32_t)(x >> 32), d, k1);
         d = (uint32_t)x;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;

@@ -54,6 +54,9 @@ struct ProductPlan {
     double cost;               // us
 };
 ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K);
+// Whether two products are worth one launch, and on which tiles.
+bool pair_plan(uint64_t Ix, uint64_t Jx, const ProductPlan& x, uint64_t Iw, uint64_t Jw, const ProductPlan& w,
+               ProductKernel* kernel);
 // d = D(dy) act'(pre), and the sums of its columns.
 struct Backward {
     const void* dy;

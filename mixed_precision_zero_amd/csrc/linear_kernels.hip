@@ -1,4 +1,13 @@
-// linear_kernels.hip -- products of half-precision matrices with an epilogue on gfx950.
+// linear_kernels.hip -- products of half-precision matrices with an epilogue on gfx950: a layer's
+// forward product (rows of K by rows of K), dx (W's rows are K) and dw (both operands' are).
+//
+// Large ones are bound by the matrix units and LDS together, as all of tile_core.h's: 8192 x 24576 x
+// 6144 forward 1850 to 1900 us without an epilogue (1.30 to 1.34 PFLOP/s, matrix units busy 66% of the
+// time), dx 1805 to 1850 (71%), dw 1790 to 1830 (73%); a library product of these 1690, 1810 and 2070.
+// The forward product is slower than the other two where a row of K is a multiple of 4 KB: its loads
+// take 128 bytes of each of 512 rows, which then lie in the same channels of the L2; rows of K + 64
+// elements take 1780 us.  Few results over long sums are split into shares of K (see product_plan).
+// Few tokens are bound by reading W: one by 24576 x 6144 (302 MB) 52 us, 5.8 TB/s.
 #include "column_sums.h"
 #include "epilogue.h"
 #include "spread.h"
@@ -46,6 +55,10 @@ __device__ __forceinline__ void linear_tile(const TileArgs& a, const TileAt& at,
     emit_tile<HT, LAYER>(r, t, at.i, at.j, lds);
 }
 
+// Measured and not taken: 64 x 64 tiles by 16 waves, four groups of four on a quarter of K each, sums
+// joined in LDS (333 x 1024 x 4096 17.8 us against 12.7 with two shares); 64 x 64 tiles with 6 or 8
+// slabs in LDS (equal with one block a CU, slower with two); 128 x 128 with 5 (equal); 128 x 64 tiles;
+// slabs begun at another K on each XCD (1 to 2% slower).
 template <class Form>
 using Lin256 = TileCore<256, 256, 2, 4, false, 2, Form>;
 template <class Form>
@@ -54,6 +67,8 @@ template <class Form>
 using Lin64 = TileCore<64, 64, 2, 2, false, 4, Form>;
 template <class Form>
 using Lin128d = TileCore<128, 128, 2, 4, false, 4, Form>;
+
+// Whole tiles of 256 x 256, the rest in quarters (see TileMap).
 template <class Form, int HT>
 __global__ __launch_bounds__(512, 2) void linear_mixed_kernel(TileArgs a, TileMap m) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Lin256<Form>::kLds];
@@ -63,7 +78,7 @@ __global__ __launch_bounds__(512, 2) void linear_mixed_kernel(TileArgs a, TileMa
 }
 // Even tiles: `down` x `across` of them, for each share of K.  Consecutive blocks go to the eight
 // XCDs in turn; each XCD, and so each L2, is given one run of neighbouring tiles, eight rows of
-// them column by column.
+// them column by column (dw of 8000 x 704 x 6000 on 64 x 64 tiles 290 us in plain order, 167 so).
 struct EvenMap {
     uint32_t across, down, per, blocks;     // per: tiles of a share
 };
@@ -260,8 +275,9 @@ ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K) {
     return best;
 }
 
-// Whether two products are worth one launch, and on which tiles; each keeps its shares, so neither's
-// results depend on the other.  A block of one lasts as long as its sums; together they fill rounds.
+// Each keeps its shares, so neither's results depend on the other.  A block of one lasts as long as its
+// sums; together they fill rounds.  2048 x 4096 x 1024 43 us against 28.5 + 21.5, 1000 x 1000 x 1000 12.7
+// against 7.7 + 8.
 bool pair_plan(uint64_t Ix, uint64_t Jx, const ProductPlan& x, uint64_t Iw, uint64_t Jw, const ProductPlan& w,
                ProductKernel* kernel) {
     double least = x.cost + w.cost + 2.0;               // a launch more

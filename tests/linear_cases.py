@@ -12,3 +12,12 @@ PRODUCTS = [
     (TILES128_DEEP, True, 100, 1200, 8000), (TILES128_DEEP, True, 1500, 333, 4000),
     (TILES256, False, 8000, 333, 40), (TILES256, False, 4200, 4300, 200), (TILES256, False, 4096, 4096, 1000),
 ]
+
+# Gradients of both operands by what takes them, (kernel, m, n, k): None for two launches, else the
+# tiles of the one.
+PAIRS = [
+    (None, 1, 2048, 4096), (None, 333, 4096, 999), (None, 4096, 3001, 4096),
+    (TILES64, 387, 1001, 999), (TILES64, 100, 512, 1024),
+    (TILES128, 700, 1001, 4096), (TILES128, 2048, 4096, 1024),
+    (TILES128_DEEP, 387, 1001, 4096), (TILES128_DEEP, 3000, 100, 999),
+]

@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 import linear_reference as R  # noqa: E402
 import mixed_precision_zero_amd as Z  # noqa: E402
 from mixed_precision_zero_amd import linear as L  # noqa: E402
-from linear_cases import PRODUCTS  # noqa: E402
+from linear_cases import PAIRS, PRODUCTS  # noqa: E402
 from mixed_precision_zero_amd import matrix as M  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -101,6 +101,28 @@ def test_every_product_kernel(kernel, shared, I, J, K, half):
     dw = res.clone()
     L.linear_backward(a.t().contiguous(), b.t().contiguous(), None, dx=False, dw=dw, accumulate=True)
     assert same_bits(dw, (want + res.double()).to(half))
+
+
+@HALVES
+@pytest.mark.parametrize("kernel,m,n,k", PAIRS)
+def test_gradients_in_one_launch_and_in_two(kernel, m, n, k, half):
+    """The three gradients together have the bits of each by itself, and the exact values."""
+    dy, x, w = ints((m, n), 1, half, 2), ints((m, k), 2, half, 2), ints((n, k), 3, half, 2)
+    db = ints((n,), 4, half, 9)
+    d, want_b = dy.double(), db.double() + dy.double().sum(0)
+    dx, dw, _ = L.linear_backward(dy, x, w)
+    assert same_bits(dx, (d @ w.double() + 0.0).to(half))
+    assert same_bits(dw, (d.t().contiguous() @ x.double() + 0.0).to(half))
+    more, again = dw.clone(), db.clone()
+    dx2, _, _ = L.linear_backward(dy, x, w, dw=more, dbias=again, accumulate=True)
+    assert same_bits(dx2, dx) and same_bits(again, want_b.to(half))
+    assert same_bits(more, (dw.double() + d.t().contiguous() @ x.double()).to(half))
+    pre = rand((m, n), 5, half)
+    drop = L.Dropout(0.2, 1)
+    a = L.linear_backward(dy, x, w, pre, "gelu", drop, dbias=True)
+    assert same_bits(a[0], L.linear_backward(dy, None, w, pre, "gelu", drop, dw=False)[0])
+    assert same_bits(a[1], L.linear_backward(dy, x, None, pre, "gelu", drop, dx=False)[1])
+    assert same_bits(a[2], L.linear_backward(dy, None, None, pre, "gelu", drop, dx=False, dw=False, dbias=True)[2])
 
 
 @HALVES

@@ -15,7 +15,7 @@ import linear_reference as R
 import mixed_precision_zero_amd as Z
 from mixed_precision_zero_amd import build
 from mixed_precision_zero_amd import linear as L
-from linear_cases import PRODUCTS
+from linear_cases import PAIRS, PRODUCTS
 from test_kernel_asm_cpu import PACKED_FP32, SCALAR_OK, _device_asm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -326,6 +326,22 @@ def test_every_product_kernel_has_its_shapes():
                     unit, threads = {0: (64, 256), 1: (128, 512), 2: (128, 512), 3: (128, 512)}[p.kernel]
                     assert -(-I // unit) * -(-J // unit) * p.shares * threads < 1 << 32
     assert swept == set(got) and all(got.count(k) > 1 for k in swept)
+
+
+def pair(m, n, k):
+    """Whether and how the host runs both gradients in one launch."""
+    f = L.lib()["_ZN3nz19pair_planEmmRKNS_11ProductPlanEmmS2_PNS_13ProductKernelE"]
+    U, P = C.c_uint64, C.POINTER(_Plan)
+    f.argtypes, f.restype = [U, U, P, U, U, P, C.POINTER(C.c_int32)], C.c_bool
+    x, w, kernel = plan(k, m, n), plan(k, n, m), C.c_int32()
+    return kernel.value if f(k, m, C.byref(x), k, n, C.byref(w), C.byref(kernel)) else None
+
+
+def test_every_pair_has_its_shapes():
+    assert [pair(*s) for _, *s in PAIRS] == [kernel for kernel, *_ in PAIRS]
+    swept = {pair(m, n, k) for m in (1, 64, 333, 1000, 2048, 5000) for n in (8, 512, 1001, 4096, 24576)
+             for k in (8, 999, 1024, 6144)}
+    assert swept == {kernel for kernel, *_ in PAIRS}
 
 
 def test_workspaces_go_by_sizes_and_alignment():
