@@ -210,14 +210,25 @@ EvenMap even_map(const TileArgs& a, uint32_t unit) {
     m.blocks = m.per * a.shares;
     return m;
 }
-template <class Form, int HT>
+// From this many bytes on, an operand that one row of tiles reads is not kept in the caches: no other
+// block asks for it, and a model's weights do not fit them.  One token by 24576 x 6144 56 -> 51 us, by
+// 4096 x 4096 11.7 -> 10.5, by 4096 x 1024 (8 MB, kept by the caches from call to call) 6.0 -> 6.7.
+constexpr uint64_t kOnce = 1ull << 25;
+
+template <bool BF, bool PS, bool QS, int HT>
 void launch_tiles(const TileArgs& a, const ProductPlan& c, hipStream_t stream) {
+    using Form = HalfOperands<BF, PS, QS>;
     const uint32_t I = a.r.I, J = a.r.J;
     auto even = [&](auto core) {
         using Core = typename decltype(core)::type;
         const EvenMap m = even_map(a, Core::BP);
         linear_even_kernel<Core, HT><<<m.blocks, Core::NT, 0, stream>>>(a, m);
     };
+    if constexpr (!QS) {
+        using Once = HalfOperands<BF, PS, QS, true>;
+        if (J <= 64 && I * a.K * 2 >= kOnce && c.kernel == kTiles64) return even(Type<Lin64<Once>>{});
+        if (J <= 64 && I * a.K * 2 >= kOnce && c.kernel == kTiles128Deep) return even(Type<Lin128d<Once>>{});
+    }
     switch (c.kernel) {
     case kTiles64: even(Type<Lin64<Form>>{}); break;
     case kTiles128: even(Type<Lin128<Form>>{}); break;
@@ -258,7 +269,9 @@ double join_cost(uint64_t shares, uint64_t I, uint64_t J) {
 //     .. deep       0.42 (128),        0.50    3.2
 //     256 x 256     1.5, its quarters 0.75     7.3, 1.8
 // and for shares (few results, long sums) a launch and the sums' way through memory, the caches
-// mostly.  Blocks beyond a round start as others end: a part of a round more.
+// mostly.  Blocks beyond a round start as others end: a part of a round more.  No launch takes less
+// than its operands at 6.8 TB/s (products of 1 to 128 tokens with weights from memory, 30 of them: 3.3%
+// longer than the fastest on average).
 ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K) {
     const uint64_t slabs = std::max<uint64_t>(1, (K + 63) / 64), n64 = tiles(I, J, 64), n128 = tiles(I, J, 128);
     ProductPlan best{kTiles256, 1, slabs, 0.0};
@@ -267,7 +280,8 @@ ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K) {
     for (uint64_t want = 1; want <= 16 && want <= slabs; want *= 2) {
         const uint64_t per = (slabs + want - 1) / want, shares = (slabs + per - 1) / per;
         for (int k = kTiles64; k <= kTiles128Deep; ++k) {
-            const double cost = join_cost(shares, I, J) + even_cost(kCost[k], (k == kTiles64 ? n64 : n128) * shares, per);
+            const double work = even_cost(kCost[k], (k == kTiles64 ? n64 : n128) * shares, per);
+            const double cost = join_cost(shares, I, J) + std::max(work, 1.9 + (double)((I + J) * K) * 2e-6 / 6.8);
             if (cost < best.cost) best = ProductPlan{(ProductKernel)k, (uint32_t)shares, per, cost};
         }
         if (n64 > 1024) break;                          // enough blocks without shares
@@ -382,9 +396,9 @@ hipError_t launch_work(const Work& w, const Backward* join, const void* sums, hi
         }
         for (int i = 0; i < w.n; ++i) {
             const Placed& t = w.at[i];
-            if (t.p->q.strided) launch_tiles<HalfOperands<BF, true, true>, HT>(t.a, t.c, stream);
-            else if (t.p->p.strided) launch_tiles<HalfOperands<BF, true, false>, HT>(t.a, t.c, stream);
-            else launch_tiles<HalfOperands<BF, false, false>, HT>(t.a, t.c, stream);
+            if (t.p->q.strided) launch_tiles<BF, true, true, HT>(t.a, t.c, stream);
+            else if (t.p->p.strided) launch_tiles<BF, true, false, HT>(t.a, t.c, stream);
+            else launch_tiles<BF, false, false, HT>(t.a, t.c, stream);
         }
     }
     for (int i = 0; i < w.n; ++i) {

@@ -45,16 +45,17 @@ struct TileRows {
 };
 // What a core's operands are: rows of K whose slabs are whole (but for MXFP4's last half slab)...
 struct WholeRows {
-    static constexpr bool kBf16 = false, kStridedP = false, kStridedQ = false, kAnyK = false;
+    static constexpr bool kBf16 = false, kStridedP = false, kStridedQ = false, kAnyK = false, kOnce = false;
 };
 // ... or 16-bit elements, FP16 or BF16, over any multiple of eight of K, each operand as rows of K
 // or strided: spitch (at most K, the rest reads as zeros) rows of `rows` consecutive elements,
 // pitch bytes apart.  A strided operand's slab lies in LDS as it does in memory, 64 rows of K;
 // fragments are read with the transposing LDS load (ds_read_b64_tr_b16: of 16 lanes' 8 bytes, as
 // 4 rows of 16 elements, lane l gets column l), two of them for eight elements of K.
-template <bool BF16, bool PS, bool QS>
+// ONCE: P is read by this launch only once and not kept, so its loads are non-temporal.
+template <bool BF16, bool PS, bool QS, bool ONCE = false>
 struct HalfOperands {
-    static constexpr bool kBf16 = BF16, kStridedP = PS, kStridedQ = QS, kAnyK = true;
+    static constexpr bool kBf16 = BF16, kStridedP = PS, kStridedQ = QS, kAnyK = true, kOnce = ONCE;
 };
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
@@ -102,6 +103,7 @@ struct TileCore {
     static_assert(LP >= 1 && LQ >= 1 && BP * 8 % NT == 0 && BQ * 8 % NT == 0, "whole loads");
     static_assert(NS >= 2 && (!FP4 || NS == 2), "");
     static_assert(kLds <= 160 * 1024, "LDS of a CU");
+    static constexpr int kHint = Form::kOnce ? 2 : 0;               // cache policy of P's loads: nt
 
     // acc[i][j]: 16x16 tile (i, j) of this wave; element e of a lane is D row
     // 16 i + 4 (lane / 16) + e, column 16 j + lane % 16 of the wave's part.
@@ -197,7 +199,7 @@ struct TileCore {
             if (n < LP)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(pb, (lptr)(buf + wave * 1024 + n * NT * 16), 16,
                                                          kPS || live ? pv : kNowhere, (kPS ? 0u : s * kSlab) + n * pstep,
-                                                         0, 0);
+                                                         0, kHint);
             else
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     qb, (lptr)(buf + BP * kSlab + wave * 1024 + (n - LP) * NT * 16), 16, kQS || live ? qv : kNowhere,
