@@ -104,6 +104,18 @@ def test_every_product_kernel(kernel, shared, I, J, K, half):
 
 
 @HALVES
+@pytest.mark.parametrize("m,n,k", [(1, 24576, 1000), (3, 50000, 400), (16, 24576, 6144), (16, 6144, 24576), (64, 6144, 8200),
+                                   (33, 4099, 4105)])
+def test_weights_read_once(m, n, k, half):
+    """Few tokens by weights that are not kept in the caches, forward and back."""
+    x, w, dy = ints((m, k), 1, half, 1), ints((n, k), 2, half, 1), ints((m, n), 3, half, 1)
+    y, _ = L.linear(x, w)
+    assert same_bits(y, (x.double() @ w.double().t() + 0.0).to(half))
+    dx, _, _ = L.linear_backward(dy, None, w, dw=False)
+    assert same_bits(dx, (dy.double() @ w.double() + 0.0).to(half))
+
+
+@HALVES
 @pytest.mark.parametrize("kernel,m,n,k", PAIRS)
 def test_gradients_in_one_launch_and_in_two(kernel, m, n, k, half):
     """The three gradients together have the bits of each by itself, and the exact values."""
