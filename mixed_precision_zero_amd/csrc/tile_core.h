@@ -1,5 +1,6 @@
-// tile_core.h -- the block-tile product both matrix operators use: D = P Q^T for two
-// operands stored as rows of consecutive K bytes, on gfx950's matrix cores.
+// tile_core.h -- the block-tile product that the matrix operators and the linear layer use: D = P Q^T
+// on gfx950's matrix cores, for two operands stored as rows of consecutive K bytes; the linear layer's
+// also with K going from row to row.
 //
 // FP16 (v_mfma_f32_16x16x32_f16) and MXFP4 (v_mfma_scale_f32_16x16x128_f8f6f4) take the
 // same bytes per lane: 16 bytes of row (lane % 16), lane group (lane / 16) of four covering

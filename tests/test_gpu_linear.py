@@ -574,6 +574,36 @@ def test_offsets_beyond_32_bits():
     assert same_bits(db, (2.0 * kept).to(F16))
 
 
+@pytest.mark.parametrize("m,n,k", [(1 << 24, 8, 8), (1, 1 << 22, 16), (3, 16, 1 << 22)])
+def test_longest_sides(m, n, k):
+    """Each side at its limit: first, last and middle rows."""
+    x, w, dy = ints((m, k), 1, BF16, 1), ints((n, k), 2, BF16, 1), ints((m, n), 3, BF16, 1)
+    y, _ = L.linear(x, w, dtype=F32)
+    dx, _, db = L.linear_backward(dy, None, w, dw=False, dbias=True)
+    for rows in (slice(0, 2), slice(m // 2, m // 2 + 2), slice(max(0, m - 2), m)):
+        assert same_bits(y[rows], (x[rows].double() @ w.double().t() + 0.0).float())
+        assert same_bits(dx[rows], (dy[rows].double() @ w.double() + 0.0).to(BF16))
+    assert same_bits(db, (dy.sum(0, dtype=torch.float64) + 0.0).to(BF16))
+    if m > 1:
+        _, dw, _ = L.linear_backward(dy, x, None, dx=False)
+        want = torch.zeros(n, k, dtype=torch.float64, device=DEV)
+        for a in range(0, m, 1 << 20):
+            want += dy[a:a + (1 << 20)].double().t().contiguous() @ x[a:a + (1 << 20)].double()
+        assert same_bits(dw, (want + 0.0).to(BF16))
+
+
+def test_rows_of_any_length():
+    """Dropout of rows that are taken as stripes and of rows that are taken in a row of all threads."""
+    for n in list(range(1, 40)) + [63, 64, 65, 127, 130, 255, 256, 257, 1000, 1040, 2047, 2050, 4096, 6150]:
+        m = max(3, 20000 // n)
+        x, b, r = rand((m, n), n, F16), rand((n,), 2, F16), rand((m, n), 3, F16)
+        want = R.dropped(x.double().cpu() + b.double().cpu(), (0.3, n, 7))
+        y = L.dropout(x, L.Dropout(0.3, n, 7), b, r)
+        err = want.abs() * 2 * R.U
+        want = want + r.double().cpu()
+        R.close(y, want, err + want.abs() * R.U, f"{m} x {n}")
+
+
 def test_long_sums():
     """A million elements of K: exact, whole numbers of -1 to 1."""
     k = (1 << 20) + 8
