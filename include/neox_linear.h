@@ -100,9 +100,9 @@ typedef struct neox_linear_args {
 int neox_linear_workspace(const neox_linear_args* a, uint64_t* bytes);
 
 /* Errors: NEOX_EINVAL (null, misaligned, a size outside the limits, an ld smaller than the
- * columns or above 2^40, unknown type or act, y_dtype neither half nor NEOX_F32, reserved not
- * 0, p outside [0, 1], arrays meeting, workspace too small or not 256-byte aligned),
- * NEOX_EHIP. */
+ * columns or above 2^40 or (rows - 1) ld above 2^60, unknown type or act, y_dtype neither half
+ * nor NEOX_F32, reserved not 0, p outside [0, 1], arrays meeting, workspace too small or not
+ * 256-byte aligned), NEOX_EHIP. */
 int neox_linear(const neox_linear_args* a, void* workspace, uint64_t workspace_bytes, void* hip_stream);
 
 /* The gradients of the same, from dy (m x n): with d = D(dy) act'(pre), rounded to half where
@@ -147,8 +147,8 @@ int neox_mxfp4_linear(const void* a_codes, const void* a_scales, uint64_t m, con
  * bias and residual may be NULL, and y may be x or residual.  drop may be NULL: no dropout.
  * rows 0 to 2^31 - 1, cols 1 to 2^31 - 1.
  * Errors: NEOX_EINVAL (null, misaligned to its element, a size outside the limits, an ld
- * smaller than cols or above 2^40, unknown type, p outside [0, 1], y meeting an input
- * otherwise), NEOX_EHIP. */
+ * smaller than cols or above 2^40 or (rows - 1) ld above 2^60, unknown type, p outside [0, 1],
+ * y meeting an input otherwise), NEOX_EHIP. */
 int neox_dropout(const void* x, uint64_t x_ld, const void* bias, const void* residual, uint64_t residual_ld,
                  void* y, uint64_t y_ld, uint64_t rows, uint64_t cols, int32_t dtype, const neox_drop* drop,
                  void* hip_stream);

@@ -59,7 +59,7 @@ struct Arrays {
                            (unsigned long long)cols);
         } else if (rows > 1 && ld > kMaxLd) {
             rc = set_error(NEOX_EINVAL, "%s: ld %llu above 2^40", name, (unsigned long long)ld);
-        } else if (rows > 1 && (rows - 1) * ld > (1ull << 60)) {
+        } else if (rows > 1 && ld > (1ull << 60) / (rows - 1)) {
             rc = set_error(NEOX_EINVAL, "%s: ld %llu too large for %llu rows", name, (unsigned long long)ld,
                            (unsigned long long)rows);
         }

@@ -191,6 +191,18 @@ def test_dropout_backward_refuses(text, kw):
     refuses(text, drop_back, **kw)
 
 
+@pytest.mark.parametrize("rows,ld", [((1 << 20) + 2, 1 << 40), ((1 << 24) + 1, 1 << 40), ((1 << 25) + 1, 1 << 40),
+                                     ((1 << 30) + 1, 1 << 34), ((1 << 31) - 1, 1 << 40)])
+def test_spans_beyond_the_address_space_are_refused(rows, ld):
+    """Also where rows times ld passes 64 bits."""
+    for name in ("x", "residual", "y"):
+        refuses(f"{name}: ld" if name != "residual" else "the residual: ld", drop, rows=rows, **{f"{name}_ld": ld})
+    for name in ("dy", "dx"):
+        refuses(f"{name}: ld", drop_back, rows=rows, **{f"{name}_ld": ld})
+    if rows < 1 << 29:                      # (more have too many tiles)
+        refuses("c: ld", mx, m=rows, ldc=ld)
+
+
 def test_nothing_to_do_is_no_error():
     """No rows: nothing is read, written or launched."""
     L.neox_dropout(None, 0, None, None, 0, None, 0, 0, 40, Z.NEOX_F16, None)
