@@ -77,8 +77,8 @@ uint64_t backward_workspace(uint64_t rows, uint64_t cols);
 hipError_t launch_backward(const Backward& b, void* workspace, bool join_here, hipStream_t stream);
 hipError_t launch_join(const Backward& b, const void* workspace, hipStream_t stream);
 
-// One product, or two (dx and dw) that may run side by side; either may be null.  join: null, or
-// sums of a launch_backward, in `sums`, that are joined too.
+// One product, or two (dx and dw, whose q is one matrix, read both ways) that may run side by side;
+// either may be null.  join: null, or sums of a launch_backward, in `sums`, that are joined too.
 uint64_t products_workspace(const Product* x, const Product* w);
 hipError_t launch_products(const Product* x, const Product* w, const Backward* join, const void* sums, void* workspace,
                            hipStream_t stream);

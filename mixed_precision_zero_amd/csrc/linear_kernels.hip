@@ -317,6 +317,7 @@ namespace {
 // The products of one call, with their packed operands and shares in the workspace.
 struct Placed {
     const Product* p = nullptr;
+    Operand q{};               // where tiles load it from
     ProductPlan c{};
     TileArgs a{};
     Result r{};
@@ -335,10 +336,14 @@ struct Work {
             Placed& t = at[i];
             const Product& p = *t.p;
             t.c = product_plan(p.I, p.J, p.K);
-            const Operand P = operand(p.p, p.I, p.K, base), Q = operand(p.q, p.J, p.K, base);
+            const Operand P = operand(p.p, p.I, p.K, base);
+            // d is an operand of both gradients' products and is copied once: its rows are the same,
+            // whichever way it is read.  (By its role, not by its address: what a workspace needs does
+            // not depend on where the operands lie.)
+            t.q = i == 0 ? operand(p.q, p.J, p.K, base) : at[0].q;
             t.r = Result{p.out, p.out_ld, p.I, p.J, p.out_dtype, (uint64_t)p.I * p.J * (p.out_dtype == NEOX_F32 ? 4 : 2) >= kBeyond,
                          p.epi};
-            t.a = TileArgs{(const uint8_t*)P.at, (const uint8_t*)Q.at, (uint32_t)(P.ld * 2), (uint32_t)(Q.ld * 2), p.K, t.c.slabs,
+            t.a = TileArgs{(const uint8_t*)P.at, (const uint8_t*)t.q.at, (uint32_t)(P.ld * 2), (uint32_t)(t.q.ld * 2), p.K, t.c.slabs,
                            t.c.shares, t.r};
             if (t.c.shares > 1) {
                 t.part = (const float*)(base + bytes);
@@ -347,17 +352,10 @@ struct Work {
             }
         }
     }
-    // The operand itself where tiles can be loaded from it, or its copy.  (d is an operand of both
-    // products, and is copied once: its rows are the same, whichever way it is read.)
+    // The operand itself where tiles can be loaded from it, or its copy.
     Operand operand(Operand o, uint64_t side, uint64_t K, uint8_t* base) {
         if (direct(o, side, K)) return o;
         const uint64_t rows = o.strided ? K : side, cols = o.strided ? side : K, pitch = packed_pitch(o, side, K);
-        for (int i = 0; i < npacks; ++i)
-            if (packs[i].src == o.at && packs[i].ld == o.ld && packs[i].rows == rows && packs[i].cols == cols) {
-                o.at = packs[i].dst;
-                o.ld = pitch;
-                return o;
-            }
         packs[npacks++] = Pack{o.at, (uint16_t*)(base + bytes), o.ld, rows, (uint32_t)cols, (uint32_t)pitch,
                                (uint32_t)std::min<uint64_t>((rows * pitch / 8 + 255) / 256, 1u << 13)};
         o.at = (const uint16_t*)(base + bytes);
