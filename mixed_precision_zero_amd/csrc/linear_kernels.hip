@@ -329,7 +329,8 @@ struct Work {
     int n = 0, npacks = 0;
     uint64_t bytes = 0;
 
-    Work(const Product* x, const Product* w, uint8_t* base) {
+    // base: the workspace's address, 0 where only its size is asked for
+    Work(const Product* x, const Product* w, uintptr_t base) {
         for (const Product* p : {x, w})
             if (p) at[n++].p = p;
         for (int i = 0; i < n; ++i) {
@@ -347,13 +348,13 @@ struct Work {
                            t.c.shares, t.r};
             if (t.c.shares > 1) {
                 t.part = (const float*)(base + bytes);
-                t.a.r = Result{base + bytes, part_ld(p.I), p.I, p.J, NEOX_F32, false, Epilogue{}};
+                t.a.r = Result{(void*)(base + bytes), part_ld(p.I), p.I, p.J, NEOX_F32, false, Epilogue{}};
                 bytes += (t.c.shares * (uint64_t)p.J * part_ld(p.I) * 4 + 255) / 256 * 256;
             }
         }
     }
     // The operand itself where tiles can be loaded from it, or its copy.
-    Operand operand(Operand o, uint64_t side, uint64_t K, uint8_t* base) {
+    Operand operand(Operand o, uint64_t side, uint64_t K, uintptr_t base) {
         if (direct(o, side, K)) return o;
         const uint64_t rows = o.strided ? K : side, cols = o.strided ? side : K, pitch = packed_pitch(o, side, K);
         packs[npacks++] = Pack{o.at, (uint16_t*)(base + bytes), o.ld, rows, (uint32_t)cols, (uint32_t)pitch,
@@ -411,11 +412,11 @@ hipError_t launch_work(const Work& w, const Backward* join, const void* sums, hi
 
 }  // namespace
 
-uint64_t products_workspace(const Product* x, const Product* w) { return Work(x, w, nullptr).bytes; }
+uint64_t products_workspace(const Product* x, const Product* w) { return Work(x, w, 0).bytes; }
 
 hipError_t launch_products(const Product* x, const Product* w, const Backward* join, const void* sums, void* workspace,
                            hipStream_t stream) {
-    const Work work(x, w, (uint8_t*)workspace);
+    const Work work(x, w, (uintptr_t)workspace);
     return (x ? x : w)->dtype == NEOX_F16 ? launch_work<NEOX_F16>(work, join, sums, stream)
                                           : launch_work<NEOX_BF16>(work, join, sums, stream);
 }
