@@ -155,7 +155,7 @@ int neox_dropout(const void* x, uint64_t x_ld, const void* bias, const void* res
 
 /* Its gradients: dx = D(dy), and dbias = the sum over its rows, in FP32, of what D gives before
  * rounding (accumulate: added to dbias, rounded once).  Either may be NULL, not both; dx may be
- * dy.  Only dbias needs a workspace.  Errors: as neox_dropout, and NEOX_EINVAL for
+ * dy.  rows = 0: dbias is zeros, or with accumulate as it was.  Only dbias needs a workspace.  Errors: as neox_dropout, and NEOX_EINVAL for
  * accumulate not 0 or 1, or a workspace too small, not 256-byte aligned or meeting an array. */
 int neox_dropout_backward_workspace(uint64_t rows, uint64_t cols, uint64_t* bytes);
 int neox_dropout_backward(const void* dy, uint64_t dy_ld, void* dx, uint64_t dx_ld, void* dbias,

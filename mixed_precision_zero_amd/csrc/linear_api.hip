@@ -221,10 +221,12 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
     if (b.drop.counter) arr.reads("the counter", b.drop.counter, 1, 1, 1, 8);
     if (arr.check()) return arr.rc;
 
+    // (nothing is added to what is there: even a zero sum would turn a -0 into 0)
+    const bool sums = m || !a->accumulate;
     g.has_dx = a->dx && m;
-    g.has_dw = a->dw != nullptr;
+    g.has_dw = a->dw && sums;
     const bool made = (act || b.drop.limit) && (g.has_dx || g.has_dw) && m;
-    g.pass = made || a->dbias;
+    g.pass = made || (a->dbias && sums);
     // rows of d are whole lines of 128 bytes
     const uint64_t d_ld = round_up(n, 64);
     g.d_bytes = made ? round_up(m * d_ld * 2, 256) : 0;
@@ -419,7 +421,7 @@ extern "C" int neox_dropout_backward(const void* dy, uint64_t dy_ld, void* dx, u
     rc = arr.check();
     if (!rc) rc = arr.check_workspace(workspace, workspace_bytes, dbias ? backward_workspace(rows, cols) : 0);
     if (rc) return rc;
-    if (rows == 0 && !dbias) return NEOX_OK;
+    if (rows == 0 && (!dbias || accumulate)) return NEOX_OK;        // as in take_gradients
     b.dy = dy;
     b.d = rows ? dx : nullptr;
     b.dbias = dbias;

@@ -54,3 +54,16 @@ def test_a_workspace_serves_other_addresses():
     with pytest.raises(Z.NeoxError) as e:
         L.neox_linear_backward(a, WORK, need - 1)
     assert e.value.code == Z.NEOX_EINVAL and f"{need} needed" in str(e.value)
+
+
+def test_no_tokens_leave_accumulated_gradients_alone():
+    """Nothing is added to them, so nothing is launched (there may be no device)."""
+    for act, dbias, parts in itertools.product((0, 2), (False, True), ("xw", "w", "")):
+        if not dbias and not parts:
+            continue
+        a = gradients((DY, X, W), 0, 40, 50, 64, Z.NEOX_F16, act, dbias, parts)
+        a.accumulate = 1
+        assert L.neox_linear_backward_workspace(a) == 0
+        L.neox_linear_backward(a, 0, 0)
+    for dtype in (Z.NEOX_F16, Z.NEOX_BF16, L.NEOX_F32):
+        L.neox_dropout_backward(None, 0, None, 0, DB, 1, 0, 40, dtype, None)
