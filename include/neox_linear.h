@@ -105,10 +105,11 @@ int neox_linear_workspace(const neox_linear_args* a, uint64_t* bytes);
  * 256-byte aligned), NEOX_EHIP. */
 int neox_linear(const neox_linear_args* a, void* workspace, uint64_t workspace_bytes, void* hip_stream);
 
-/* The gradients of the same, from dy (m x n): with d = D(dy) act'(pre), rounded to half where
- * there is dropout or an act,
- *     dx = d W,    dw = d^T x,    dbias = sum over the rows of d (before its rounding)
- * (the residual's gradient is dy itself).  accumulate: dw and dbias are added to in FP32 and
+/* The gradients of the same, from dy (m x n): with d = M(dy) act'(pre), M dropout's mask without
+ * its factor f = 65536 / (65536 - T) (1 without dropout, 0 for T = 65536),
+ *     dx = f d W,    dw = f d^T x,    dbias = f times the sum over the rows of d
+ * (the residual's gradient is dy itself).  With an act, d is rounded to half for dx and dw (not
+ * for dbias), as an operand of their products; f is applied to the sums, in FP32.  accumulate: dw and dbias are added to in FP32 and
  * rounded once; dx is always overwritten.  act' is 0 at -inf, and of RELU 0 at 0.
  * All of half; dx m x k, dw n x k, dbias n; each may be NULL, not all.  x is needed for dw, W
  * for dx, pre for an act.  m = 0: dw and dbias are zeros, or with accumulate as they were.

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256) void backward_kernel(BackArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     d[k][e] = opaque(d[k][e]);
-                    s[e] += d[k][e];
+                    s[e] = __builtin_fmaf(d[k][e], b.scale, s[e]);
                 }
                 if (b.d) store8<DT, NT>(b.d, row * b.d_ld + c, b.padded ? 8 : n, d[k]);
             }

@@ -228,6 +228,7 @@ struct Result {
     uint32_t I, J;             // columns, rows
     int32_t dtype;             // of out
     bool beyond;               // out is larger than the caches
+    float scale;               // of the sums; looked at where there is nothing but a residual
     Epilogue e;                // (of nothing: all zero)
 };
 constexpr uint64_t kBeyond = 1ull << 28;
@@ -237,7 +238,7 @@ constexpr uint64_t kBeyond = 1ull << 28;
 // and 2044 -> 1925 us there, but 20.0 -> 24.3 and 23.6 -> 29.4 at 2048 x 4096 x 1024.
 // Takes the sums of elements (row, col) to (row, col + 7), col a multiple of 8, to memory; bias and
 // residual: what lies there (looked at where there are such).  LAYER: whether there may be anything
-// but a residual.
+// but a residual; if not, the sums are those of a gradient, times r.scale.
 template <int DT, int HT, bool LAYER>
 __device__ __forceinline__ void emit8(const Result& r, uint64_t off, uint32_t row, uint32_t col, float (&v)[8],
                                       const Raw8<HT>& bias, const Raw8<DT>& residual) {
@@ -260,7 +261,10 @@ __device__ __forceinline__ void emit8(const Result& r, uint64_t off, uint32_t ro
     }
     if (r.e.residual) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += element(residual, e);
+        for (int e = 0; e < 8; ++e) v[e] = LAYER ? v[e] + element(residual, e) : __builtin_fmaf(v[e], r.scale, element(residual, e));
+    } else if constexpr (!LAYER) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= r.scale;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = opaque(v[e]);

@@ -181,6 +181,7 @@ int take_linear(const neox_linear_args* a, Arrays& arr, Product& p) {
     p.out_dtype = a->y_dtype;
     p.out = a->y;
     p.out_ld = a->y_ld;
+    p.scale = 1.0f;
     return NEOX_OK;
 }
 
@@ -242,6 +243,10 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
     b.act = a->act;
     b.accumulate = a->accumulate != 0;
     b.padded = made;
+    // (p = 1: nothing is kept, the factor is zero)
+    const float scale = b.drop.limit ? b.drop.scale : 1.0f;
+    b.scale = scale;
+    b.drop.scale = 1.0f;
 
     auto product = [&](Operand p, Operand q, uint64_t I, uint64_t J, uint64_t K, void* out, uint64_t out_ld) {
         Product r{};
@@ -253,6 +258,7 @@ int take_gradients(const neox_linear_grads* a, Arrays& arr, Gradients& g) {
         r.dtype = r.out_dtype = a->dtype;
         r.out = out;
         r.out_ld = out_ld;
+        r.scale = scale;
         return r;
     };
     // (d's place is filled in when the workspace is known; its alignment is the workspace's)
@@ -431,6 +437,7 @@ extern "C" int neox_dropout_backward(const void* dy, uint64_t dy_ld, void* dx, u
     b.cols = cols;
     b.dtype = dtype;
     b.accumulate = accumulate != 0;
+    b.scale = 1.0f;                                   // (dx itself is D(dy))
     const hipError_t e = launch_backward(b, workspace, true, static_cast<hipStream_t>(hip_stream));
     return e == hipSuccess ? NEOX_OK : set_hip_error(e, "dropout_backward launch");
 }

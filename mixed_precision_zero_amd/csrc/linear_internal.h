@@ -32,7 +32,7 @@ struct Operand {
     bool strided;
     bool padded;               // its rows may be read up to a multiple of 8 elements: zeros
 };
-// out[j][i] = sum over k of p(i, k) q(j, k): I columns, J rows.
+// out[j][i] = scale times the sum over k of p(i, k) q(j, k): I columns, J rows.
 struct Product {
     Operand p, q;
     uint32_t I, J;
@@ -41,6 +41,7 @@ struct Product {
     int32_t out_dtype;
     void* out;
     uint64_t out_ld;
+    float scale;               // 1 but for gradients behind dropout
     Epilogue epi;              // (of nothing: all zero)
 };
 // Which kernel a product takes, and into how many shares of how many slabs (64 elements) its sums
@@ -57,7 +58,9 @@ ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K);
 // Whether two products are worth one launch, and on which tiles.
 bool pair_plan(uint64_t Ix, uint64_t Jx, const ProductPlan& x, uint64_t Iw, uint64_t Jw, const ProductPlan& w,
                ProductKernel* kernel);
-// d = D(dy) act'(pre), and the sums of its columns.
+// d = D(dy) act'(pre), and the sums of its columns times `scale`.  A linear layer's d lacks dropout's
+// factor: drop.scale is 1 there, and `scale`, which its products take too, is the factor.  So d, which
+// is rounded to half, overflows only where dy act'(pre) does, and is not rounded at all without an act.
 struct Backward {
     const void* dy;
     const uint16_t* pre;       // null: no act
@@ -68,6 +71,7 @@ struct Backward {
     int32_t dtype, act;
     bool accumulate;
     bool padded;               // rows of d are filled with zeros up to a multiple of 8 elements
+    float scale;
     Drop drop;
 };
 // The sums of blocks that share the rows, [parts][cols] in FP32 in the workspace, are joined by

@@ -137,6 +137,8 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, uint64_t l
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = opaque(v[e] * r.scale);
     emit8_any<HT>(r, drop_offset(r.e.drop), (uint32_t)u.row, c, v);
 }
 
@@ -343,12 +345,12 @@ struct Work {
             // not depend on where the operands lie.)
             t.q = i == 0 ? operand(p.q, p.J, p.K, base) : at[0].q;
             t.r = Result{p.out, p.out_ld, p.I, p.J, p.out_dtype, (uint64_t)p.I * p.J * (p.out_dtype == NEOX_F32 ? 4 : 2) >= kBeyond,
-                         p.epi};
+                         p.scale, p.epi};
             t.a = TileArgs{(const uint8_t*)P.at, (const uint8_t*)t.q.at, (uint32_t)(P.ld * 2), (uint32_t)(t.q.ld * 2), p.K, t.c.slabs,
                            t.c.shares, t.r};
             if (t.c.shares > 1) {
                 t.part = (const float*)(base + bytes);
-                t.a.r = Result{(void*)(base + bytes), part_ld(p.I), p.I, p.J, NEOX_F32, false, Epilogue{}};
+                t.a.r = Result{(void*)(base + bytes), part_ld(p.I), p.I, p.J, NEOX_F32, false, 1.0f, Epilogue{}};
                 bytes += (t.c.shares * (uint64_t)p.J * part_ld(p.I) * 4 + 255) / 256 * 256;
             }
         }

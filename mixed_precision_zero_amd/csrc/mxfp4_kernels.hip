@@ -517,7 +517,7 @@ hipError_t launch_mx_linear(const void* a_codes, const void* a_scales, uint64_t 
     auto run = [&](auto ht) {
         LinearArgs<decltype(ht)::value> a{};
         static_cast<ProductArgs&>(a) = product_args(a_codes, a_scales, m, b_codes, b_scales, n, k, c, dtype, ldc);
-        a.r = Result{c, ldc, (uint32_t)n, (uint32_t)m, dtype, m * n * (dtype == NEOX_F32 ? 4 : 2) >= kBeyond, epi};
+        a.r = Result{c, ldc, (uint32_t)n, (uint32_t)m, dtype, m * n * (dtype == NEOX_F32 ? 4 : 2) >= kBeyond, 1.0f, epi};
         return launch_mx(a, stream);
     };
     return half == NEOX_F16 ? run(std::integral_constant<int, NEOX_F16>{}) : run(std::integral_constant<int, NEOX_BF16>{});

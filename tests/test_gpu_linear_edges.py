@@ -1,11 +1,12 @@
 """The linear layer's operators on the GPU where calls are unusual: operands that are one array,
-no tokens."""
+no tokens, gradients at the top of their type's range behind dropout."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
+import linear_reference as R  # noqa: E402
 from mixed_precision_zero_amd import linear as L  # noqa: E402
-from test_gpu_linear import HALVES, inside, ints, same_bits  # noqa: E402
+from test_gpu_linear import HALVES, drops, inside, ints, rand, same_bits  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,48 @@ def test_no_tokens_leave_accumulated_gradients_as_they_were(half):
         assert same_bits(dw, was_w) and same_bits(db, was_b)
     L.dropout_backward(dy, L.Dropout(0.5, 1), dx=False, dbias=db, accumulate=True)
     assert same_bits(db, was_b)
+
+
+@pytest.mark.parametrize("act", R.ACTS)
+@pytest.mark.parametrize("p", [0.25, 0.5, 0.9])
+@pytest.mark.parametrize("m,n,k", [(5, 96, 40), (96, 72, 200), (300, 96, 264)])
+def test_dropout_does_not_overflow_gradients(m, n, k, p, act):
+    """dy of up to 60000 in FP16, which dropout's factor of 1.3 to 10 takes beyond the type's range:
+    dx, dw and dbias are finite, and so are the results (slopes are 1 where an act is)."""
+    half = torch.float16
+    dy = (rand((m, n), 1, torch.float32).sign() * 60000).to(half)
+    x, w = rand((m, k), 2, half, 2.0 ** -12), rand((n, k), 3, half, 2.0 ** -12)
+    pre = torch.full((m, n), 20.0, dtype=half, device="cuda:0")
+    drop, ref = drops(p)
+    got = dict(zip(("dx", "dw", "dbias"), L.linear_backward(dy, x, w, pre, act, drop, dbias=True)))
+    want = R.backward(dy, x, w, pre, act, ref)[2]
+    for name in ("dx", "dw"):
+        assert float(want[name][0].abs().max()) < 60000 and bool(torch.isfinite(got[name]).all()), name
+        R.close(got[name], *want[name], what=name)
+    R.close(got["dbias"], *want["dbias"], what="dbias")
+
+
+@HALVES
+@pytest.mark.parametrize("p", [0.25, 0.3, 0.9])
+@pytest.mark.parametrize("m,n,k", [(1, 50, 70), (37, 129, 260), (300, 264, 136), (333, 64, 4096), (64, 64, 16384)])
+def test_dropout_without_act_rounds_no_operand(m, n, k, p, half):
+    """Whole numbers, so that the sums of what is kept are exact: the results are those times
+    dropout's factor, off by FP32's roundings of the product and of what it is added to, and by their
+    own to half."""
+    dy, x, w = ints((m, n), 1, half), ints((m, k), 2, half), ints((n, k), 3, half)
+    old_w, old_b = ints((n, k), 4, half, 50), ints((n,), 5, half, 50)
+    drop, ref = drops(p)
+    scale, kept = R.keep(ref, m, n)
+    d = torch.where(kept, dy.double().cpu(), 0.0)
+    dx, dw, db = L.linear_backward(dy, x, w, dropout=drop, dbias=True)
+    sums = d @ w.double().cpu(), d.t() @ x.double().cpu(), d.sum(0)
+    assert all(float(v.abs().max()) < 2 ** 24 for v in sums)
+    for got, v, name in zip((dx, dw, db), sums, ("dx", "dw", "dbias")):
+        # (dbias adds up m products with the factor, each with a rounding)
+        err = R.U * scale * (v.abs() if name != "dbias" else (m + 1) * d.abs().sum(0))
+        R.close(got, v * scale, err, name)
+    L.linear_backward(dy, x, None, dropout=drop, dx=False, dw=old_w, dbias=old_b, accumulate=True)
+    total = sums[1] * scale + ints((n, k), 4, half, 50).double().cpu()
+    R.close(old_w, total, R.U * (scale * sums[1].abs() + total.abs()), "dw, added")
+    total = sums[2] * scale + ints((n,), 5, half, 50).double().cpu()
+    R.close(old_b, total, R.U * (scale * (m + 1) * d.abs().sum(0) + total.abs()), "dbias, added")
