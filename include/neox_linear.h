@@ -95,8 +95,8 @@ typedef struct neox_linear_args {
     neox_epilogue epi;
 } neox_linear_args;
 
-/* Bytes of workspace that this call needs (0 for many; the addresses' alignment matters, the
- * rest of what they point to does not).  Host only.  Errors: as neox_linear. */
+/* Bytes of workspace that this call needs (0 for many): by sizes, lds, types and the addresses'
+ * alignment; other addresses of the same alignment need as much.  Host only.  Errors: as neox_linear. */
 int neox_linear_workspace(const neox_linear_args* a, uint64_t* bytes);
 
 /* Errors: NEOX_EINVAL (null, misaligned, a size outside the limits, an ld smaller than the

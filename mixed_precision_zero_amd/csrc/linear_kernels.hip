@@ -1,13 +1,15 @@
 // linear_kernels.hip -- products of half-precision matrices with an epilogue on gfx950: a layer's
 // forward product (rows of K by rows of K), dx (W's rows are K) and dw (both operands' are).
 //
-// Large ones are bound by the matrix units and LDS together, as all of tile_core.h's: 8192 x 24576 x
-// 6144 forward 1850 to 1900 us without an epilogue (1.30 to 1.34 PFLOP/s, matrix units busy 66% of the
-// time), dx 1805 to 1850 (71%), dw 1790 to 1830 (73%); a library product of these 1690, 1810 and 2070.
+// Large ones are bound by the matrix units, which are busy most of the time at a clock that this load
+// lowers (see tile_core.h): 8192 x 24576 x 6144 forward 1850 to 1900 us without an epilogue (1.30 to
+// 1.34 PFLOP/s, matrix units busy 67% of the time), dx 1805 to 1850 (70%), dw 1790 to 1870 (73%); a
+// library product of these 1690, 1810 and 2070.
 // The forward product is slower than the other two where a row of K is a multiple of 4 KB: its loads
 // take 128 bytes of each of 512 rows, which then lie in the same channels of the L2; rows of K + 64
 // elements take 1780 us.  Few results over long sums are split into shares of K (see product_plan).
-// Few tokens are bound by reading W: one by 24576 x 6144 (302 MB) 52 us, 5.8 TB/s.
+// Few tokens are bound by reading W: one by 24576 x 6144 (302 MB) 50.8 us, 47 of them the product's
+// (6.4 TB/s), the rest the join of its shares.
 #include "column_sums.h"
 #include "epilogue.h"
 #include "spread.h"
@@ -273,7 +275,9 @@ double join_cost(uint64_t shares, uint64_t I, uint64_t J) {
 // and for shares (few results, long sums) a launch and the sums' way through memory, the caches
 // mostly.  Blocks beyond a round start as others end: a part of a round more.  No launch takes less
 // than its operands at 6.8 TB/s (products of 1 to 128 tokens with weights from memory, 30 of them: 3.3%
-// longer than the fastest on average).
+// longer than the fastest on average).  At most 16 shares: few results of the longest sums leave CUs
+// without a block (64 x 64 over K = 2^20: 16 blocks, 280 us by these costs where the bytes take 43), and
+// a share's FP32 sums are as long as a sixteenth of K.
 ProductPlan product_plan(uint64_t I, uint64_t J, uint64_t K) {
     const uint64_t slabs = std::max<uint64_t>(1, (K + 63) / 64), n64 = tiles(I, J, 64), n128 = tiles(I, J, 128);
     ProductPlan best{kTiles256, 1, slabs, 0.0};

@@ -17,9 +17,12 @@
 //
 // Measured, all tiles whole: FP16 8192 x 8192 x 4096 on 256 x 256 tiles 1.28 to 1.38 PFLOP/s
 // (a library product of 8192^3 reaches 1.43, products from registers alone 2.13), on 128 x 128
-// ones 1.1; MXFP4 8192 x 8192 x 16384 4.2 to 4.4 and 3.5.  The matrix units are busy 64% of the
-// time in FP16; LDS, from which each wave reads 8 + 4 fragments for 32 products and into which
-// the loads write, is busy nearly as long, and the two do not overlap in full.
+// ones 1.1; MXFP4 8192 x 8192 x 16384 4.2 to 4.4 and 3.5.  Counters of 16-bit products of 8192 x
+// 24576 x 6144 have the matrix units busy 67 to 73% of the cycles, at a clock of 1.67 to 1.88 GHz (of
+// 2.4: the card lowers it under this load, an element-wise pass runs at 2.2), LDS reads active 27 to 29%
+// with next to no conflicts (8 + 4 fragments of a wave for 32 products; the loads' writes into LDS,
+// a third of those bytes on top, are not counted), and waves waiting 27 to 29%.  Of MXFP4 products
+// (4000 x 24576 x 6144): matrix units 44%, LDS reads 49%, half of those cycles in bank conflicts.
 #pragma once
 
 #include "neox_matrix.h"

@@ -6,6 +6,8 @@ As in the package itself, the functions with C names take addresses and only mar
 arguments; below them are the conveniences that take torch tensors.  Those run on the
 current stream of their tensors' device, take their workspace from torch's allocator on
 that stream, and reject what the operators do not cover; nothing falls back to torch.
+They are no part of torch's autograd: results carry no graph, even of inputs that require
+gradients; those are for the backward functions to make.
 """
 from __future__ import annotations
 
@@ -310,7 +312,7 @@ def linear_backward(dy, x=None, w=None, pre=None, act: str = "none", dropout: Dr
 def mxfp4_linear(x, w: MXFP4, bias=None, act: str = "none", dropout: Dropout | None = None,
                  residual=None, dtype=None, out=None, pre=False, half=None):
     """linear on the MXFP4 copy w of an n x k weight, by the MXFP4 copy of x: x is one, or a
-    matrix of which one is made.  half: the type of bias and pre (x's where x is a float16 or
+    matrix (of one row or more) of which one is made.  half: the type of bias and pre (x's where x is a float16 or
     bfloat16 matrix, else bfloat16).  dtype: the result's, `half` by default, float16, bfloat16
     or float32; of the half types only `half`."""
     import torch
