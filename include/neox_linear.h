@@ -96,7 +96,8 @@ typedef struct neox_linear_args {
 } neox_linear_args;
 
 /* Bytes of workspace that this call needs (0 for many): by sizes, lds, types and the addresses'
- * alignment; other addresses of the same alignment need as much.  Host only.  Errors: as neox_linear. */
+ * alignment; other addresses of the same alignment need as much.  Host only.  Errors: as
+ * neox_linear. */
 int neox_linear_workspace(const neox_linear_args* a, uint64_t* bytes);
 
 /* Errors: NEOX_EINVAL (null, misaligned, a size outside the limits, an ld smaller than the
@@ -109,8 +110,9 @@ int neox_linear(const neox_linear_args* a, void* workspace, uint64_t workspace_b
  * its factor f = 65536 / (65536 - T) (1 without dropout, 0 for T = 65536),
  *     dx = f d W,    dw = f d^T x,    dbias = f times the sum over the rows of d
  * (the residual's gradient is dy itself).  With an act, d is rounded to half for dx and dw (not
- * for dbias), as an operand of their products; f is applied to the sums, in FP32.  accumulate: dw and dbias are added to in FP32 and
- * rounded once; dx is always overwritten.  act' is 0 at -inf, and of RELU 0 at 0.
+ * for dbias), as an operand of their products; f is applied to the sums, in FP32.  accumulate:
+ * dw and dbias are added to in FP32 and rounded once; dx is always overwritten.  act' is 0 at
+ * -inf, and of RELU 0 at 0.
  * All of half; dx m x k, dw n x k, dbias n; each may be NULL, not all.  x is needed for dw, W
  * for dx, pre for an act.  m = 0: dw and dbias are zeros, or with accumulate as they were.
  * Sizes, alignment and overlap as above; the outputs are apart from everything else. */
@@ -156,8 +158,9 @@ int neox_dropout(const void* x, uint64_t x_ld, const void* bias, const void* res
 
 /* Its gradients: dx = D(dy), and dbias = the sum over its rows, in FP32, of what D gives before
  * rounding (accumulate: added to dbias, rounded once).  Either may be NULL, not both; dx may be
- * dy.  rows = 0: dbias is zeros, or with accumulate as it was.  Only dbias needs a workspace.  Errors: as neox_dropout, and NEOX_EINVAL for
- * accumulate not 0 or 1, or a workspace too small, not 256-byte aligned or meeting an array. */
+ * dy.  rows = 0: dbias is zeros, or with accumulate as it was.  Only dbias needs a workspace.
+ * Errors: as neox_dropout, and NEOX_EINVAL for accumulate not 0 or 1, or a workspace too small,
+ * not 256-byte aligned or meeting an array. */
 int neox_dropout_backward_workspace(uint64_t rows, uint64_t cols, uint64_t* bytes);
 int neox_dropout_backward(const void* dy, uint64_t dy_ld, void* dx, uint64_t dx_ld, void* dbias,
                           int32_t accumulate, uint64_t rows, uint64_t cols, int32_t dtype, const neox_drop* drop,

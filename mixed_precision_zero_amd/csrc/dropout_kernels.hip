@@ -92,9 +92,10 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, Spread sp, 
 // column, then over the blocks by join_kernel.  The sums' order goes by the sizes alone.
 //
 // Memory-bound without an act: BF16 16384 x 6144 73 us, 5.5 TB/s, and 4.5 of the join (64 without
-// sums, by dropout_kernel).  Blocks that take runs of rows instead 97 (their rows lie far apart), 512 of them
-// 119, 1024 80, two rows in flight 81.  With an act and dropout bound by their arithmetic, some 60
-// instructions an element: 8192 x 24576 GELU 205 us to read 805 MB, 160 without dropout.
+// sums, by dropout_kernel).  With the join, blocks that take runs of rows instead 97 (their rows lie
+// far apart), 512 of them 119, 1024 80, two rows in flight 81.  With an act and dropout bound by
+// their arithmetic, some 60 instructions an element: 8192 x 24576 GELU 205 us to read 805 MB, 160
+// without dropout.
 struct BackArgs {
     Backward b;
     float* part;               // [count][cols], or null: no sums, or one block that writes dbias

@@ -62,7 +62,7 @@ constexpr uint64_t kGrid = 1ull << 23;
 // Launches f(first row, rows, their spread) for as many rows at a time as a grid takes.
 template <class F>
 void rows_in_grids(uint64_t rows, uint64_t units, uint32_t deep, F f) {
-    const Spread one = spread(1, units, deep);             // (at most 2^20 blocks across)
+    const Spread one = spread(1, units, deep);          // (at most 2^20 blocks across)
     const uint64_t most = kGrid / one.across * ((256u >> one.shift) * deep);
     for (uint64_t r = 0; r < rows; r += most) {
         const uint64_t n = std::min(most, rows - r);

@@ -312,9 +312,9 @@ def linear_backward(dy, x=None, w=None, pre=None, act: str = "none", dropout: Dr
 def mxfp4_linear(x, w: MXFP4, bias=None, act: str = "none", dropout: Dropout | None = None,
                  residual=None, dtype=None, out=None, pre=False, half=None):
     """linear on the MXFP4 copy w of an n x k weight, by the MXFP4 copy of x: x is one, or a
-    matrix (of one row or more) of which one is made.  half: the type of bias and pre (x's where x is a float16 or
-    bfloat16 matrix, else bfloat16).  dtype: the result's, `half` by default, float16, bfloat16
-    or float32; of the half types only `half`."""
+    matrix (of one row or more) of which one is made.  half: the type of bias and pre (x's where
+    x is a float16 or bfloat16 matrix, else bfloat16).  dtype: the result's, `half` by default,
+    float16, bfloat16 or float32; of the half types only `half`."""
     import torch
     if not isinstance(x, MXFP4):
         if half is None and x.dtype != torch.float32:
